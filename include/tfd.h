@@ -5,7 +5,8 @@
  * server: a few-row (1..16 token rows) vocabulary-head GEMV in bf16 or FP8 fused with a
  * split-vocabulary top-1 / top-k, the two-stage head (low-rank top-cand_k then exact rescore), the
  * qk_norm + RoPE ring-window attention, the accept-prefix count, and the FP8 quantisation of the
- * weights these calls read.
+ * weights these calls read; and, for requests that sample, drawing tokens from logits and the
+ * rejection accept of such drafts.
  *
  * Conventions shared by every call:
  *  - Pointers named as device buffers are caller-owned device memory on the current CUDA device.
@@ -84,6 +85,7 @@ typedef enum { TFD_OUT_NONE = 0, TFD_OUT_F32 = 1, TFD_OUT_BF16 = 2, TFD_OUT_ADD_
 #define TFD_MAX_ROWS 32
 #define TFD_MAX_TOPK 512    /* [TFE] commit "... ocabulary head": cand_k from 1 to 512 */
 #define TFD_MAX_WINDOW 511  /* [TFE] commit "... ocabulary head": window up to 511 (512 keys) */
+#define TFD_MAX_DRAW_COLS 1048576 /* columns of a row that a token is drawn from (exact sums) */
 
 /* A static string naming a status. Never NULL. */
 const char* tfd_status_string(int status);
@@ -320,6 +322,75 @@ tfd_status tfd_absorb(const void* k_rows, const void* v_rows, const void* k_gamm
                       float rope_base, const int32_t* p0, int n, void* k_ring, void* v_ring,
                       int ring, int streams, int heads, int dim, int32_t* dev_status,
                       void* stream);
+
+/*
+ * tfd_sample - draw one token a row from its logits, given a random number u in [0, 1).
+ *   For a row with logits l and w_i = exp((l_i - max l) / temperature):
+ *     1. top_k keeps the top_k largest logits (<= 0 or >= n: all), ties to the lower (mapped) id;
+ *     2. top_p keeps, in that order, every column before which the mass of the kept ones is below
+ *        top_p times their total; the first always stays (>= 1: all; <= 0: the first alone);
+ *     3. min_p keeps columns with w_i >= min_p (<= 0: all; >= 1: those equal to the largest).
+ *   The token is the first column, in column order, at which the running mass of the kept columns
+ *   exceeds u times their total. temperature 0 takes the largest logit (ties to the lower id).
+ *   NaN and -inf logits, and weights below 2^-44 of the largest, have no mass; where logits are
+ *   +inf, those share the mass. A row without any mass gets id -1 and probability 0.
+ *   Masses are summed as integers (multiples of 2^-43 of the largest weight), so a row's token
+ *   does not depend on the other rows, the launch or the order of the sums. The pages take the
+ *   round's draws as inputs; this call makes them, and has no counterpart there.
+ * Args:
+ *   logits   device bf16 or float (lfmt TFD_X_BF16, TFD_X_F32) [rows][ld], ld >= n; any
+ *            element-aligned base and stride; rows >= 1, 1 <= n <= TFD_MAX_DRAW_COLS.
+ *   temperature, top_p, min_p device float [rows], top_k device int32 [rows]; each may be NULL
+ *            (1, 1, 0 and 0). u device float [rows].
+ *   id_map   device int32 [n] or NULL: the id reported (and compared on ties) for column i.
+ *   ids      device int32, row r at ids[r * ldt] (ldt 0 = 1), so that the tokens of one step can
+ *            land in a column of a [streams][steps] array; prob device float or NULL, the same
+ *            stride: the token's probability in the filtered distribution.
+ *   probs    device float [rows][ldp] or NULL, ldp >= n, not overlapping the logits: the filtered,
+ *            normalised distribution by column (written in full, zeros where nothing is kept).
+ *   A negative, infinite or NaN temperature, a NaN top_p or min_p, or a u outside [0, 1) sets
+ *   TFD_ERR_DEVICE_DATA; that row gets id -1, probability 0 and a distribution of zeros.
+ */
+tfd_status tfd_sample(const void* logits, int lfmt, int rows, int64_t n, int64_t ld,
+                      const float* temperature, const int32_t* top_k, const float* top_p,
+                      const float* min_p, const float* u, const int32_t* id_map, int32_t* ids,
+                      float* prob, int64_t ldt, float* probs, int64_t ldp, int32_t* dev_status,
+                      void* stream);
+
+/*
+ * tfd_accept_sampled - the rejection accept of drafts that were drawn from q, and the next token.
+ *   Beside tfd_accept, which keeps drafts equal to the round's draws: here draft t of stream s is
+ *   kept when all before it are, t < n_asked[s] and u[s][t] * q[s][t](d) < p[s][t](d) (decided
+ *   without rounding). With m drafts kept, the next token is drawn with u_next[s] from
+ *   max(p[s][m] - q[s][m], 0) when a draft was turned down (from p[s][m] where that is zero
+ *   everywhere), else from p[s][m], m = n_asked[s]; "drawn" as in tfd_sample: the first column at
+ *   which the running mass exceeds u_next times the total. Kept drafts and next token are then
+ *   distributed as if drawn from p. Probabilities are clamped to 0..1, NaN to 0, and summed as
+ *   integer multiples of 2^-43; one-hot rows (temperature 0) make this the greedy accept. A
+ *   stream whose p row has no mass gets next token -1 and probability 0.
+ * Args:
+ *   p        device float [streams][win + 1][ldp], ldp >= n: the target's distributions at the
+ *            win drafts' positions and the one after; only rows 0..n_asked[s] are read.
+ *   q        device float [streams][win][ldq], ldq >= nq: the distributions the drafts were drawn
+ *            from. nq == n when q_map is NULL.
+ *   q_map    device int32 [n] or NULL: the column of q of token i, or -1 where the draft head
+ *            does not have it (q = 0): the inverse of a subset head's id map.
+ *   drafts   device int32 [streams][win], token ids in [0, n); n_asked device int32 [streams];
+ *   u        device float [streams][win]; u_next device float [streams]; all in [0, 1).
+ *   n_kept, next_ids device int32 [streams]; next_prob device float [streams] or NULL: the next
+ *            token's probability in the distribution it was drawn from.
+ *   asked_hist, kept_hist device int64 [win] or NULL (both or neither), accumulated as in
+ *            tfd_accept. streams >= 1; win 1..512; n, nq <= TFD_MAX_DRAW_COLS. p and q at
+ *            any element-aligned base and row stride.
+ *   An n_asked outside [0, win], an asked draft outside [0, n), or a u outside [0, 1) sets
+ *   TFD_ERR_DEVICE_DATA; that stream keeps 0, gets next token -1 and adds nothing.
+ */
+tfd_status tfd_accept_sampled(const float* p, int64_t ldp, const float* q, int64_t ldq, int64_t n,
+                              int64_t nq, const int32_t* q_map, const int32_t* drafts,
+                              const int32_t* n_asked, const float* u, const float* u_next,
+                              int streams, int win, int32_t* n_kept, int32_t* next_ids,
+                              float* next_prob, int64_t* asked_hist, int64_t* kept_hist,
+                              int32_t* dev_status, void* stream);
 
 #ifdef __cplusplus
 }

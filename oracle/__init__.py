@@ -16,6 +16,7 @@ Modules (each function cites the passage it follows):
 * ``two_stage`` - low-rank top-cand_k, exact rescore, argmax.
 * ``attn``      - qk_norm + RoPE + ring-window attention for one decode position.
 * ``accept``    - accept-prefix count with per-position asked/kept histograms.
+* ``sample``    - tokens drawn from filtered logits, and the rejection accept of such drafts.
 * ``draft_pass``- the chained multi-step draft pass (composition of the above).
 
 Every function here is pinned by ``tests/test_oracle_*.py`` against closed forms, brute force,

@@ -1,0 +1,302 @@
+// accept_sampled.cu - the rejection accept of sampled drafts, and the round's next token.
+//
+// Draft t of a stream is kept when all before it are and u_t q_t(d_t) < p_t(d_t): the product of two
+// fp32 numbers is exact in 53 bits, so this decision has no rounding. The next token is drawn from
+// max(p_m - q_m, 0) at the first draft turned down (from p_m where that is zero everywhere), or from
+// p_m behind the last asked draft; kept drafts and next token are then distributed as if drawn from
+// p one by one.
+//
+// The draw sums integers: each probability as a multiple of 2^-43 (weight.cuh gives the reasons),
+// clamped to 0..1 with NaN as 0, so sums do not depend on the order and equal p and q leave exactly
+// zero. One thread-block cluster takes a stream, every block decides its drafts for itself, each
+// warp sums a contiguous part of the columns, and after one cluster barrier the block that holds
+// the drawn column scans the part of one warp.
+#include <cooperative_groups.h>
+
+#include "weight.cuh"
+
+namespace {
+
+using namespace tfd;
+namespace cg = cooperative_groups;
+
+constexpr int kT = 512;
+constexpr int kW = kT / 32;
+constexpr int kMaxC = 16;
+constexpr int kCols = 4;  // columns a lane takes at once
+
+struct Args {
+  const float* p;
+  int64_t ldp;
+  const float* q;
+  int64_t ldq;
+  int64_t n, nq;
+  const int32_t* q_map;
+  const int32_t* drafts;
+  const int32_t* n_asked;
+  const float* u;
+  const float* u_next;
+  int win;
+  int32_t* n_kept;
+  int32_t* next_ids;
+  float* next_prob;
+  unsigned long long* asked_hist;
+  unsigned long long* kept_hist;
+  int32_t* dev_status;
+};
+
+// A probability as an integer multiple of 2^-43: 21 bits, then 22.
+__device__ __forceinline__ uint64_t prob_fix(float x) {
+  x = fminf(fmaxf(x, 0.0f), 1.0f);  // NaN -> 0
+  const float y = x * 2097152.0f;
+  const uint32_t hi = __float2uint_rz(y);
+  const uint32_t lo = __float2uint_rn((y - (float)hi) * 4194304.0f);
+  return ((uint64_t)hi << 22) + lo;
+}
+
+__device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, (unsigned long long)v, m);
+  return v;
+}
+
+struct Shared {
+  uint64_t cres[kMaxC], cp[kMaxC];  // every block's residual mass and p mass
+  uint64_t wres[kW], wp[kW];        // this block's warps
+  int fail, bad;
+};
+
+__global__ void __launch_bounds__(kT) accept_sampled_kernel(const Args a) {
+  __shared__ Shared sh;
+  cg::cluster_group cl = cg::this_cluster();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  const int s = blockIdx.x / C;
+  const int na = a.n_asked[s];
+  const bool counted = na >= 0 && na <= a.win;
+  if (tid == 0) {
+    sh.fail = counted ? na : 0;
+    sh.bad = counted ? 0 : 1;
+  }
+  __syncthreads();
+  const float* prow = a.p + (int64_t)s * (a.win + 1) * a.ldp;
+  const float* qrow = a.q + (int64_t)s * a.win * a.ldq;
+  const float un = a.u_next[s];
+  if (counted) {
+    for (int t = tid; t < na; t += kT) {
+      const int d = a.drafts[(int64_t)s * a.win + t];
+      const float ut = a.u[(int64_t)s * a.win + t];
+      int dq = d;
+      if (d < 0 || d >= a.n || !(ut >= 0.0f && ut < 1.0f)) {
+        sh.bad = 1;
+      } else {
+        if (a.q_map) dq = a.q_map[d];
+        const float qd = dq >= 0 && dq < a.nq ? qrow[(int64_t)t * a.ldq + dq] : 0.0f;
+        const float pd = prow[(int64_t)t * a.ldp + d];
+        if (!((double)ut * (double)qd < (double)pd)) atomicMin(&sh.fail, t);
+      }
+    }
+  }
+  if (tid == 0 && !(un >= 0.0f && un < 1.0f)) sh.bad = 1;
+  __syncthreads();
+  if (sh.bad) {  // the whole cluster sees the same
+    if (rank == 0 && tid == 0) {
+      a.n_kept[s] = 0;
+      a.next_ids[s] = -1;
+      if (a.next_prob) a.next_prob[s] = 0.0f;
+      set_dev_status(a.dev_status, TFD_ERR_DEVICE_DATA);
+    }
+    return;
+  }
+  const int m = sh.fail;
+  if (rank == 0) {
+    if (tid == 0) a.n_kept[s] = m;
+    if (a.asked_hist) {
+      for (int i = tid; i < na; i += kT) atomicAdd(a.asked_hist + i, 1ull);
+      for (int i = tid; i < m; i += kT) atomicAdd(a.kept_hist + i, 1ull);
+    }
+  }
+  const bool rejected = m < na;
+  prow += (int64_t)m * a.ldp;
+  qrow += (int64_t)(rejected ? m : 0) * a.ldq;
+
+  // columns in chunks of 128 a warp; each warp a contiguous range of chunks
+  const int n = (int)a.n;
+  const int off = (int)((uintptr_t)prow & 15) / 4;
+  const int chunks = (off + n + 32 * kCols - 1) / (32 * kCols);
+  const int per_c = (chunks + C - 1) / C, per_w = (per_c + kW - 1) / kW;
+  const int cbeg = rank * per_c + warp * per_w;
+  const int cend = min(min(cbeg + per_w, (rank + 1) * per_c), chunks);
+  const bool qvec = rejected && !a.q_map && (((uintptr_t)(qrow - off)) & 15) == 0;
+
+  auto load = [&](int chunk, uint64_t (&r)[kCols], uint64_t (&p)[kCols]) {
+    const int c0 = chunk * 32 * kCols + lane * kCols - off;
+    float pv[kCols], qv[kCols] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (c0 >= 0 && c0 + kCols <= n) {
+      const float4 v = __ldg((const float4*)(prow + c0));
+      pv[0] = v.x, pv[1] = v.y, pv[2] = v.z, pv[3] = v.w;
+      if (qvec) {
+        const float4 w = __ldg((const float4*)(qrow + c0));
+        qv[0] = w.x, qv[1] = w.y, qv[2] = w.z, qv[3] = w.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) {
+        const int c = c0 + j;
+        const bool in = c >= 0 && c < n;
+        pv[j] = in ? prow[c] : 0.0f;
+        if (qvec && in) qv[j] = qrow[c];
+      }
+    }
+    if (rejected && !qvec) {
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) {
+        const int c = c0 + j;
+        if (c < 0 || c >= n) continue;
+        const int k = a.q_map ? a.q_map[c] : c;
+        if (k >= 0 && k < a.nq) qv[j] = qrow[k];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) {
+      p[j] = prob_fix(pv[j]);
+      const uint64_t q = prob_fix(qv[j]);
+      r[j] = p[j] > q ? p[j] - q : 0;
+    }
+  };
+
+  uint64_t rs = 0, ps = 0;
+#pragma unroll 4
+  for (int c = cbeg; c < cend; ++c) {
+    uint64_t r[kCols], p[kCols];
+    load(c, r, p);
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) {
+      rs += r[j];
+      ps += p[j];
+    }
+  }
+  rs = warp_sum64(rs);
+  ps = warp_sum64(ps);
+  if (lane == 0) {
+    sh.wres[warp] = rs;
+    sh.wp[warp] = ps;
+  }
+  cl.sync();  // every block runs, and this block's sums are written
+  if (tid < C) {
+    uint64_t x = 0, y = 0;
+    for (int w = 0; w < kW; ++w) {
+      x += sh.wres[w];
+      y += sh.wp[w];
+    }
+    *cl.map_shared_rank(&sh.cres[rank], tid) = x;
+    *cl.map_shared_rank(&sh.cp[rank], tid) = y;
+  }
+  cl.sync();
+  uint64_t res = 0, all = 0;
+  for (int c = 0; c < C; ++c) {
+    res += sh.cres[c];
+    all += sh.cp[c];
+  }
+  const bool from_p = res == 0;  // nothing is left of p above q
+  const uint64_t total = from_p ? all : res;
+  if (total == 0) {
+    if (rank == 0 && tid == 0) {
+      a.next_ids[s] = -1;
+      if (a.next_prob) a.next_prob[s] = 0.0f;
+    }
+    return;
+  }
+  const uint64_t target = mul_frac(un, total, false);
+  const uint64_t* blocks = from_p ? sh.cp : sh.cres;
+  const uint64_t* warps = from_p ? sh.wp : sh.wres;
+  uint64_t before = 0;
+  for (int c = 0; c < rank; ++c) before += blocks[c];
+  if (target < before || target >= before + blocks[rank]) return;
+  for (int w = 0; w < warp; ++w) before += warps[w];
+  if (target < before || target >= before + warps[warp]) return;
+  for (int c = cbeg; c < cend; ++c) {
+    uint64_t r[kCols], p[kCols];
+    load(c, r, p);
+    uint64_t sum = 0;
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) {
+      if (from_p) r[j] = p[j];
+      sum += r[j];
+    }
+    uint64_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t x = __shfl_up_sync(0xffffffffu, (unsigned long long)incl, o);
+      if (lane >= o) incl += x;
+    }
+    const uint64_t chunk = __shfl_sync(0xffffffffu, (unsigned long long)incl, 31);
+    if (before + chunk > target) {
+      uint64_t run = before + incl - sum;
+      if (run <= target && before + incl > target) {
+        bool done = false;
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) {
+          run += r[j];
+          if (!done && run > target) {
+            done = true;
+            a.next_ids[s] = c * 32 * kCols + lane * kCols - off + j;
+            if (a.next_prob) a.next_prob[s] = __ull2float_rn(r[j]) / __ull2float_rn(total);
+          }
+        }
+      }
+      return;
+    }
+    before += chunk;
+  }
+}
+
+}  // namespace
+
+extern "C" tfd_status tfd_accept_sampled(const float* p, int64_t ldp, const float* q, int64_t ldq,
+                                         int64_t n, int64_t nq, const int32_t* q_map,
+                                         const int32_t* drafts, const int32_t* n_asked,
+                                         const float* u, const float* u_next, int streams, int win,
+                                         int32_t* n_kept, int32_t* next_ids, float* next_prob,
+                                         int64_t* asked_hist, int64_t* kept_hist,
+                                         int32_t* dev_status, void* stream) {
+  using tfd_host::aligned;
+  if (!p || !q || !drafts || !n_asked || !u || !u_next || !n_kept || !next_ids)
+    return TFD_ERR_INVALID;
+  if (streams < 1 || win < 1 || win > TFD_MAX_TOPK || n < 1 || nq < 1 || ldp < n || ldq < nq)
+    return TFD_ERR_INVALID;
+  if (!q_map && nq != n) return TFD_ERR_INVALID;
+  if ((asked_hist == nullptr) != (kept_hist == nullptr)) return TFD_ERR_INVALID;
+  if (n > kMaxDrawCols || nq > kMaxDrawCols || streams > (1 << 24)) return TFD_ERR_UNSUPPORTED;
+  if (!aligned(p, 4) || !aligned(q, 4)) return TFD_ERR_INVALID;
+  for (const void* x : {(const void*)q_map, (const void*)drafts, (const void*)n_asked,
+                        (const void*)u, (const void*)u_next, (const void*)n_kept,
+                        (const void*)next_ids, (const void*)next_prob, (const void*)dev_status})
+    if (x && !aligned(x, 4)) return TFD_ERR_INVALID;
+  if (asked_hist && (!aligned(asked_hist, 8) || !aligned(kept_hist, 8))) return TFD_ERR_INVALID;
+  const int sms = tfd_host::sm_count();
+  int c = 1;
+  while (c < kMaxC && n / c > 2048 && (int64_t)streams * c * 2 <= 4 * (int64_t)sms) c *= 2;
+  if (c > 8 && cudaFuncSetAttribute(accept_sampled_kernel,
+                                    cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                    1) != cudaSuccess) {
+    cudaGetLastError();
+    c = 8;
+  }
+  Args a = {p, ldp, q, ldq, n, nq, q_map, drafts, n_asked, u, u_next, win, n_kept, next_ids,
+            next_prob, reinterpret_cast<unsigned long long*>(asked_hist),
+            reinterpret_cast<unsigned long long*>(kept_hist), dev_status};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)streams * c);
+  cfg.blockDim = dim3(kT);
+  cfg.stream = tfd_host::as_stream(stream);
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = c;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, accept_sampled_kernel, a);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e == cudaSuccess ? TFD_OK : TFD_ERR_CUDA;
+}

@@ -42,6 +42,10 @@ SIGNATURES = {
     "tfd_fp8_block32_relayout": (_i32, [_vp, _i64, _i64, _i32, _vp, _vp]),
     "tfd_rmsnorm": (_i32, [_vp, _i64, _vp, _f32, _i32, _i64, _vp, _i64, _vp]),
     "tfd_swiglu": (_i32, [_vp, _vp, _i64, _i32, _i64, _vp, _i64, _vp]),
+    "tfd_sample": (_i32, [_vp, _i32, _i32, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                          _i64, _vp, _i64, _vp, _vp]),
+    "tfd_accept_sampled": (_i32, [_vp, _i64, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i32,
+                                  _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "tfd_absorb": (_i32, [_vp, _vp, _vp, _f32, _f32, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32,
                           _vp, _vp]),
 }
@@ -318,3 +322,101 @@ def tfd_fp8_block32_relayout(codes, to_interleaved=True, out=None, stream=None):
                                             _stream(stream))
     _check("tfd_fp8_block32_relayout", st)
     return out
+
+
+def _vec(t, dtype, count, name):
+    """A contiguous device vector (or matrix) of ``count`` elements of one type, or None."""
+    if t is not None and (t.dtype != dtype or not t.is_cuda or t.numel() != count or
+                          not t.is_contiguous()):
+        raise ValueError(f"{name}: a contiguous CUDA tensor of {count} {dtype} is wanted")
+
+
+def tfd_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, id_map=None,
+               ids=None, prob=None, probs=None, want_probs=False, dev_status=None, n=None,
+               stream=None):
+    """One token a row of logits [rows][>= n] (bf16 or float32), drawn with the random numbers
+    u [rows] after temperature, top_k, top_p and min_p (each [rows] or None). ``ids`` [rows] may be
+    a column of a larger array (``prob`` then with the same stride); ``probs`` [rows][>= n] (or
+    want_probs) receives the filtered distribution. Returns (ids, prob, probs)."""
+    dev = logits.device
+    rows, cols = logits.shape
+    n = cols if n is None else n
+    if logits.dtype == torch.float32:
+        fmt = X_F32
+    elif logits.dtype == torch.bfloat16:
+        fmt = X_BF16
+    else:
+        raise ValueError("logits: float32 or bfloat16 is wanted")
+    if not logits.is_cuda or logits.stride(1) != 1 and cols > 1 or n > cols:
+        raise ValueError("logits: CUDA rows of at least n contiguous columns are wanted")
+    _vec(u, torch.float32, rows, "u")
+    _vec(temperature, torch.float32, rows, "temperature")
+    _vec(top_k, torch.int32, rows, "top_k")
+    _vec(top_p, torch.float32, rows, "top_p")
+    _vec(min_p, torch.float32, rows, "min_p")
+    _vec(id_map, torch.int32, n, "id_map")
+    if ids is None:
+        ids = torch.empty(rows, dtype=torch.int32, device=dev)
+        if prob is None:
+            prob = torch.empty(rows, dtype=torch.float32, device=dev)
+    if ids.dtype != torch.int32 or ids.shape != (rows,) or not ids.is_cuda:
+        raise ValueError("ids: a CUDA int32 vector of one id a row is wanted")
+    ldt = ids.stride(0) if rows > 1 else 1
+    if prob is not None and (prob.dtype != torch.float32 or prob.shape != (rows,) or
+                             not prob.is_cuda or (rows > 1 and prob.stride(0) != ldt)):
+        raise ValueError("prob: a CUDA float32 vector with the stride of ids is wanted")
+    if probs is None and want_probs:
+        probs = torch.empty((rows, n), dtype=torch.float32, device=dev)
+    ldp = 0
+    if probs is not None:
+        if probs.dtype != torch.float32 or not probs.is_cuda or probs.shape[0] != rows or \
+                probs.shape[1] < n or (probs.shape[1] > 1 and probs.stride(1) != 1):
+            raise ValueError("probs: CUDA float32 rows of at least n contiguous columns are wanted")
+        ldp = probs.stride(0) if rows > 1 else max(n, probs.stride(0))
+    st = library().tfd_sample(_p(logits), fmt, rows, n, logits.stride(0) if rows > 1 else
+                              max(n, logits.stride(0)), _p(temperature), _p(top_k), _p(top_p),
+                              _p(min_p), _p(u), _p(id_map), _p(ids), _p(prob), ldt, _p(probs), ldp,
+                              _p(dev_status), _stream(stream))
+    _check("tfd_sample", st)
+    return ids, prob, probs
+
+
+def tfd_accept_sampled(p, q, drafts, n_asked, u, u_next, q_map=None, n_kept=None, next_ids=None,
+                       next_prob=None, asked_hist=None, kept_hist=None, dev_status=None,
+                       stream=None):
+    """The rejection accept of drafts [streams][win] drawn from q [streams][win][nq] against the
+    target's p [streams][win + 1][n], with the random numbers u [streams][win], and the next token
+    drawn with u_next [streams]. q_map [n] gives a token's column in q (-1: none). The streams and
+    steps of p and q are contiguous but for the row stride. Returns (n_kept, next_ids, next_prob)."""
+    streams, win = drafts.shape
+    n, nq = p.shape[2], q.shape[2]
+    for t, steps, name in ((p, win + 1, "p"), (q, win, "q")):
+        if t.dtype != torch.float32 or not t.is_cuda or t.shape[:2] != (streams, steps) or \
+                (t.shape[2] > 1 and t.stride(2) != 1) or \
+                (streams > 1 and t.stride(0) != steps * t.stride(1)):
+            raise ValueError(f"{name}: CUDA float32 [streams][{steps}][columns] with evenly spaced "
+                             "rows is wanted")
+    _vec(drafts, torch.int32, streams * win, "drafts")
+    _vec(n_asked, torch.int32, streams, "n_asked")
+    _vec(u, torch.float32, streams * win, "u")
+    _vec(u_next, torch.float32, streams, "u_next")
+    _vec(q_map, torch.int32, n, "q_map")
+    dev = p.device
+    if n_kept is None:
+        n_kept = torch.empty(streams, dtype=torch.int32, device=dev)
+    if next_ids is None:
+        next_ids = torch.empty(streams, dtype=torch.int32, device=dev)
+        if next_prob is None:
+            next_prob = torch.empty(streams, dtype=torch.float32, device=dev)
+    _vec(n_kept, torch.int32, streams, "n_kept")
+    _vec(next_ids, torch.int32, streams, "next_ids")
+    _vec(next_prob, torch.float32, streams, "next_prob")
+    _vec(asked_hist, torch.int64, win, "asked_hist")
+    _vec(kept_hist, torch.int64, win, "kept_hist")
+    st = library().tfd_accept_sampled(_p(p), max(n, p.stride(1)), _p(q), max(nq, q.stride(1)), n,
+                                      nq, _p(q_map), _p(drafts), _p(n_asked), _p(u), _p(u_next),
+                                      streams, win, _p(n_kept), _p(next_ids), _p(next_prob),
+                                      _p(asked_hist), _p(kept_hist), _p(dev_status),
+                                      _stream(stream))
+    _check("tfd_accept_sampled", st)
+    return n_kept, next_ids, next_prob

@@ -1,0 +1,44 @@
+"""Host-side argument checks of the sampled-drafting calls: refused before the GPU is touched."""
+import pytest
+
+from speculative_decoding_draft_row_gb300 import tfd
+
+FAKE = 1 << 20  # a 16-byte aligned non-null address; never dereferenced by refused calls
+
+
+def sample_call(**kw):
+    a = dict(x=FAKE, fmt=1, rows=2, n=100, ld=100, t=None, k=None, p=None, mp=None, u=FAKE, m=None,
+             ids=FAKE, prob=None, ldt=0, probs=None, ldp=0, st=None, stream=None)
+    a.update(kw)
+    return tfd.library().tfd_sample(*a.values())
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(x=None), 1), (dict(u=None), 1), (dict(ids=None), 1), (dict(fmt=2), 1), (dict(fmt=-1), 1),
+    (dict(rows=0), 1), (dict(n=0), 1), (dict(ld=99), 1), (dict(ldt=-1), 1), (dict(x=FAKE + 2), 1),
+    (dict(t=FAKE + 2), 1), (dict(ids=FAKE + 1), 1), (dict(probs=FAKE * 2, ldp=99), 1),
+    (dict(probs=FAKE * 2 + 2, ldp=100), 1), (dict(probs=FAKE + 16, ldp=100), 1),
+    (dict(n=(1 << 20) + 1, ld=1 << 21), 2), (dict(rows=(1 << 24) + 1), 2),
+])
+def test_sample_refusals(bad, code):
+    assert sample_call(**bad) == code
+
+
+def accept_sampled_call(**kw):
+    a = dict(p=FAKE, ldp=100, q=FAKE, ldq=100, n=100, nq=100, m=None, d=FAKE, na=FAKE, u=FAKE,
+             un=FAKE, streams=4, win=5, nk=FAKE, nx=FAKE, pr=None, ah=None, kh=None, st=None,
+             stream=None)
+    a.update(kw)
+    return tfd.library().tfd_accept_sampled(*a.values())
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(p=None), 1), (dict(q=None), 1), (dict(d=None), 1), (dict(na=None), 1), (dict(u=None), 1),
+    (dict(un=None), 1), (dict(nk=None), 1), (dict(nx=None), 1), (dict(streams=0), 1),
+    (dict(win=0), 1), (dict(win=513), 1), (dict(n=0), 1), (dict(ldp=99), 1), (dict(ldq=99), 1),
+    (dict(nq=50), 1), (dict(nq=0, m=FAKE), 1), (dict(p=FAKE + 2), 1), (dict(q=FAKE + 1), 1),
+    (dict(u=FAKE + 2), 1), (dict(ah=FAKE), 1), (dict(ah=FAKE + 4, kh=FAKE), 1),
+    (dict(n=1 << 21, ldp=1 << 21, nq=1 << 21, ldq=1 << 21), 2),
+])
+def test_accept_sampled_refusals(bad, code):
+    assert accept_sampled_call(**bad) == code
