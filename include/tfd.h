@@ -85,6 +85,7 @@ typedef enum { TFD_OUT_NONE = 0, TFD_OUT_F32 = 1, TFD_OUT_BF16 = 2, TFD_OUT_ADD_
 #define TFD_MAX_ROWS 32
 #define TFD_MAX_TOPK 512    /* [TFE] commit "... ocabulary head": cand_k from 1 to 512 */
 #define TFD_MAX_WINDOW 511  /* [TFE] commit "... ocabulary head": window up to 511 (512 keys) */
+#define TFD_MAX_RANK 128     /* rank of a low-rank adapter */
 #define TFD_MAX_DRAW_COLS 1048576 /* columns of a row that a token is drawn from (exact sums) */
 
 /* A static string naming a status. Never NULL. */
@@ -391,6 +392,31 @@ tfd_status tfd_accept_sampled(const float* p, int64_t ldp, const float* q, int64
                               int streams, int win, int32_t* n_kept, int32_t* next_ids,
                               float* next_prob, int64_t* asked_hist, int64_t* kept_hist,
                               int32_t* dev_status, void* stream);
+
+/*
+ * tfd_lora - low-rank adapters of many requests at once, beside a projection they share.
+ *   y[r] = base[r] + scales[a] * B[a] (A[a] x[r]) with a = adapter_ids[r]: the base is the shared
+ *   projection's result (tfd_head_gemv's y), in place or not. Sums in fp32, A[a] x[r] kept in fp32,
+ *   y rounded once. Rows may name adapters in any order and share them; -1 is no adapter
+ *   (y[r] = base[r]). One row up to whole prompts. The pages run one set of weights for all
+ *   streams; this call has no counterpart there.
+ * Args:
+ *   x        device bf16 [rows][ldx], ldx >= k, ldx % 8 == 0; rows >= 1.
+ *   a_w, b_w device bf16 [n_adapters][rank][k] and [n_adapters][n][rank]; k >= 8, k % 8 == 0;
+ *            rank 8..TFD_MAX_RANK, rank % 8 == 0 (smaller ones padded with zeros); n >= 1;
+ *            n_adapters 1..4096. x, a_w and b_w 16-byte aligned.
+ *   adapter_ids device int32 [rows]; any other id outside [0, n_adapters) sets
+ *            TFD_ERR_DEVICE_DATA and counts as -1. scales device float [n_adapters] or NULL (1).
+ *   out_mode TFD_OUT_F32 or TFD_OUT_BF16: the type of base and y.
+ *   base     device [rows][ldb], ldb >= n, or NULL (zeros); y device [rows][ldy], ldy >= n: any
+ *            element-aligned base and stride (16-byte aligned rows are faster). y may be base
+ *            itself (same stride); it overlaps nothing else the call reads.
+ */
+tfd_status tfd_lora(const void* x, int rows, int64_t k, int64_t ldx, const void* a_w,
+                    const void* b_w, int n_adapters, int rank, int64_t n,
+                    const int32_t* adapter_ids, const float* scales, int out_mode,
+                    const void* base, int64_t ldb, void* y, int64_t ldy, int32_t* dev_status,
+                    void* stream);
 
 #ifdef __cplusplus
 }

@@ -17,6 +17,7 @@ Modules (each function cites the passage it follows):
 * ``attn``      - qk_norm + RoPE + ring-window attention for one decode position.
 * ``accept``    - accept-prefix count with per-position asked/kept histograms.
 * ``sample``    - tokens drawn from filtered logits, and the rejection accept of such drafts.
+* ``lora``      - low-rank adapters of many requests beside a shared projection.
 * ``draft_pass``- the chained multi-step draft pass (composition of the above).
 
 Every function here is pinned by ``tests/test_oracle_*.py`` against closed forms, brute force,

@@ -1,0 +1,456 @@
+// lora.cu - low-rank adapters of many requests at once: y_r = base_r + s_a B_a (A_a x_r), a the
+// adapter of row r, for one decode row up to whole prompts, in one launch without a workspace.
+//
+// Rows are grouped by adapter into tiles of up to TM rows, so an adapter used by many rows is read
+// once a tile. Every block derives its tile from the ids itself (a count per adapter, then the
+// members of its own tile): a few thousand ids cost less than another launch.
+//
+// A thread-block cluster takes a tile. Shrink: h = A x over the rank x TM outputs, k split over the
+// cluster's blocks and their warps; both operands go from global memory straight to the registers
+// of warp-level MMAs (m16n8k16, A the 16 ranks, x the 8 rows), since within a tile every weight and
+// every activation is used by one warp only. The k order is permuted alike for both so that a
+// thread's 16 contiguous bytes are its operands. The partial sums are added in a fixed order, over
+// the warps and, through distributed shared memory, over the blocks: every block then has all of h.
+// Expand: each block takes a range of the n outputs in steps of 32 a warp; h is the MMA's row
+// operand, split into bf16 parts that add up to it (below), and B's rows its columns, dealt so that
+// a thread holds 8 contiguous outputs of a row: 16-byte loads of the base and stores of y. The
+// first step's rows of B are in flight while h is reduced.
+//
+// h stays in fp32 and enters the MMAs as two (bf16 outputs: 2^-17 relative, under a 2^-9 rounding) or
+// three (fp32 outputs: all 24 bits) bf16 parts, whose products are exact in the fp32 accumulators.
+#include <cooperative_groups.h>
+
+#include "common.cuh"
+
+namespace {
+
+using namespace tfd;
+namespace cg = cooperative_groups;
+
+constexpr int kT = 256;
+constexpr int kW = kT / 32;
+constexpr int kMaxAdapters = 4096;
+constexpr int kSmallRows = 256;  // up to here one thread a row groups the rows
+
+struct Args {
+  const __nv_bfloat16* x;
+  int64_t ldx;
+  const __nv_bfloat16* a;
+  const __nv_bfloat16* b;
+  const int32_t* ids;
+  const float* scales;
+  const char* base;
+  char* y;
+  int64_t ldb, ldy;
+  int32_t* dev_status;
+  int rows, k, n, rank, n_adapters, splits;
+  bool f32, vec;
+};
+
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Which adapter (n_adapters = none) and which rows tile `t` has; 0 rows when there is no such tile.
+template <int TM>
+__device__ int find_tile(const Args& a, int t, int32_t* rows_out, int32_t* cnt, int& key) {
+  __shared__ int s_key, s_first, s_n, s_warp[kW];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) s_n = 0;
+  auto key_of = [&](int r) {
+    const int id = a.ids[r];
+    if (id >= 0 && id < a.n_adapters) return id;
+    if (id != -1) set_dev_status(a.dev_status, TFD_ERR_DEVICE_DATA);
+    return a.n_adapters;
+  };
+  if (a.rows <= kSmallRows) {
+    int mine = -1, c = 0;
+    if (tid < a.rows) cnt[tid] = mine = key_of(tid);
+    __syncthreads();
+    for (int j = 0; j < tid && tid < a.rows; ++j) c += cnt[j] == mine;
+    const bool first = tid < a.rows && c % TM == 0;
+    const unsigned bal = __ballot_sync(0xffffffffu, first);
+    if (lane == 0) s_warp[warp] = __popc(bal);
+    __syncthreads();
+    int no = __popc(bal & ((1u << lane) - 1));
+    for (int w = 0; w < warp; ++w) no += s_warp[w];
+    if (first && no == t) {
+      s_key = mine;
+      s_first = c;
+      s_n = 1;
+    }
+    __syncthreads();
+    if (s_n == 0) return 0;
+    key = s_key;
+    const int at = c - s_first;
+    const bool member = tid < a.rows && mine == key && at >= 0 && at < TM;
+    if (member) rows_out[at] = tid;
+    const int n = __syncthreads_count(member);
+    return n;
+  }
+  // counts of every adapter, the tiles before and of each, then the members in row order
+  for (int i = tid; i <= a.n_adapters; i += kT) cnt[i] = 0;
+  __syncthreads();
+  for (int r0 = 0; r0 < a.rows; r0 += kT) {
+    const int r = r0 + tid;
+    const int kk = r < a.rows ? key_of(r) : -1;
+    const unsigned same = __match_any_sync(0xffffffffu, kk);
+    if (kk >= 0 && lane == __ffs(same) - 1) atomicAdd(&cnt[kk], __popc(same));
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int before = 0;
+    for (int i0 = 0; i0 <= a.n_adapters; i0 += 32) {
+      const int i = i0 + lane;
+      const int m = i <= a.n_adapters ? (cnt[i] + TM - 1) / TM : 0;
+      int incl = m;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      if (t >= before + incl - m && t < before + incl) {
+        s_key = i;
+        s_first = (t - (before + incl - m)) * TM;
+        s_n = min(TM, cnt[i] - s_first);
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+  __syncthreads();
+  const int n = s_n;
+  if (n == 0) return 0;
+  key = s_key;
+  const int per = (a.rows + kT - 1) / kT, r0 = tid * per, r1 = min(a.rows, r0 + per);
+  int c = 0;
+  for (int r = r0; r < r1; ++r) {
+    const int id = a.ids[r];
+    c += (id >= 0 && id < a.n_adapters ? id : a.n_adapters) == key;
+  }
+  int incl = c;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) s_warp[warp] = incl;
+  __syncthreads();
+  int at = incl - c - s_first;
+  for (int w = 0; w < warp; ++w) at += s_warp[w];
+  if (at < TM && at + c > 0) {
+    for (int r = r0; r < r1; ++r) {
+      const int id = a.ids[r];
+      if ((id >= 0 && id < a.n_adapters ? id : a.n_adapters) != key) continue;
+      if (at >= 0 && at < TM) rows_out[at] = r;
+      ++at;
+    }
+  }
+  __syncthreads();
+  return n;
+}
+
+__device__ __forceinline__ uint4 zero4() { return make_uint4(0u, 0u, 0u, 0u); }
+
+// RT: 16-rank tiles (rank <= 16 RT); NT: 8-row tiles of x (TM = 8 NT).
+template <int RT, int NT>
+__global__ void __launch_bounds__(kT, 2) lora_kernel(const Args a) {
+  constexpr int TM = 8 * NT, R = 16 * RT, RP = R + 4;  // RP: partial sums without bank conflicts
+  constexpr int MT = (TM + 15) / 16, HT = 16 * MT;     // row tiles of the expand
+  constexpr int KP = RT == 1 ? 1 : RT / 2;             // 16-byte (RT 1: 8-byte) pieces of a B row
+  constexpr int HP = R + 8;
+  extern __shared__ __align__(16) unsigned char smem[];
+  float* part = reinterpret_cast<float*>(smem);                  // [kW][TM][RP]
+  float* mine = part + kW * TM * RP;                             // [TM][RP], read by the cluster
+  __nv_bfloat16* hs = reinterpret_cast<__nv_bfloat16*>(mine + TM * RP);  // [3][HT][HP]
+  __shared__ int32_t tile_rows[TM];
+  cg::cluster_group cl = cg::this_cluster();
+  const int C = (int)cl.num_blocks(), rank_c = (int)cl.block_rank();
+  const int unit = blockIdx.x / C, tile = unit / a.splits, split = unit % a.splits;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  int key = 0;
+  const int m = find_tile<TM>(a, tile, tile_rows, reinterpret_cast<int32_t*>(smem), key);
+  if (m == 0) return;  // all blocks of the cluster alike
+  const bool none = key == a.n_adapters;
+  if (none && a.base == a.y) return;
+
+  // this block's share of the outputs, in steps of 32
+  const int steps = (a.n + 31) / 32, parts = C * a.splits, part_no = split * C + rank_c;
+  const int s0 = (int)((int64_t)steps * part_no / parts);
+  const int s1 = (int)((int64_t)steps * (part_no + 1) / parts);
+  const __nv_bfloat16* bw = a.b + (int64_t)(none ? 0 : key) * a.n * a.rank;
+
+  // rows of B of step s: tile j, column g -> output 32 s + 8 (g / 2) + 2 j + g % 2
+  auto load_b = [&](int s, uint4 (&w)[4][KP]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int o = s * 32 + (g >> 1) * 8 + 2 * j + (g & 1);
+      const __nv_bfloat16* row = bw + (int64_t)o * a.rank;
+#pragma unroll
+      for (int q = 0; q < KP; ++q) {
+        w[j][q] = zero4();
+        if (RT == 1) {
+          if (o < a.n && 4 * t < a.rank) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(row + 4 * t));
+            w[j][q].x = v.x;
+            w[j][q].y = v.y;
+          }
+        } else if (o < a.n && 32 * q + 8 * t < a.rank) {
+          w[j][q] = __ldg(reinterpret_cast<const uint4*>(row + 32 * q + 8 * t));
+        }
+      }
+    }
+  };
+
+  uint4 wb[4][KP];
+  if (!none) {
+    // ---- shrink -------------------------------------------------------------------------------
+    const int blocks = (a.k + 31) / 32, slots = C * kW, slot = rank_c * kW + warp;
+    const int b0 = (int)((int64_t)blocks * slot / slots);
+    const int b1 = (int)((int64_t)blocks * (slot + 1) / slots);
+    const __nv_bfloat16* aw = a.a + ((int64_t)key * a.rank + g) * a.k + 8 * t;
+    const __nv_bfloat16* xr[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int i = 8 * j + g;  // rows past the tile's last repeat it; their sums are not used
+      xr[j] = a.x + (int64_t)tile_rows[min(i, m - 1)] * a.ldx + 8 * t;
+    }
+    float acc[RT][NT][4] = {};
+#pragma unroll 2
+    for (int b = b0; b < b1; ++b) {
+      const int k0 = b * 32;
+      const bool in = k0 + 8 * t < a.k;
+      uint4 av[RT][2], xv[NT];
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          av[i][h] = in && 16 * i + 8 * h + g < a.rank
+                         ? __ldg(reinterpret_cast<const uint4*>(aw + (int64_t)(16 * i + 8 * h) * a.k + k0))
+                         : zero4();
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        xv[j] = in ? __ldg(reinterpret_cast<const uint4*>(xr[j] + k0)) : zero4();
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          mma(acc[i][j], av[i][0].x, av[i][1].x, av[i][0].y, av[i][1].y, xv[j].x, xv[j].y);
+          mma(acc[i][j], av[i][0].z, av[i][1].z, av[i][0].w, av[i][1].w, xv[j].z, xv[j].w);
+        }
+    }
+    if (s0 + warp < s1) load_b(s0 + warp, wb);  // in flight while h is reduced
+    __syncthreads();                            // the tile search's counts are done with
+    float* p = part + warp * TM * RP;
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          p[(8 * j + 2 * t + (e & 1)) * RP + 16 * i + g + 8 * (e >> 1)] = acc[i][j][e];
+    __syncthreads();
+    for (int i = tid; i < TM * R; i += kT) {
+      const int o = (i / R) * RP + i % R;
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kW; ++w) v += part[w * TM * RP + o];
+      mine[o] = v;
+    }
+    cl.sync();
+    const float scale = a.scales ? a.scales[key] : 1.0f;
+    for (int i = tid; i < HT * R; i += kT) {
+      const int row = i / R, o = row * RP + i % R;
+      float v = 0.0f;
+      if (row < TM)
+        for (int c = 0; c < C; ++c) v += cl.map_shared_rank(mine, c)[o];
+      v *= scale;
+      const __nv_bfloat16 h0 = __float2bfloat16_rn(v);
+      const float r1 = v - __bfloat162float(h0);
+      const __nv_bfloat16 h1 = __float2bfloat16_rn(r1);
+      hs[row * HP + i % R] = h0;
+      hs[(HT + row) * HP + i % R] = h1;
+      if (a.f32) hs[(2 * HT + row) * HP + i % R] = __float2bfloat16_rn(r1 - __bfloat162float(h1));
+    }
+    cl.barrier_arrive();  // this block has read the others' sums
+    __syncthreads();
+  }
+
+  // ---- expand -----------------------------------------------------------------------------------
+  const int parts_h = a.f32 ? 3 : 2;
+  for (int s = s0 + warp; s < s1; s += kW) {
+    float acc[MT][4][4] = {};
+    if (!none) {
+      if (s != s0 + warp) load_b(s, wb);
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int q = 0; q < (RT == 1 ? 1 : 2 * KP); ++q) {
+          // 16 ranks: RT 1: 4t .. 4t+3; else half q % 2 of the thread's 8
+          const int col = RT == 1 ? 4 * t : 32 * (q >> 1) + 8 * t + 4 * (q & 1);
+          for (int h = 0; h < parts_h; ++h) {
+            const uint2 u = *reinterpret_cast<const uint2*>(hs + (h * HT + 16 * i + g) * HP + col);
+            const uint2 v =
+                *reinterpret_cast<const uint2*>(hs + (h * HT + 16 * i + 8 + g) * HP + col);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint4 w = wb[j][q >> 1];
+              mma(acc[i][j], u.x, v.x, u.y, v.y, (q & 1) ? w.z : w.x, (q & 1) ? w.w : w.y);
+            }
+          }
+        }
+    }
+    const int o = s * 32 + 8 * t;
+    if (o >= a.n) continue;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int slot = 16 * i + 8 * h + g;
+        if (slot >= m) continue;
+        const int64_t row = tile_rows[slot];
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[2 * j] = acc[i][j][2 * h];
+          v[2 * j + 1] = acc[i][j][2 * h + 1];
+        }
+        if (a.f32) {
+          const float* bp = reinterpret_cast<const float*>(a.base) + row * a.ldb + o;
+          float* yp = reinterpret_cast<float*>(a.y) + row * a.ldy + o;
+          if (a.vec && o + 8 <= a.n) {
+#pragma unroll
+            for (int e = 0; e < 8; e += 4) {
+              float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              if (a.base) r = *reinterpret_cast<const float4*>(bp + e);
+              *reinterpret_cast<float4*>(yp + e) =
+                  make_float4(r.x + v[e], r.y + v[e + 1], r.z + v[e + 2], r.w + v[e + 3]);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (o + e < a.n) yp[e] = (a.base ? bp[e] : 0.0f) + v[e];
+          }
+        } else {
+          const uint16_t* bp = reinterpret_cast<const uint16_t*>(a.base) + row * a.ldb + o;
+          uint16_t* yp = reinterpret_cast<uint16_t*>(a.y) + row * a.ldy + o;
+          if (a.vec && o + 8 <= a.n) {
+            uint4 r = zero4();
+            if (a.base) r = *reinterpret_cast<const uint4*>(bp);
+            uint32_t* w = &r.x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = (uint32_t)f32_to_bf16_bits(bf16_lo(w[e]) + v[2 * e]) |
+                     ((uint32_t)f32_to_bf16_bits(bf16_hi(w[e]) + v[2 * e + 1]) << 16);
+            *reinterpret_cast<uint4*>(yp) = r;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (o + e < a.n)
+                yp[e] = f32_to_bf16_bits((a.base ? bf16_bits_to_f32(bp[e]) : 0.0f) + v[e]);
+          }
+        }
+      }
+  }
+  if (!none) cl.barrier_wait();  // the others have read this block's sums
+}
+
+template <int RT, int NT>
+tfd_status launch(const Args& a, int c, int64_t units, cudaStream_t stream) {
+  constexpr int TM = 8 * NT, R = 16 * RT, RP = R + 4, HT = (TM + 15) / 16 * 16;
+  size_t smem = (size_t)(kW + 1) * TM * RP * 4 + (size_t)3 * HT * (R + 8) * 2;
+  const size_t counts = (size_t)4 * (a.rows <= kSmallRows ? kSmallRows : a.n_adapters + 1);
+  if (smem < counts) smem = counts;
+  auto* k = lora_kernel<RT, NT>;
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+          cudaSuccess ||
+      cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+    cudaGetLastError();
+    return TFD_ERR_CUDA;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units * c));
+  cfg.blockDim = dim3(kT);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = c;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, a);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e == cudaSuccess ? TFD_OK : TFD_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" tfd_status tfd_lora(const void* x, int rows, int64_t k, int64_t ldx, const void* a_w,
+                               const void* b_w, int n_adapters, int rank, int64_t n,
+                               const int32_t* adapter_ids, const float* scales, int out_mode,
+                               const void* base, int64_t ldb, void* y, int64_t ldy,
+                               int32_t* dev_status, void* stream) {
+  using tfd_host::aligned;
+  if (!x || !a_w || !b_w || !adapter_ids || !y) return TFD_ERR_INVALID;
+  if (out_mode != TFD_OUT_F32 && out_mode != TFD_OUT_BF16) return TFD_ERR_INVALID;
+  if (rows < 1 || k < 8 || k % 8 || n < 1 || n_adapters < 1 || rank < 8 || rank % 8)
+    return TFD_ERR_INVALID;
+  if (ldx < k || ldx % 8 || ldy < n || (base && ldb < n)) return TFD_ERR_INVALID;
+  if (rank > TFD_MAX_RANK || n_adapters > kMaxAdapters || k > (1 << 24) || n > (1 << 24) ||
+      rows > (1 << 22))
+    return TFD_ERR_UNSUPPORTED;
+  const int es = out_mode == TFD_OUT_F32 ? 4 : 2;
+  if (!aligned(x, 16) || !aligned(a_w, 16) || !aligned(b_w, 16) || !aligned(y, es) ||
+      !aligned(base, es) || !aligned(adapter_ids, 4) || !aligned(scales, 4) ||
+      !aligned(dev_status, 4))
+    return TFD_ERR_INVALID;
+  auto overlap = [&](const void* p, int64_t bytes, const void* q, int64_t qbytes) {
+    return (const char*)p < (const char*)q + qbytes && (const char*)q < (const char*)p + bytes;
+  };
+  const int64_t ybytes = (((int64_t)rows - 1) * ldy + n) * es;
+  if (overlap(y, ybytes, x, (((int64_t)rows - 1) * ldx + k) * 2)) return TFD_ERR_INVALID;
+  if (base && !(base == y && ldb == ldy) &&
+      overlap(y, ybytes, base, (((int64_t)rows - 1) * ldb + n) * es))
+    return TFD_ERR_INVALID;
+
+  const bool vec = aligned(y, 16) && ldy * es % 16 == 0 &&
+                   (!base || (aligned(base, 16) && ldb * es % 16 == 0));
+  // rows of a tile: what one adapter is likely to have, within the accumulators' registers
+  const int rt = rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8;
+  const int each = (rows + n_adapters - 1) / n_adapters;
+  int nt = each <= 8 ? 1 : each <= 32 ? 2 : 16 / rt;
+  if (nt > 8) nt = 8;
+  const int tm = 8 * nt;
+  const int64_t bound = (int64_t)rows / tm + n_adapters + 1;
+  const int64_t tiles = bound < rows ? bound : rows;
+  // blocks: as many as fit the SMs once, a cluster's share of k and n at least 32 a warp
+  int64_t likely = (rows + tm - 1) / tm;
+  if (likely < n_adapters) likely = n_adapters < rows ? n_adapters : rows;
+  const int sms = tfd_host::sm_count() > 0 ? tfd_host::sm_count() : 1;
+  const int64_t wide = k > n ? k : n;
+  int c = 1, splits = 1;
+  while (c < 8 && likely * c * 2 <= 2 * sms && wide / (c * 2) >= 32 * kW) c *= 2;
+  if (c == 8)
+    while (likely * c * splits * 2 <= 2 * sms && n / (c * splits * 2) >= 32 * kW &&
+           n / splits >= 2 * k)
+      splits *= 2;
+  Args a = {(const __nv_bfloat16*)x, ldx, (const __nv_bfloat16*)a_w, (const __nv_bfloat16*)b_w,
+            adapter_ids, scales, (const char*)base, (char*)y, ldb, ldy, dev_status, rows, (int)k,
+            (int)n, rank, n_adapters, splits, es == 4, vec};
+  cudaStream_t st = tfd_host::as_stream(stream);
+  const int64_t units = tiles * splits;
+  if (units * c > 0x7fffffff) return TFD_ERR_UNSUPPORTED;
+#define TFD_LORA_CASE(RT, NT) \
+  if (rt == RT && nt == NT) return launch<RT, NT>(a, c, units, st);
+  TFD_LORA_CASE(1, 1) TFD_LORA_CASE(1, 2) TFD_LORA_CASE(1, 8)
+  TFD_LORA_CASE(2, 1) TFD_LORA_CASE(2, 2) TFD_LORA_CASE(2, 8)
+  TFD_LORA_CASE(4, 1) TFD_LORA_CASE(4, 2) TFD_LORA_CASE(4, 4)
+  TFD_LORA_CASE(8, 1) TFD_LORA_CASE(8, 2)
+#undef TFD_LORA_CASE
+  return TFD_ERR_UNSUPPORTED;
+}

@@ -46,6 +46,8 @@ SIGNATURES = {
                           _i64, _vp, _i64, _vp, _vp]),
     "tfd_accept_sampled": (_i32, [_vp, _i64, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i32,
                                   _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "tfd_lora": (_i32, [_vp, _i32, _i64, _i64, _vp, _vp, _i32, _i32, _i64, _vp, _vp, _i32, _vp, _i64,
+                        _vp, _i64, _vp, _vp]),
     "tfd_absorb": (_i32, [_vp, _vp, _vp, _f32, _f32, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32,
                           _vp, _vp]),
 }
@@ -420,3 +422,41 @@ def tfd_accept_sampled(p, q, drafts, n_asked, u, u_next, q_map=None, n_kept=None
                                       _stream(stream))
     _check("tfd_accept_sampled", st)
     return n_kept, next_ids, next_prob
+
+
+def _rows_of(t, rows, cols, dtype, name):
+    """Row stride of a CUDA matrix [rows][>= cols] with contiguous columns."""
+    if t.dtype != dtype or not t.is_cuda or t.dim() != 2 or t.shape[0] != rows or \
+            t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: a CUDA {dtype} [{rows}][{cols}] with contiguous columns is wanted")
+    return t.stride(0) if rows > 1 else max(cols, t.stride(0))
+
+
+def tfd_lora(x, a, b, adapter_ids, base=None, y=None, scales=None, out_mode=OUT_BF16,
+             dev_status=None, stream=None):
+    """y[r] = base[r] + scales[i] * b[i] (a[i] x[r]), i = adapter_ids[r] (-1: none), for bf16 x
+    [rows][k], a [adapters][rank][k], b [adapters][n][rank]. base (or None for zeros) and y have one
+    type, float32 or bfloat16 (base's or y's, else out_mode); y may be base. Returns y."""
+    rows, k = x.shape
+    na, rank, _ = a.shape
+    n = b.shape[1]
+    like = y if y is not None else base
+    if like is not None:
+        out_mode = OUT_F32 if like.dtype == torch.float32 else OUT_BF16
+    dt = torch.float32 if out_mode == OUT_F32 else torch.bfloat16
+    ldx = _rows_of(x, rows, k, torch.bfloat16, "x")
+    if a.shape[2] != k or b.shape != (na, n, rank):
+        raise ValueError("a [adapters][rank][k] and b [adapters][n][rank] do not fit x")
+    _vec(a, torch.bfloat16, na * rank * k, "a")
+    _vec(b, torch.bfloat16, na * n * rank, "b")
+    _vec(adapter_ids, torch.int32, rows, "adapter_ids")
+    _vec(scales, torch.float32, na, "scales")
+    if y is None:
+        y = torch.empty((rows, n), dtype=dt, device=x.device)
+    ldy = _rows_of(y, rows, n, dt, "y")
+    ldb = _rows_of(base, rows, n, dt, "base") if base is not None else 0
+    st = library().tfd_lora(_p(x), rows, k, ldx, _p(a), _p(b), na, rank, n, _p(adapter_ids),
+                            _p(scales), out_mode, _p(base), ldb, _p(y), ldy, _p(dev_status),
+                            _stream(stream))
+    _check("tfd_lora", st)
+    return y

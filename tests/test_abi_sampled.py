@@ -42,3 +42,25 @@ def accept_sampled_call(**kw):
 ])
 def test_accept_sampled_refusals(bad, code):
     assert accept_sampled_call(**bad) == code
+
+
+def lora_call(**kw):
+    a = dict(x=FAKE, rows=2, k=64, ldx=64, a=FAKE, b=FAKE, na=3, rank=8, n=100, ids=FAKE, s=None,
+             out=2, base=None, ldb=0, y=FAKE * 2, ldy=100, st=None, stream=None)
+    a.update(kw)
+    return tfd.library().tfd_lora(*a.values())
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(x=None), 1), (dict(a=None), 1), (dict(b=None), 1), (dict(ids=None), 1), (dict(y=None), 1),
+    (dict(out=0), 1), (dict(out=3), 1), (dict(rows=0), 1), (dict(k=60), 1), (dict(k=0), 1),
+    (dict(ldx=56), 1), (dict(ldx=68), 1), (dict(n=0), 1), (dict(na=0), 1), (dict(rank=0), 1),
+    (dict(rank=12), 1), (dict(ldy=99), 1), (dict(base=FAKE * 3, ldb=99), 1), (dict(x=FAKE + 8), 1),
+    (dict(a=FAKE + 8), 1), (dict(y=FAKE * 2 + 1), 1), (dict(ids=FAKE + 2), 1),
+    (dict(y=FAKE), 1),                                          # y overlaps x
+    (dict(base=FAKE * 2 + 200, ldb=100), 1),                    # y overlaps base, shifted
+    (dict(base=FAKE * 2, ldb=104), 1),                          # the same base, another stride
+    (dict(rank=136), 2), (dict(na=4097), 2), (dict(rows=(1 << 22) + 1, y=FAKE << 20), 2),
+])
+def test_lora_refusals(bad, code):
+    assert lora_call(**bad) == code
