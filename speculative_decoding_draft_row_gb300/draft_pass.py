@@ -7,6 +7,16 @@ streams: attention, wo, w2 and the top-1 per step) and the update "main3x heads,
 linears" (wo and w2 in e4m3 with a row scale; a pass's steps captured once as a CUDA graph and
 replayed). The steps' inputs (q, k, v, the w2 input, positions) are staged in fixed buffers so the
 whole pass can be captured. Every computation is a libtfd call; this module only marshals buffers.
+
+Two options, both off by default, serve requests of their own kind (the pages' pass is greedy, with
+one set of weights):
+
+* ``adapters`` gives wo, w2 and/or the head low-rank adapters; each stream names its own
+  (``adapter_ids``, -1 for none), and its term is added to the projection's result.
+* ``sampled`` draws each step's draft from the filtered distribution of its logits (temperature,
+  top-k, top-p, min-p and the random numbers are fixed buffers per stream) and keeps the
+  distributions; the accept is then the rejection accept against the target's distributions ``p``,
+  which also draws the round's next token.
 """
 import torch
 
@@ -15,7 +25,10 @@ from . import tfd
 
 class DraftPass:
     def __init__(self, wo_codes, wo_scales, w2_codes, w2_scales, head, head_fmt, head_scales,
-                 k_ring, v_ring, window, steps, eps=1e-6, rope_base=10000.0):
+                 k_ring, v_ring, window, steps, eps=1e-6, rope_base=10000.0, adapters=None,
+                 adapter_scales=None, sampled=False):
+        """``adapters``: {"wo" | "w2" | "head": (a [adapters][rank][in], b [adapters][out][rank])},
+        all with the same number of adapters; ``adapter_scales`` float32 [adapters] or None."""
         dev = head.device
         self.steps = steps
         self.S, self.ring, self.H, self.D = k_ring.shape
@@ -44,6 +57,30 @@ class DraftPass:
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         self.ws = tfd.zeroed_workspace(tfd.tfd_head_gemv_workspace(S, head.shape[0], 1), dev)
         self.graph = None
+        self.adapters = dict(adapters or {})
+        if set(self.adapters) - {"wo", "w2", "head"}:
+            raise ValueError("adapters: wo, w2 and head can have them")
+        self.adapter_scales = adapter_scales
+        self.adapter_ids = torch.full((S,), -1, dtype=torch.int32, device=dev)
+        self.sampled = sampled
+        vocab = head.shape[0]
+        f32 = dict(dtype=torch.float32, device=dev)
+        self.logits = None
+        if sampled or "head" in self.adapters:
+            self.logits = torch.zeros((S, vocab), **f32)
+            self.topk_ws = tfd.zeroed_workspace(tfd.tfd_topk_workspace(S, vocab, 1), dev)
+            self.top_val = torch.zeros((S, 1), **f32)
+            self.top_id = torch.zeros((S, 1), dtype=torch.int32, device=dev)
+        if sampled:
+            self.temperature, self.top_p = torch.ones(S, **f32), torch.ones(S, **f32)
+            self.min_p = torch.zeros(S, **f32)
+            self.top_k = torch.zeros(S, dtype=torch.int32, device=dev)
+            self.u_draft = torch.zeros((steps, S), **f32)
+            self.u_accept, self.u_next = torch.zeros((S, steps), **f32), torch.zeros(S, **f32)
+            self.q_dist = torch.zeros((S, steps, vocab), **f32)
+            self.p_dist = torch.zeros((S, steps + 1, vocab), **f32)
+            self.next_ids = torch.zeros(S, dtype=torch.int32, device=dev)
+            self.next_prob = torch.zeros(S, **f32)
 
     def load(self, qs, ks, vs, us, pos0, resid, n_asked=None, draws=None):
         """Copy one pass's inputs into the fixed buffers (host or device tensors)."""
@@ -60,6 +97,27 @@ class DraftPass:
         if draws is not None:
             self.draws.copy_(torch.as_tensor(draws, dtype=torch.int32), non_blocking=True)
 
+    def load_sampling(self, u_draft, u_accept, u_next, temperature=None, top_k=None, top_p=None,
+                      min_p=None, p_dist=None):
+        """Copy a sampled pass's random numbers (u_draft [steps][S], u_accept [S][steps], u_next
+        [S]), settings [S] and the target's distributions p_dist [S][steps + 1][vocab]."""
+        given = dict(u_draft=u_draft, u_accept=u_accept, u_next=u_next, temperature=temperature,
+                     top_k=top_k, top_p=top_p, min_p=min_p, p_dist=p_dist)
+        for name, v in given.items():
+            if v is not None:
+                buf = getattr(self, name)
+                buf.copy_(torch.as_tensor(v).to(buf.dtype), non_blocking=True)
+
+    def load_adapter_ids(self, ids):
+        """Copy each stream's adapter (-1: none)."""
+        self.adapter_ids.copy_(torch.as_tensor(ids, dtype=torch.int32), non_blocking=True)
+
+    def add_adapter(self, name, x, y):
+        if name in self.adapters:
+            a, b = self.adapters[name]
+            tfd.tfd_lora(x, a, b, self.adapter_ids, base=y, y=y, scales=self.adapter_scales,
+                         dev_status=self.status)
+
     def step_attn(self, t):
         tfd.tfd_window_attn(self.q[t], self.k[t], self.v[t], self.pos[t], self.k_ring, self.v_ring,
                             self.window, eps=self.eps, rope_base=self.rope_base, out=self.attn,
@@ -68,12 +126,29 @@ class DraftPass:
     def step_wo(self):
         tfd.tfd_head_gemv(self.wo, tfd.W_FP8_ROW, self.wo_s, self.attn, tfd.OUT_ADD_BF16,
                           y=self.resid)
+        self.add_adapter("wo", self.attn, self.resid)
 
     def step_w2(self, t):
         tfd.tfd_head_gemv(self.w2, tfd.W_FP8_ROW, self.w2_s, self.u[t], tfd.OUT_ADD_BF16,
                           y=self.resid)
+        self.add_adapter("w2", self.u[t], self.resid)
 
     def step_head(self, t):
+        if self.logits is not None:
+            tfd.tfd_head_gemv(self.head, self.head_fmt, self.head_s, self.resid, tfd.OUT_F32,
+                              y=self.logits)
+            self.add_adapter("head", self.resid, self.logits)
+            if self.sampled:
+                # the draft and its probability under the distribution it was drawn from
+                tfd.tfd_sample(self.logits, self.u_draft[t], self.temperature, self.top_k,
+                               self.top_p, self.min_p, ids=self.drafts[:, t],
+                               prob=self.draft_vals[:, t], probs=self.q_dist[:, t],
+                               dev_status=self.status)
+            else:
+                tfd.tfd_topk(self.logits, 1, vals=self.top_val, ids=self.top_id, ws=self.topk_ws)
+                self.drafts[:, t:t + 1].copy_(self.top_id)
+                self.draft_vals[:, t:t + 1].copy_(self.top_val)
+            return
         tfd.tfd_head_gemv(self.head, self.head_fmt, self.head_s, self.resid, tfd.OUT_NONE, topk=1,
                           top_vals=self.draft_vals[:, t:t + 1], top_ids=self.drafts[:, t:t + 1],
                           ws=self.ws)
@@ -85,6 +160,13 @@ class DraftPass:
         self.step_head(t)
 
     def enqueue_accept(self):
+        if self.sampled:
+            tfd.tfd_accept_sampled(self.p_dist, self.q_dist, self.drafts, self.n_asked,
+                                   self.u_accept, self.u_next, n_kept=self.n_kept,
+                                   next_ids=self.next_ids, next_prob=self.next_prob,
+                                   asked_hist=self.asked_hist, kept_hist=self.kept_hist,
+                                   dev_status=self.status)
+            return
         tfd.tfd_accept(self.drafts, self.n_asked, self.draws, n_kept=self.n_kept,
                        asked_hist=self.asked_hist, kept_hist=self.kept_hist,
                        dev_status=self.status)
@@ -95,8 +177,10 @@ class DraftPass:
         self.enqueue_accept()
 
     def launches(self):
-        """Kernels one pass launches: 4 per step (attention, wo, w2, head) and the accept."""
-        return 4 * self.steps + 1
+        """Kernels of this library one pass launches: per step attention, wo, w2 and head, one more
+        for each adapted projection, and one for a draft taken from written logits; the accept."""
+        per = 4 + len(self.adapters) + (1 if self.logits is not None else 0)
+        return per * self.steps + 1
 
     def capture(self):
         """Capture one whole pass as a CUDA graph (replayed by run())."""
