@@ -13,6 +13,7 @@
 // the drawn column scans the part of one warp.
 #include <cooperative_groups.h>
 
+#include "launch.cuh"
 #include "weight.cuh"
 
 namespace {
@@ -20,10 +21,11 @@ namespace {
 using namespace tfd;
 namespace cg = cooperative_groups;
 
-constexpr int kT = 512;
+constexpr int kT = 256;
 constexpr int kW = kT / 32;
 constexpr int kMaxC = 16;
-constexpr int kCols = 4;  // columns a lane takes at once
+constexpr int kCols = 4;   // columns a lane takes at once
+constexpr int kBatch = 4;  // such loads in flight
 
 struct Args {
   const float* p;
@@ -45,13 +47,24 @@ struct Args {
   int32_t* dev_status;
 };
 
-// A probability as an integer multiple of 2^-43: 21 bits, then 22.
-__device__ __forceinline__ uint64_t prob_fix(float x) {
-  x = fminf(fmaxf(x, 0.0f), 1.0f);  // NaN -> 0
-  const float y = x * 2097152.0f;
-  const uint32_t hi = __float2uint_rz(y);
-  const uint32_t lo = __float2uint_rn((y - (float)hi) * 4194304.0f);
-  return ((uint64_t)hi << 22) + lo;
+// max(p - q, 0) as an integer multiple of 2^-43, p and q clamped to 0..1 (NaN to 0). For p > q the
+// difference is dh + dl exactly; it is cut into 21 bits and a signed rest below 2^-21, each taken
+// from the low bits of a float to which 1.5 * 2^23 was added: no float-to-integer conversions,
+// whose unit has a sixteenth of the FMA rate (48 x 163840 columns: 32.7 us with them).
+__device__ __forceinline__ uint64_t rest_fix(float p, float q) {
+  p = fminf(fmaxf(p, 0.0f), 1.0f);
+  q = fminf(fmaxf(q, 0.0f), 1.0f);
+  const float dh = fmaxf(__fsub_rn(p, q), 0.0f);
+  const float dl = __fsub_rn(__fsub_rn(p, dh), q);
+  const float magic = 12582912.0f;
+  const float a = __fmaf_rn(dh, 2097152.0f, magic);
+  const float top = __fsub_rn(a, magic);
+  float rest = __fmaf_rn(dh, 2097152.0f, -top);              // exact, |rest| <= 1/2
+  rest = __fmaf_rn(dl, 2097152.0f, rest);
+  const float b = __fmaf_rn(rest, 4194304.0f, magic);
+  const int64_t v = ((int64_t)(int32_t)(__float_as_uint(a) - 0x4B400000u) << 22) +
+                    (int32_t)(__float_as_uint(b) - 0x4B400000u);
+  return dh > 0.0f ? (uint64_t)v : 0;
 }
 
 __device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
@@ -61,8 +74,8 @@ __device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
 }
 
 struct Shared {
-  uint64_t cres[kMaxC], cp[kMaxC];  // every block's residual mass and p mass
-  uint64_t wres[kW], wp[kW];        // this block's warps
+  uint64_t blocks[2][kMaxC];  // every block's mass of max(p - q, 0); of p, where that is zero
+  uint64_t warps[kW];         // this block's warps'
   int fail, bad;
 };
 
@@ -127,28 +140,28 @@ __global__ void __launch_bounds__(kT) accept_sampled_kernel(const Args a) {
   const int per_c = (chunks + C - 1) / C, per_w = (per_c + kW - 1) / kW;
   const int cbeg = rank * per_c + warp * per_w;
   const int cend = min(min(cbeg + per_w, (rank + 1) * per_c), chunks);
-  const bool qvec = rejected && !a.q_map && (((uintptr_t)(qrow - off)) & 15) == 0;
+  const bool qvec = !a.q_map && (((uintptr_t)(qrow - off)) & 15) == 0;
 
-  auto load = [&](int chunk, uint64_t (&r)[kCols], uint64_t (&p)[kCols]) {
+  bool from_p = !rejected;
+  auto load = [&](int chunk, float4& p, float4& q) {
     const int c0 = chunk * 32 * kCols + lane * kCols - off;
-    float pv[kCols], qv[kCols] = {0.0f, 0.0f, 0.0f, 0.0f};
+    p = q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (c0 >= 0 && c0 + kCols <= n) {
-      const float4 v = __ldg((const float4*)(prow + c0));
-      pv[0] = v.x, pv[1] = v.y, pv[2] = v.z, pv[3] = v.w;
-      if (qvec) {
-        const float4 w = __ldg((const float4*)(qrow + c0));
-        qv[0] = w.x, qv[1] = w.y, qv[2] = w.z, qv[3] = w.w;
-      }
+      p = __ldg((const float4*)(prow + c0));
+      if (qvec && !from_p) q = __ldg((const float4*)(qrow + c0));
     } else {
+      float* pv = &p.x;
+      float* qv = &q.x;
 #pragma unroll
       for (int j = 0; j < kCols; ++j) {
         const int c = c0 + j;
-        const bool in = c >= 0 && c < n;
-        pv[j] = in ? prow[c] : 0.0f;
-        if (qvec && in) qv[j] = qrow[c];
+        if (c < 0 || c >= n) continue;
+        pv[j] = prow[c];
+        if (qvec && !from_p) qv[j] = qrow[c];
       }
     }
-    if (rejected && !qvec) {
+    if (!qvec && !from_p) {
+      float* qv = &q.x;
 #pragma unroll
       for (int j = 0; j < kCols; ++j) {
         const int c = c0 + j;
@@ -157,49 +170,40 @@ __global__ void __launch_bounds__(kT) accept_sampled_kernel(const Args a) {
         if (k >= 0 && k < a.nq) qv[j] = qrow[k];
       }
     }
-#pragma unroll
-    for (int j = 0; j < kCols; ++j) {
-      p[j] = prob_fix(pv[j]);
-      const uint64_t q = prob_fix(qv[j]);
-      r[j] = p[j] > q ? p[j] - q : 0;
-    }
   };
 
-  uint64_t rs = 0, ps = 0;
-#pragma unroll 4
-  for (int c = cbeg; c < cend; ++c) {
-    uint64_t r[kCols], p[kCols];
-    load(c, r, p);
+  // the masses; a second round over p alone where nothing of it lies above q
+  uint64_t total = 0;
+  const uint64_t* blocks = sh.blocks[0];
+  for (int round = 0; round < 2; ++round) {
+    uint64_t sum = 0;
+    for (int c = cbeg; c < cend; c += kBatch) {
+      float4 p[kBatch], q[kBatch];
 #pragma unroll
-    for (int j = 0; j < kCols; ++j) {
-      rs += r[j];
-      ps += p[j];
+      for (int i = 0; i < kBatch; ++i) {
+        p[i] = q[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (c + i < cend) load(c + i, p[i], q[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        sum += rest_fix(p[i].x, q[i].x) + rest_fix(p[i].y, q[i].y) + rest_fix(p[i].z, q[i].z) +
+               rest_fix(p[i].w, q[i].w);
     }
-  }
-  rs = warp_sum64(rs);
-  ps = warp_sum64(ps);
-  if (lane == 0) {
-    sh.wres[warp] = rs;
-    sh.wp[warp] = ps;
-  }
-  cl.sync();  // every block runs, and this block's sums are written
-  if (tid < C) {
-    uint64_t x = 0, y = 0;
-    for (int w = 0; w < kW; ++w) {
-      x += sh.wres[w];
-      y += sh.wp[w];
+    sum = warp_sum64(sum);
+    if (lane == 0) sh.warps[warp] = sum;
+    if (round == 0) cl.sync();  // every block runs, and this block's sums are written
+    else __syncthreads();
+    if (tid < C) {
+      uint64_t x = 0;
+      for (int w = 0; w < kW; ++w) x += sh.warps[w];
+      *cl.map_shared_rank(&sh.blocks[round][rank], tid) = x;
     }
-    *cl.map_shared_rank(&sh.cres[rank], tid) = x;
-    *cl.map_shared_rank(&sh.cp[rank], tid) = y;
+    cl.sync();
+    blocks = sh.blocks[round];
+    for (int c = 0; c < C; ++c) total += blocks[c];
+    if (total != 0 || from_p) break;
+    from_p = true;
   }
-  cl.sync();
-  uint64_t res = 0, all = 0;
-  for (int c = 0; c < C; ++c) {
-    res += sh.cres[c];
-    all += sh.cp[c];
-  }
-  const bool from_p = res == 0;  // nothing is left of p above q
-  const uint64_t total = from_p ? all : res;
   if (total == 0) {
     if (rank == 0 && tid == 0) {
       a.next_ids[s] = -1;
@@ -208,22 +212,17 @@ __global__ void __launch_bounds__(kT) accept_sampled_kernel(const Args a) {
     return;
   }
   const uint64_t target = mul_frac(un, total, false);
-  const uint64_t* blocks = from_p ? sh.cp : sh.cres;
-  const uint64_t* warps = from_p ? sh.wp : sh.wres;
   uint64_t before = 0;
   for (int c = 0; c < rank; ++c) before += blocks[c];
   if (target < before || target >= before + blocks[rank]) return;
-  for (int w = 0; w < warp; ++w) before += warps[w];
-  if (target < before || target >= before + warps[warp]) return;
+  for (int w = 0; w < warp; ++w) before += sh.warps[w];
+  if (target < before || target >= before + sh.warps[warp]) return;
   for (int c = cbeg; c < cend; ++c) {
-    uint64_t r[kCols], p[kCols];
-    load(c, r, p);
-    uint64_t sum = 0;
-#pragma unroll
-    for (int j = 0; j < kCols; ++j) {
-      if (from_p) r[j] = p[j];
-      sum += r[j];
-    }
+    float4 p, q;
+    load(c, p, q);
+    const uint64_t r[kCols] = {rest_fix(p.x, q.x), rest_fix(p.y, q.y), rest_fix(p.z, q.z),
+                               rest_fix(p.w, q.w)};
+    const uint64_t sum = r[0] + r[1] + r[2] + r[3];
     uint64_t incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -274,29 +273,14 @@ extern "C" tfd_status tfd_accept_sampled(const float* p, int64_t ldp, const floa
                         (const void*)next_ids, (const void*)next_prob, (const void*)dev_status})
     if (x && !aligned(x, 4)) return TFD_ERR_INVALID;
   if (asked_hist && (!aligned(asked_hist, 8) || !aligned(kept_hist, 8))) return TFD_ERR_INVALID;
-  const int sms = tfd_host::sm_count();
+  // blocks a stream: enough to load every SM with a few, each at least 1024 columns
+  int dev = 0;
+  const int sms = tfd_host::device_sms(dev);
   int c = 1;
-  while (c < kMaxC && n / c > 2048 && (int64_t)streams * c * 2 <= 4 * (int64_t)sms) c *= 2;
-  if (c > 8 && cudaFuncSetAttribute(accept_sampled_kernel,
-                                    cudaFuncAttributeNonPortableClusterSizeAllowed,
-                                    1) != cudaSuccess) {
-    cudaGetLastError();
-    c = 8;
-  }
+  while (c < kMaxC && n / c > 1024 && (int64_t)streams * c * 2 <= 4 * (int64_t)sms) c *= 2;
   Args a = {p, ldp, q, ldq, n, nq, q_map, drafts, n_asked, u, u_next, win, n_kept, next_ids,
             next_prob, reinterpret_cast<unsigned long long*>(asked_hist),
             reinterpret_cast<unsigned long long*>(kept_hist), dev_status};
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)streams * c);
-  cfg.blockDim = dim3(kT);
-  cfg.stream = tfd_host::as_stream(stream);
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = c;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, accept_sampled_kernel, a);
-  if (e != cudaSuccess) cudaGetLastError();
-  return e == cudaSuccess ? TFD_OK : TFD_ERR_CUDA;
+  return tfd_host::launch_clusters<accept_sampled_kernel>(a, streams, c, kT, 0, 0,
+                                                          tfd_host::as_stream(stream));
 }

@@ -20,7 +20,7 @@
 // three (fp32 outputs: all 24 bits) bf16 parts, whose products are exact in the fp32 accumulators.
 #include <cooperative_groups.h>
 
-#include "common.cuh"
+#include "launch.cuh"
 
 namespace {
 
@@ -365,27 +365,7 @@ tfd_status launch(const Args& a, int c, int64_t units, cudaStream_t stream) {
   size_t smem = (size_t)(kW + 1) * TM * RP * 4 + (size_t)3 * HT * (R + 8) * 2;
   const size_t counts = (size_t)4 * (a.rows <= kSmallRows ? kSmallRows : a.n_adapters + 1);
   if (smem < counts) smem = counts;
-  auto* k = lora_kernel<RT, NT>;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-          cudaSuccess ||
-      cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
-    cudaGetLastError();
-    return TFD_ERR_CUDA;
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(units * c));
-  cfg.blockDim = dim3(kT);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = c;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, a);
-  if (e != cudaSuccess) cudaGetLastError();
-  return e == cudaSuccess ? TFD_OK : TFD_ERR_CUDA;
+  return tfd_host::launch_clusters<lora_kernel<RT, NT>>(a, units, c, kT, smem, 112 * 1024, stream);
 }
 
 }  // namespace
@@ -431,7 +411,8 @@ extern "C" tfd_status tfd_lora(const void* x, int rows, int64_t k, int64_t ldx, 
   // blocks: as many as fit the SMs once, a cluster's share of k and n at least 32 a warp
   int64_t likely = (rows + tm - 1) / tm;
   if (likely < n_adapters) likely = n_adapters < rows ? n_adapters : rows;
-  const int sms = tfd_host::sm_count() > 0 ? tfd_host::sm_count() : 1;
+  int dev = 0;
+  const int sms = tfd_host::device_sms(dev);
   const int64_t wide = k > n ? k : n;
   int c = 1, splits = 1;
   while (c < 8 && likely * c * 2 <= 2 * sms && wide / (c * 2) >= 32 * kW) c *= 2;

@@ -18,6 +18,7 @@
 // and 3 fall away.
 #include <cooperative_groups.h>
 
+#include "launch.cuh"
 #include "weight.cuh"
 
 namespace {
@@ -664,31 +665,6 @@ __global__ void __launch_bounds__(kT) sample_kernel(const Args a) {
   s.run();
 }
 
-template <bool BF16, bool KEEP>
-tfd_status launch(const Args& a, int rows, int c, size_t smem, cudaStream_t stream) {
-  auto* k = sample_kernel<BF16, KEEP>;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-          cudaSuccess ||
-      cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
-    cudaGetLastError();
-    return TFD_ERR_CUDA;
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)rows * c);
-  cfg.blockDim = dim3(kT);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = c;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, a);
-  if (e != cudaSuccess) cudaGetLastError();
-  return e == cudaSuccess ? TFD_OK : TFD_ERR_CUDA;
-}
-
 }  // namespace
 
 extern "C" tfd_status tfd_sample(const void* logits, int lfmt, int rows, int64_t n, int64_t ld,
@@ -718,7 +694,8 @@ extern "C" tfd_status tfd_sample(const void* logits, int lfmt, int rows, int64_t
   const int64_t nv = (n + ve - 1) / ve + 1;  // one more where a row starts off a 16-byte boundary
   const size_t fixed = (sizeof(Shared) + 15) / 16 * 16;
   const size_t room = 227 * 1024 - fixed;
-  const int sms = tfd_host::sm_count();
+  int dev = 0;
+  const int sms = tfd_host::device_sms(dev);
   int c = 1;
   while (c < kMaxC && n / c > 2048 && ((int64_t)rows * c * 2 <= sms || nv / c * 16 > 100 * 1024))
     c *= 2;
@@ -728,8 +705,12 @@ extern "C" tfd_status tfd_sample(const void* logits, int lfmt, int rows, int64_t
   Args a = {logits, n, ld, temperature, top_k, top_p, min_p, u, id_map, ids, prob, ldt, probs, ldp,
             dev_status};
   cudaStream_t st = tfd_host::as_stream(stream);
-  if (bf16)
-    return keep ? launch<true, true>(a, rows, c, smem, st) : launch<true, false>(a, rows, c, smem, st);
-  return keep ? launch<false, true>(a, rows, c, smem, st)
-              : launch<false, false>(a, rows, c, smem, st);
+#define TFD_SAMPLE_CASE(B, K) \
+  if (bf16 == B && keep == K) \
+    return tfd_host::launch_clusters<sample_kernel<B, K>>(a, rows, c, kT, smem, \
+                                                          tfd_host::kSmemLimit, st);
+  TFD_SAMPLE_CASE(true, true) TFD_SAMPLE_CASE(true, false)
+  TFD_SAMPLE_CASE(false, true) TFD_SAMPLE_CASE(false, false)
+#undef TFD_SAMPLE_CASE
+  return TFD_ERR_UNSUPPORTED;
 }

@@ -88,8 +88,15 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
+# The raw handle of the current stream; building a Stream object costs microseconds a call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(_current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -326,11 +333,25 @@ def tfd_fp8_block32_relayout(codes, to_interleaved=True, out=None, stream=None):
     return out
 
 
-def _vec(t, dtype, count, name):
-    """A contiguous device vector (or matrix) of ``count`` elements of one type, or None."""
-    if t is not None and (t.dtype != dtype or not t.is_cuda or t.numel() != count or
-                          not t.is_contiguous()):
-        raise ValueError(f"{name}: a contiguous CUDA tensor of {count} {dtype} is wanted")
+def _vec(t, dtype, count, dev, name):
+    """A contiguous vector (or matrix) of ``count`` elements of one type on the device: its address
+    (None for None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() != count or t.get_device() != dev or \
+            not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor of {count} {dtype} on the current CUDA "
+                         "device is wanted")
+    return t.data_ptr()
+
+
+def _rows_of(t, rows, cols, dtype, dev, name):
+    """Row stride of a matrix [rows][cols] with contiguous columns on the device."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != (rows, cols) or \
+            (cols > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: {dtype} [{rows}][{cols}] with contiguous columns on the current "
+                         "CUDA device is wanted")
+    return t.stride(0) if rows > 1 else max(cols, t.stride(0))
 
 
 def tfd_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, id_map=None,
@@ -338,48 +359,41 @@ def tfd_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, 
                stream=None):
     """One token a row of logits [rows][>= n] (bf16 or float32), drawn with the random numbers
     u [rows] after temperature, top_k, top_p and min_p (each [rows] or None). ``ids`` [rows] may be
-    a column of a larger array (``prob`` then with the same stride); ``probs`` [rows][>= n] (or
+    a column of a larger array (``prob`` then with the same stride); ``probs`` [rows][n] (or
     want_probs) receives the filtered distribution. Returns (ids, prob, probs)."""
-    dev = logits.device
+    f32, i32, dev = torch.float32, torch.int32, _current_device()
     rows, cols = logits.shape
-    n = cols if n is None else n
-    if logits.dtype == torch.float32:
+    if logits.dtype is f32:
         fmt = X_F32
-    elif logits.dtype == torch.bfloat16:
+    elif logits.dtype is torch.bfloat16:
         fmt = X_BF16
     else:
         raise ValueError("logits: float32 or bfloat16 is wanted")
-    if not logits.is_cuda or logits.stride(1) != 1 and cols > 1 or n > cols:
-        raise ValueError("logits: CUDA rows of at least n contiguous columns are wanted")
-    _vec(u, torch.float32, rows, "u")
-    _vec(temperature, torch.float32, rows, "temperature")
-    _vec(top_k, torch.int32, rows, "top_k")
-    _vec(top_p, torch.float32, rows, "top_p")
-    _vec(min_p, torch.float32, rows, "min_p")
-    _vec(id_map, torch.int32, n, "id_map")
+    ld = _rows_of(logits, rows, cols, logits.dtype, dev, "logits")
+    n = cols if n is None else n
+    if n > cols:
+        raise ValueError("logits have fewer than n columns")
     if ids is None:
-        ids = torch.empty(rows, dtype=torch.int32, device=dev)
+        ids = torch.empty(rows, dtype=i32, device=logits.device)
         if prob is None:
-            prob = torch.empty(rows, dtype=torch.float32, device=dev)
-    if ids.dtype != torch.int32 or ids.shape != (rows,) or not ids.is_cuda:
-        raise ValueError("ids: a CUDA int32 vector of one id a row is wanted")
+            prob = torch.empty(rows, dtype=f32, device=logits.device)
+    if ids.dtype is not i32 or ids.shape != (rows,) or ids.get_device() != dev:
+        raise ValueError("ids: an int32 vector of one id a row is wanted")
     ldt = ids.stride(0) if rows > 1 else 1
-    if prob is not None and (prob.dtype != torch.float32 or prob.shape != (rows,) or
-                             not prob.is_cuda or (rows > 1 and prob.stride(0) != ldt)):
-        raise ValueError("prob: a CUDA float32 vector with the stride of ids is wanted")
+    if prob is not None and (prob.dtype is not f32 or prob.shape != (rows,) or
+                             prob.get_device() != dev or (rows > 1 and prob.stride(0) != ldt)):
+        raise ValueError("prob: a float32 vector with the stride of ids is wanted")
     if probs is None and want_probs:
-        probs = torch.empty((rows, n), dtype=torch.float32, device=dev)
-    ldp = 0
-    if probs is not None:
-        if probs.dtype != torch.float32 or not probs.is_cuda or probs.shape[0] != rows or \
-                probs.shape[1] < n or (probs.shape[1] > 1 and probs.stride(1) != 1):
-            raise ValueError("probs: CUDA float32 rows of at least n contiguous columns are wanted")
-        ldp = probs.stride(0) if rows > 1 else max(n, probs.stride(0))
-    st = library().tfd_sample(_p(logits), fmt, rows, n, logits.stride(0) if rows > 1 else
-                              max(n, logits.stride(0)), _p(temperature), _p(top_k), _p(top_p),
-                              _p(min_p), _p(u), _p(id_map), _p(ids), _p(prob), ldt, _p(probs), ldp,
-                              _p(dev_status), _stream(stream))
-    _check("tfd_sample", st)
+        probs = torch.empty((rows, n), dtype=f32, device=logits.device)
+    ldp = 0 if probs is None else _rows_of(probs, rows, n, f32, dev, "probs")
+    st = library().tfd_sample(
+        logits.data_ptr(), fmt, rows, n, ld, _vec(temperature, f32, rows, dev, "temperature"),
+        _vec(top_k, i32, rows, dev, "top_k"), _vec(top_p, f32, rows, dev, "top_p"),
+        _vec(min_p, f32, rows, dev, "min_p"), _vec(u, f32, rows, dev, "u"),
+        _vec(id_map, i32, n, dev, "id_map"), ids.data_ptr(), _p(prob), ldt, _p(probs), ldp,
+        _vec(dev_status, i32, 1, dev, "dev_status"), _stream(stream))
+    if st:
+        _check("tfd_sample", st)
     return ids, prob, probs
 
 
@@ -390,46 +404,37 @@ def tfd_accept_sampled(p, q, drafts, n_asked, u, u_next, q_map=None, n_kept=None
     target's p [streams][win + 1][n], with the random numbers u [streams][win], and the next token
     drawn with u_next [streams]. q_map [n] gives a token's column in q (-1: none). The streams and
     steps of p and q are contiguous but for the row stride. Returns (n_kept, next_ids, next_prob)."""
+    f32, i32, dev = torch.float32, torch.int32, _current_device()
     streams, win = drafts.shape
     n, nq = p.shape[2], q.shape[2]
+    lds = []
     for t, steps, name in ((p, win + 1, "p"), (q, win, "q")):
-        if t.dtype != torch.float32 or not t.is_cuda or t.shape[:2] != (streams, steps) or \
-                (t.shape[2] > 1 and t.stride(2) != 1) or \
-                (streams > 1 and t.stride(0) != steps * t.stride(1)):
-            raise ValueError(f"{name}: CUDA float32 [streams][{steps}][columns] with evenly spaced "
-                             "rows is wanted")
-    _vec(drafts, torch.int32, streams * win, "drafts")
-    _vec(n_asked, torch.int32, streams, "n_asked")
-    _vec(u, torch.float32, streams * win, "u")
-    _vec(u_next, torch.float32, streams, "u_next")
-    _vec(q_map, torch.int32, n, "q_map")
-    dev = p.device
+        cols = t.shape[2]
+        s0, s1, s2 = t.stride()
+        if t.dtype is not f32 or t.get_device() != dev or t.shape != (streams, steps, cols) or \
+                (cols > 1 and s2 != 1) or (streams > 1 and s0 != steps * s1):
+            raise ValueError(f"{name}: float32 [{streams}][{steps}][columns] with evenly spaced "
+                             "rows on the current CUDA device is wanted")
+        lds.append(max(cols, s1) if steps * streams == 1 else s1)
     if n_kept is None:
-        n_kept = torch.empty(streams, dtype=torch.int32, device=dev)
+        n_kept = torch.empty(streams, dtype=i32, device=p.device)
     if next_ids is None:
-        next_ids = torch.empty(streams, dtype=torch.int32, device=dev)
+        next_ids = torch.empty(streams, dtype=i32, device=p.device)
         if next_prob is None:
-            next_prob = torch.empty(streams, dtype=torch.float32, device=dev)
-    _vec(n_kept, torch.int32, streams, "n_kept")
-    _vec(next_ids, torch.int32, streams, "next_ids")
-    _vec(next_prob, torch.float32, streams, "next_prob")
-    _vec(asked_hist, torch.int64, win, "asked_hist")
-    _vec(kept_hist, torch.int64, win, "kept_hist")
-    st = library().tfd_accept_sampled(_p(p), max(n, p.stride(1)), _p(q), max(nq, q.stride(1)), n,
-                                      nq, _p(q_map), _p(drafts), _p(n_asked), _p(u), _p(u_next),
-                                      streams, win, _p(n_kept), _p(next_ids), _p(next_prob),
-                                      _p(asked_hist), _p(kept_hist), _p(dev_status),
-                                      _stream(stream))
-    _check("tfd_accept_sampled", st)
+            next_prob = torch.empty(streams, dtype=f32, device=p.device)
+    st = library().tfd_accept_sampled(
+        p.data_ptr(), lds[0], q.data_ptr(), lds[1], n, nq, _vec(q_map, i32, n, dev, "q_map"),
+        _vec(drafts, i32, streams * win, dev, "drafts"),
+        _vec(n_asked, i32, streams, dev, "n_asked"), _vec(u, f32, streams * win, dev, "u"),
+        _vec(u_next, f32, streams, dev, "u_next"), streams, win,
+        _vec(n_kept, i32, streams, dev, "n_kept"), _vec(next_ids, i32, streams, dev, "next_ids"),
+        _vec(next_prob, f32, streams, dev, "next_prob"),
+        _vec(asked_hist, torch.int64, win, dev, "asked_hist"),
+        _vec(kept_hist, torch.int64, win, dev, "kept_hist"),
+        _vec(dev_status, i32, 1, dev, "dev_status"), _stream(stream))
+    if st:
+        _check("tfd_accept_sampled", st)
     return n_kept, next_ids, next_prob
-
-
-def _rows_of(t, rows, cols, dtype, name):
-    """Row stride of a CUDA matrix [rows][>= cols] with contiguous columns."""
-    if t.dtype != dtype or not t.is_cuda or t.dim() != 2 or t.shape[0] != rows or \
-            t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name}: a CUDA {dtype} [{rows}][{cols}] with contiguous columns is wanted")
-    return t.stride(0) if rows > 1 else max(cols, t.stride(0))
 
 
 def tfd_lora(x, a, b, adapter_ids, base=None, y=None, scales=None, out_mode=OUT_BF16,
@@ -437,26 +442,27 @@ def tfd_lora(x, a, b, adapter_ids, base=None, y=None, scales=None, out_mode=OUT_
     """y[r] = base[r] + scales[i] * b[i] (a[i] x[r]), i = adapter_ids[r] (-1: none), for bf16 x
     [rows][k], a [adapters][rank][k], b [adapters][n][rank]. base (or None for zeros) and y have one
     type, float32 or bfloat16 (base's or y's, else out_mode); y may be base. Returns y."""
+    f32, bf, dev = torch.float32, torch.bfloat16, _current_device()
     rows, k = x.shape
-    na, rank, _ = a.shape
+    na, rank, ka = a.shape
     n = b.shape[1]
     like = y if y is not None else base
     if like is not None:
-        out_mode = OUT_F32 if like.dtype == torch.float32 else OUT_BF16
-    dt = torch.float32 if out_mode == OUT_F32 else torch.bfloat16
-    ldx = _rows_of(x, rows, k, torch.bfloat16, "x")
-    if a.shape[2] != k or b.shape != (na, n, rank):
+        out_mode = OUT_F32 if like.dtype is f32 else OUT_BF16
+    dt = f32 if out_mode == OUT_F32 else bf
+    if ka != k or b.shape != (na, n, rank):
         raise ValueError("a [adapters][rank][k] and b [adapters][n][rank] do not fit x")
-    _vec(a, torch.bfloat16, na * rank * k, "a")
-    _vec(b, torch.bfloat16, na * n * rank, "b")
-    _vec(adapter_ids, torch.int32, rows, "adapter_ids")
-    _vec(scales, torch.float32, na, "scales")
+    ldx = _rows_of(x, rows, k, bf, dev, "x")
     if y is None:
         y = torch.empty((rows, n), dtype=dt, device=x.device)
-    ldy = _rows_of(y, rows, n, dt, "y")
-    ldb = _rows_of(base, rows, n, dt, "base") if base is not None else 0
-    st = library().tfd_lora(_p(x), rows, k, ldx, _p(a), _p(b), na, rank, n, _p(adapter_ids),
-                            _p(scales), out_mode, _p(base), ldb, _p(y), ldy, _p(dev_status),
-                            _stream(stream))
-    _check("tfd_lora", st)
+    ldy = _rows_of(y, rows, n, dt, dev, "y")
+    ldb = 0 if base is None else _rows_of(base, rows, n, dt, dev, "base")
+    st = library().tfd_lora(
+        x.data_ptr(), rows, k, ldx, _vec(a, bf, na * rank * k, dev, "a"),
+        _vec(b, bf, na * n * rank, dev, "b"), na, rank, n,
+        _vec(adapter_ids, torch.int32, rows, dev, "adapter_ids"),
+        _vec(scales, f32, na, dev, "scales"), out_mode, _p(base), ldb, y.data_ptr(), ldy,
+        _vec(dev_status, torch.int32, 1, dev, "dev_status"), _stream(stream))
+    if st:
+        _check("tfd_lora", st)
     return y
