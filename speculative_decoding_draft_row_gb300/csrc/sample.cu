@@ -2,20 +2,24 @@
 // top-k, top-p and min-p, optionally with the whole filtered distribution.
 //
 // Weights are exact integers (weight.cuh), so a row's sums are the same in any order. One
-// thread-block cluster takes a row, each block a contiguous part of its columns, each warp a
-// contiguous part of the block's. The steps, with a cluster barrier after each of 1 to 4:
-//  1. the row's largest and smallest finite logit;
-//  2. with top-k or top-p: a histogram of the columns over log2 of their weight (2048 bins from
-//     the largest down to the smallest or to the 2^-44 cut; counts, and masses where top-p asks);
-//  3. the blocks' histograms summed, an eighth of the bins or so by each block, into every block;
-//  4. the bin in which the border falls is found by each block on its own; the columns above it
-//     are kept for certain and their mass summed per warp, the few columns inside it are sent to
-//     every block, which ranks them and knows the last kept (value, id) key;
-//  5. every block knows all blocks' kept masses, so the one that holds the drawn column finds its
-//     warp, and that warp scans its columns for it.
-// A bin with more columns than the candidate list holds is split again by the columns' 64-bit keys
-// until it fits (equal logits differ by their ids, so this ends). Without top-k and top-p steps 2
-// and 3 fall away.
+// thread-block cluster takes a row, each block a contiguous part of its columns (kept in shared
+// memory where they fit), each warp a contiguous part of the block's. After the row's largest logit
+// (one cluster barrier) a row goes one of three ways:
+//  A. no top-k, no top-p: every warp sums its weights (those that min_p keeps); one barrier.
+//  B. top-k up to the list's length: the k-th largest of the threads' own maxima bounds the k-th
+//     largest logit from below (k threads each hold a logit at least that large). A histogram of
+//     the maxima over log2 of the weight finds a bin edge under it, and only the threads whose
+//     maximum reaches the edge look through their columns again; little more than k columns go to
+//     every block's list, and each block resolves top-k and top-p on the list alone.
+//  C. top-p alone (or what B cannot hold): the histogram takes every column's weight, as three
+//     integer pieces that shared-memory adds without a carry; the bin in which the border falls is
+//     found, its columns go to the lists, and each block resolves the border on its list. A bin
+//     with more columns than the list is split again by the columns' 64-bit (value, id) keys until
+//     it fits (equal logits differ by their ids, so this ends).
+// The blocks' kept masses then name the block that holds the drawn column, which finds the warp,
+// which scans its columns. The histogram is summed across the cluster through distributed shared
+// memory, a share of the bins by each block, into every block, so the steps behind it are done by
+// each block for itself and need no further barrier.
 #include <cooperative_groups.h>
 
 #include "launch.cuh"
@@ -28,10 +32,12 @@ namespace cg = cooperative_groups;
 
 constexpr int kT = 512;
 constexpr int kW = kT / 32;
-constexpr int kBins = 2048;
+constexpr int kBins = 1024;
 constexpr int kPer = kBins / kT;
-constexpr int kCand = 256;
+constexpr int kList = 1024;      // columns of a list
+constexpr int kRank = 128;       // lists up to here are ranked outright
 constexpr int kMaxC = 16;
+constexpr int kMaxPart = 65536;  // columns of a block, or a few more: 15-bit pieces sum within 32 bits
 
 struct Args {
   const void* logits;
@@ -50,33 +56,40 @@ struct Args {
   int32_t* dev_status;
 };
 
-struct Shared {
-  unsigned long long tab[128];
-  uint32_t cnt[kBins], mlo[kBins], mhi[kBins];  // this block's histogram
-  uint32_t rcnt[kBins];                         // the row's
-  uint64_t rmass[kBins];
-  uint64_t ckey[2][kCand], cw[2][kCand];  // candidates of the border bin, in every block
-  uint32_t ccol[2][kCand];
-  uint32_t ccount[2];                     // rank 0: candidates appended
-  float cmax[kMaxC], cmin[kMaxC];
-  uint64_t cdef[2][kMaxC];                // mass of each block's columns above the border bin
-  uint64_t klo[kMaxC], khi[kMaxC];
-  uint64_t wdef[kW];                      // the same of this block's warps
-  uint64_t cmass[kMaxC];
-  uint64_t w64[kW];
-  uint32_t w32[kW];
-  float wmax[kW], wmin[kW];
-  uint64_t f_above_m, f_in_m, tkey, zk;
-  uint32_t f_bin, f_above_n, f_in_n;
+// A sum of weights in three pieces (bits 0-14, 15-29, 30-43), for adds without carries.
+struct Pieces {
+  uint32_t lo[kBins], mid[kBins], top[kBins];
 };
 
-// The border of a filter: columns in bins below `bin` (higher weights) are kept for certain, and
-// of `bin` itself those with a key above khi; keys in [klo, khi] are undecided.
+struct Shared {
+  unsigned long long tab[128];
+  uint32_t cnt[kBins];  // this block's histogram: columns, and their weights
+  Pieces w;
+  uint32_t rcnt[kBins];  // the row's
+  uint64_t rmass[kBins];
+  uint64_t lent[kList];           // the list, in every block: logit bits, column
+  uint64_t lkey[kList], lw[kList];  // its keys (own columns on their way out before that), weights
+  uint16_t lmem[kList];           // entries of the list's border bin
+  uint32_t ltotal[2];             // columns sent to this block's list
+  float4 cext[kMaxC];             // every block's largest and smallest logit, smallest thread maximum
+  uint64_t cdef[2][kMaxC];        // every block's mass above the border bin
+  uint64_t klo[kMaxC], khi[kMaxC];
+  uint64_t wsum[kW];              // this block's warps
+  uint64_t w64[kW], x64[kW];
+  uint32_t w32[kW];
+  float wext[3][kW];
+  uint32_t cw3[3][kMaxC], ww3[3][kW];  // kept list columns' masses by block and by warp, in pieces
+  uint64_t f_above_m, f_in_m, tkey, zk;
+  uint32_t f_bin, f_above_n, f_in_n, n_out, base, n_mem;
+};
+
+// The border of a filter: columns in bins below `bin` (higher weights) are kept for certain, and of
+// `bin` itself those with a key above khi; keys in [klo, khi] are undecided.
 struct Border {
   int bin;
   uint64_t klo, khi;
   uint32_t n_above, n_in;
-  uint64_t m_above, m_in;
+  uint64_t m_above;
 };
 
 __device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
@@ -95,8 +108,8 @@ struct Sampler {
   const int tid = threadIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int C, rank, row, off, n, nvc, nvw, vcta, vbeg, vend;
   const char* base;
-  // the row's parameters
-  float m, binscale, minp;
+  float m, binscale, lfloor;  // largest logit; bins per unit of log2; no logit below has a say
+  bool inf;                   // the largest logit is +inf
   Scale sc;
   uint64_t minw;
 
@@ -105,6 +118,7 @@ struct Sampler {
     rank = (int)cl.block_rank();
     row = blockIdx.x / C;
     n = (int)a.n;
+    inf = false;
     const int es = BF16 ? 2 : 4;
     const char* p = (const char*)a.logits + (int64_t)row * a.ld * es;
     off = (int)((uintptr_t)p & 15) / es;
@@ -137,7 +151,21 @@ struct Sampler {
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
-  __device__ __forceinline__ uint4 get(int v) const { return KEEP ? keep[v - vcta] : load(v); }
+  __device__ __forceinline__ uint4 get(int v) const {
+    if (KEEP) return keep[v - vcta];
+    const uint4 r = load(v);
+    return inf ? only_inf(r) : r;
+  }
+  // +inf -> 0, all else -> NaN: where the largest logit is +inf, the +inf columns share the mass
+  __device__ static uint4 only_inf(const uint4& r) {
+    uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] = BF16 ? (((w[j] & 0xFFFFu) == 0x7F80u ? 0u : 0x7FC0u) |
+                     ((w[j] >> 16) == 0x7F80u ? 0u : 0x7FC00000u))
+                  : (w[j] == 0x7F800000u ? 0u : 0x7FC00000u);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
   __device__ __forceinline__ static float elem(const uint4& r, int j) {
     if (BF16) {
       const uint32_t w = (j >> 1) == 0 ? r.x : (j >> 1) == 1 ? r.y : (j >> 1) == 2 ? r.z : r.w;
@@ -153,27 +181,41 @@ struct Sampler {
       for (int j = 0; j < VE; ++j) f(v * VE + j - off, elem(r, j));
     }
   }
+  // f(column, logit) for the columns whose logit is in [lo, hi]
+  template <class F>
+  __device__ __forceinline__ void each_in(float lo, float hi, F f) const {
+    for (int v = vbeg + lane; v < vend; v += 32) {
+      const uint4 r = get(v);
+#pragma unroll
+      for (int j = 0; j < VE; ++j) {
+        const float l = elem(r, j);
+        if (l >= lo && l <= hi) f(v * VE + j - off, l);
+      }
+    }
+  }
 
   __device__ __forceinline__ float lead(float l) const { return lead_log2(l, m, sc); }
+  __device__ __forceinline__ float place(float ph) const { return -ph * binscale; }
   __device__ __forceinline__ int bin_of(float ph) const {
-    return min(kBins - 1, (int)(-ph * binscale));
+    return min(kBins - 1, (int)place(ph));
   }
-  __device__ __forceinline__ uint64_t weight(float l, float ph) const {
-    int e;
-    const uint64_t t = weight_mant(l, m, sc, ph, sh.tab, e);
-    return weight_fix(t, e);
+  // A logit whose lead_log2 is about ph, less (or more) than its rounding can make.
+  __device__ __forceinline__ float logit_at(float ph, bool below) const {
+    const float d = ph / sc.hi, slack = (fabsf(m) + fabsf(d)) * 1e-6f;
+    if (!(d > -3e38f)) return below ? -INFINITY : m;
+    return below ? m + d - slack : m + d + slack;
+  }
+  __device__ __forceinline__ uint64_t weight(float l) const {
+    return weight_of(l, m, sc, sh.tab);
   }
   __device__ __forceinline__ uint64_t key_of(float l, int col) const {
     return make_key(l, a.id_map ? a.id_map[col] : col);
   }
-  __device__ __forceinline__ bool at_least(float l, int col, uint64_t tkey) const {
-    const uint32_t vk = value_key(l), th = (uint32_t)(tkey >> 32);
-    return vk != th ? vk > th : key_of(l, col) >= tkey;
-  }
 
-  __device__ void extremes(float& mn) {
+  // The row's largest logit, smallest finite one, and smallest thread maximum; each thread's own.
+  __device__ void extremes(float& mn, float& mt, float& own) {
     float mx = -INFINITY;
-    mn = INFINITY;
+    mn = mt = INFINITY;
     for (int v0 = vbeg + lane; v0 < vend; v0 += 128) {
       uint4 r[4];
 #pragma unroll
@@ -187,87 +229,135 @@ struct Sampler {
           for (int j = 0; j < VE; ++j) {
             const float x = elem(r[q], j);
             mx = fmaxf(mx, x);  // fmaxf and fminf pass NaN over
-            if (x > -INFINITY) mn = fminf(mn, x);
+            mn = fminf(mn, x == -INFINITY ? INFINITY : x);
           }
         }
     }
+    own = mx;
+    if (mx > -INFINITY) mt = mx;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+      mt = fminf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
     }
     if (lane == 0) {
-      sh.wmax[warp] = mx;
-      sh.wmin[warp] = mn;
+      sh.wext[0][warp] = mx;
+      sh.wext[1][warp] = mn;
+      sh.wext[2][warp] = mt;
     }
     __syncthreads();
-    if (tid < C) {  // the other blocks run: barrier of the constructor's caller
-      for (int w = 0; w < kW; ++w) {
-        mx = fmaxf(mx, sh.wmax[w]);
-        mn = fminf(mn, sh.wmin[w]);
+    cl.barrier_wait();  // every block runs and has cleared its counters
+    if (warp == 0) {
+      const int w = lane & (kW - 1);
+      mx = sh.wext[0][w];
+      mn = sh.wext[1][w];
+      mt = sh.wext[2][w];
+#pragma unroll
+      for (int o = kW / 2; o > 0; o >>= 1) {
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+        mt = fminf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
       }
-      *cl.map_shared_rank(&sh.cmax[rank], tid) = mx;
-      *cl.map_shared_rank(&sh.cmin[rank], tid) = mn;
+      if (lane < C) *cl.map_shared_rank(&sh.cext[rank], lane) = make_float4(mx, mn, mt, 0.0f);
     }
     cl.sync();
-    m = sh.cmax[0];
-    mn = sh.cmin[0];
+    float4 e = sh.cext[0];
     for (int c = 1; c < C; ++c) {
-      m = fmaxf(m, sh.cmax[c]);
-      mn = fminf(mn, sh.cmin[c]);
+      const float4 x = sh.cext[c];
+      e.x = fmaxf(e.x, x.x);
+      e.y = fminf(e.y, x.y);
+      e.z = fminf(e.z, x.z);
     }
+    m = e.x;
+    mn = e.y;
+    mt = e.z;
   }
 
-  __device__ __forceinline__ void hist_add(int b, uint64_t w, bool mass) {
-    atomicAdd(&sh.cnt[b], 1u);
-    if (mass) {  // a 64-bit sum in two words, the carry taken from the low word's old value
-      const uint32_t lo = (uint32_t)w;
-      const uint32_t old = atomicAdd(&sh.mlo[b], lo);
-      const uint32_t hi = (uint32_t)(w >> 32) + (old + lo < old ? 1u : 0u);
-      if (hi) atomicAdd(&sh.mhi[b], hi);
+  // ---- histogram ----------------------------------------------------------------------------
+  __device__ __forceinline__ void pieces_add(uint32_t* lo, uint32_t* mid, uint32_t* top,
+                                             uint64_t w) {
+    atomicAdd(lo, (uint32_t)w & 0x7FFFu);
+    atomicAdd(mid, ((uint32_t)w >> 15) & 0x7FFFu);
+    const uint32_t t = (uint32_t)(w >> 30);
+    if (t) atomicAdd(top, t);
+  }
+  __device__ __forceinline__ static uint64_t pieces(uint32_t lo, uint32_t mid, uint32_t top) {
+    return lo + ((uint64_t)mid << 15) + ((uint64_t)top << 30);
+  }
+  __device__ __forceinline__ void mass_add(int b, uint64_t w) {
+    pieces_add(&sh.w.lo[b], &sh.w.mid[b], &sh.w.top[b], w);
+  }
+  __device__ __forceinline__ uint64_t own_mass(int b) const {
+    return pieces(sh.w.lo[b], sh.w.mid[b], sh.w.top[b]);
+  }
+  __device__ void hist_zero() {  // the caller synchronises
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int b = tid + i * kT;
+      sh.cnt[b] = sh.w.lo[b] = sh.w.mid[b] = sh.w.top[b] = 0u;
     }
   }
-  __device__ void hist_zero() {
-    for (int b = tid; b < kBins; b += kT) sh.cnt[b] = sh.mlo[b] = sh.mhi[b] = 0u;
-    __syncthreads();
-  }
-  // The blocks' histograms summed into every block's rcnt, rmass.
-  __device__ void hist_sum() {
+  // The blocks' histograms summed into every block's rcnt, rmass: a share of the bins by each.
+  __device__ void hist_sum(bool count, bool mass) {
     cl.sync();
     const int per = kBins / C;
     for (int i = tid; i < per; i += kT) {
       const int b = rank * per + i;
-      uint32_t c = 0;
-      uint64_t w = 0;
-      for (int r = 0; r < C; ++r) {
-        c += *cl.map_shared_rank(&sh.cnt[b], r);
-        w += *cl.map_shared_rank(&sh.mlo[b], r) +
-             ((uint64_t)*cl.map_shared_rank(&sh.mhi[b], r) << 32);
+      if (count) {
+        uint32_t c = 0;
+#pragma unroll 4
+        for (int r = 0; r < C; ++r) c += *cl.map_shared_rank(&sh.cnt[b], r);
+        for (int r = 0; r < C; ++r) *cl.map_shared_rank(&sh.rcnt[b], r) = c;
       }
-      for (int r = 0; r < C; ++r) {
-        *cl.map_shared_rank(&sh.rcnt[b], r) = c;
-        *cl.map_shared_rank(&sh.rmass[b], r) = w;
+      if (mass) {
+        uint64_t lo = 0, mid = 0, top = 0;
+#pragma unroll 4
+        for (int r = 0; r < C; ++r) {
+          lo += *cl.map_shared_rank(&sh.w.lo[b], r);
+          mid += *cl.map_shared_rank(&sh.w.mid[b], r);
+          top += *cl.map_shared_rank(&sh.w.top[b], r);
+        }
+        const uint64_t w = lo + (mid << 15) + (top << 30);
+        for (int r = 0; r < C; ++r) *cl.map_shared_rank(&sh.rmass[b], r) = w;
       }
     }
     cl.sync();
   }
-  __device__ void hist_rows(bool mass) {
-    hist_zero();
-    each([&](int, float l) {
-      const float ph = lead(l);
-      if (alive(ph)) hist_add(bin_of(ph), mass ? weight(l, ph) : 0, mass);
-    });
-    hist_sum();
+  // The whole row's histogram.
+  __device__ void hist_row(bool count, bool mass) {
+    for (int v = vbeg + lane; v < vend; v += 32) {
+      const uint4 r = get(v);
+#pragma unroll
+      for (int j0 = 0; j0 < VE; j0 += 4) {
+        uint64_t w[4];
+        if (mass) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[j] = weight(elem(r, j0 + j));
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float ph = lead(elem(r, j0 + j));
+          if (alive(ph)) {
+            const int b = bin_of(ph);
+            if (count) atomicAdd(&sh.cnt[b], 1u);
+            if (mass) mass_add(b, w[j]);
+          }
+        }
+      }
+    }
+    hist_sum(count, mass);
   }
 
-  // The first bin at which the running count (or mass) from bin 0 reaches `target`; false if none.
-  __device__ bool find(uint64_t target, bool by_mass, uint32_t n0, uint64_t m0, Border& b) {
-    uint32_t c = 0;
-    uint64_t w = 0;
+  // The first bin at which the running count (or mass) from bin 0 on, n0 and m0 before it, reaches
+  // the target; kBins if none does.
+  __device__ int find(uint64_t target, bool by_mass, uint32_t n0, uint64_t m0) {
+    uint32_t cn[kPer], c = 0;
+    uint64_t wn[kPer], w = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      c += sh.rcnt[tid * kPer + i];
-      w += sh.rmass[tid * kPer + i];
+      c += cn[i] = sh.rcnt[tid * kPer + i];
+      w += wn[i] = sh.rmass[tid * kPer + i];
     }
     uint32_t ci = c;
     uint64_t wi = w;
@@ -280,7 +370,6 @@ struct Sampler {
         wi += y;
       }
     }
-    __syncthreads();
     if (tid == 0) sh.f_bin = kBins;
     if (lane == 31) {
       sh.w32[warp] = ci;
@@ -295,37 +384,149 @@ struct Sampler {
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const uint32_t cn = sh.rcnt[tid * kPer + i];
-      const uint64_t wn = sh.rmass[tid * kPer + i];
-      const uint64_t before = by_mass ? wb : cb, after = by_mass ? wb + wn : cb + cn;
+      const uint64_t before = by_mass ? wb : cb, after = by_mass ? wb + wn[i] : cb + cn[i];
       if (before < target && after >= target) {
         sh.f_bin = tid * kPer + i;
         sh.f_above_n = cb;
         sh.f_above_m = wb;
-        sh.f_in_n = cn;
-        sh.f_in_m = wn;
+        sh.f_in_n = cn[i];
+        sh.f_in_m = wn[i];
       }
-      cb += cn;
-      wb += wn;
+      cb += cn[i];
+      wb += wn[i];
     }
     __syncthreads();
-    b.bin = (int)sh.f_bin;
-    b.klo = 0;
-    b.khi = ~0ull;
-    b.n_above = sh.f_above_n;
-    b.m_above = sh.f_above_m;
-    b.n_in = sh.f_in_n;
-    b.m_in = sh.f_in_m;
-    return b.bin < kBins;
+    return (int)sh.f_bin;
+  }
+  __device__ void zero_counts() {  // rcnt or rmass where the histogram did not have them
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sh.rcnt[tid + i * kT] = 0u;
+    __syncthreads();
+  }
+  __device__ void zero_masses() {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sh.rmass[tid + i * kT] = 0u;
+    __syncthreads();
   }
 
+  // ---- the list -----------------------------------------------------------------------------
+  // Own columns for the list collect in lkey; n_out counts them.
+  __device__ __forceinline__ void list_add(int col, float l) {
+    const uint32_t slot = atomicAdd(&sh.n_out, 1u);
+    if (slot < (uint32_t)kList)
+      sh.lkey[slot] = ((uint64_t)__float_as_uint(l) << 32) | (uint32_t)col;
+  }
+  // Sends them, and this block's mass above the border, to every block. Returns the columns of the
+  // whole row, which are all in the list if they are at most kList. Ends in a cluster barrier.
+  __device__ uint32_t list_send(int buf, uint64_t mass) {
+    __syncthreads();
+    const uint32_t mine = sh.n_out;
+    if (tid < C) {
+      const uint32_t old = atomicAdd(cl.map_shared_rank(&sh.ltotal[buf], tid), mine);
+      if (tid == 0) sh.base = old;  // rank 0's order places the blocks' columns
+      *cl.map_shared_rank(&sh.cdef[buf][rank], tid) = mass;
+    }
+    __syncthreads();
+    const uint32_t at = sh.base, cnt = min(mine, (uint32_t)kList);
+    for (uint32_t i = tid; i < cnt * C; i += kT) {
+      const uint32_t e = i / C, r = i % C;
+      if (at + e < (uint32_t)kList) *cl.map_shared_rank(&sh.lent[at + e], r) = sh.lkey[e];
+    }
+    cl.sync();
+    if (tid == 0) sh.n_out = 0;
+    return sh.ltotal[buf];
+  }
+  // Keys and weights of the list.
+  __device__ void list_weigh(int cnt) {
+    for (int i = tid; i < cnt; i += kT) {
+      const uint64_t e = sh.lent[i];
+      const float l = __uint_as_float((uint32_t)(e >> 32));
+      sh.lkey[i] = key_of(l, (int)(uint32_t)e);
+      sh.lw[i] = weight(l);
+    }
+    __syncthreads();
+  }
+  // The last kept key among the list's columns (n0 columns of mass m0 rank above all of them): the
+  // target-th column, or the one at which the running mass reaches the target; and the mass up to
+  // and with it. t0 and mul spread the list's places in the histogram over the bins.
+  __device__ void list_border(int cnt, float t0, float mul, uint32_t n0, uint64_t m0,
+                              uint64_t target, bool by_mass) {
+    int mem = cnt;
+    uint32_t na = n0;
+    uint64_t ma = m0;
+    const bool split = cnt > kRank;
+    if (split) {
+      auto sub = [&](int i) {
+        const float l = __uint_as_float((uint32_t)(sh.lent[i] >> 32));
+        return max(0, min(kBins - 1, (int)((place(lead(l)) - t0) * mul)));
+      };
+      hist_zero();
+      if (tid == 0) sh.n_mem = 0;
+      __syncthreads();
+      for (int i = tid; i < cnt; i += kT) {
+        const int b = sub(i);
+        atomicAdd(&sh.cnt[b], 1u);
+        mass_add(b, sh.lw[i]);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int b = tid + i * kT;
+        sh.rcnt[b] = sh.cnt[b];
+        sh.rmass[b] = own_mass(b);
+      }
+      __syncthreads();
+      const int b = find(target, by_mass, n0, m0);
+      na = sh.f_above_n;
+      ma = sh.f_above_m;
+      for (int i = tid; i < cnt; i += kT)
+        if (sub(i) == b) sh.lmem[atomicAdd(&sh.n_mem, 1u)] = (uint16_t)i;
+      __syncthreads();
+      mem = (int)sh.n_mem;
+    }
+    // 2^g threads rank a column together
+    int g = 0;
+    while (g < 5 && (mem << (g + 1)) <= kT) ++g;
+    const int step = kT >> g, part = tid & ((1 << g) - 1);
+    for (int i0 = 0; i0 < mem; i0 += step) {
+      const int i = i0 + (tid >> g);
+      const int ii = i < mem ? (split ? sh.lmem[i] : i) : 0;
+      const uint64_t k = sh.lkey[ii], w = sh.lw[ii];
+      const uint32_t col = (uint32_t)sh.lent[ii];
+      uint32_t above = 0;
+      uint64_t before = 0;
+      for (int j = part; j < mem; j += 1 << g) {
+        const int jj = split ? sh.lmem[j] : j;
+        const uint64_t kj = sh.lkey[jj];
+        if (kj > k || (kj == k && (uint32_t)sh.lent[jj] < col)) {
+          ++above;
+          before += sh.lw[jj];
+        }
+      }
+      for (int o = 1; o < (1 << g); o <<= 1) {
+        above += __shfl_xor_sync(0xffffffffu, above, o);
+        before += __shfl_xor_sync(0xffffffffu, (unsigned long long)before, o);
+      }
+      above += na;
+      before += ma;
+      const bool hit = by_mass ? (before < target && before + w >= target)
+                               : (uint64_t)above + 1 == target;
+      if (hit && i < mem && part == 0) {
+        sh.tkey = k;
+        sh.zk = before + w;
+      }
+    }
+    __syncthreads();
+  }
+
+  // ---- way C: borders in the row's histogram --------------------------------------------------
   // Splits the border's bin by its columns' keys until the undecided columns fit the list, or have
-  // one key. Overwrites the histogram; returns whether it did.
-  __device__ bool refine(Border& b, uint64_t target, bool by_mass, bool mass) {
-    bool did = false;
+  // one key. Overwrites the histogram.
+  __device__ void refine(Border& b, uint64_t target, bool by_mass) {
     const int bin = b.bin;
-    while (b.n_in > kCand && b.klo < b.khi) {
-      did = true;
+    do {
       uint64_t lo = ~0ull, hi = 0;
       each([&](int col, float l) {
         const float ph = lead(l);
@@ -345,13 +546,13 @@ struct Sampler {
       __syncthreads();
       if (lane == 0) {
         sh.w64[warp] = lo;
-        sh.cmass[warp] = hi;  // free until the draw
+        sh.x64[warp] = hi;
       }
       __syncthreads();
       if (tid < C) {
         for (int w = 0; w < kW; ++w) {
           lo = min(lo, sh.w64[w]);
-          hi = max(hi, sh.cmass[w]);
+          hi = max(hi, sh.x64[w]);
         }
         *cl.map_shared_rank(&sh.klo[rank], tid) = lo;
         *cl.map_shared_rank(&sh.khi[rank], tid) = hi;
@@ -365,101 +566,107 @@ struct Sampler {
         hi = max(hi, sh.khi[c]);
       }
       const uint64_t span = hi - lo;
-      const int shift = max(0, 64 - __clzll((long long)span) - 11);  // (span >> shift) < 2048
+      const int shift = max(0, 64 - __clzll((long long)span) - 10);  // (span >> shift) < 1024
       each([&](int col, float l) {
         const float ph = lead(l);
         if (alive(ph) && bin_of(ph) == bin) {
           const uint64_t k = key_of(l, col);
-          if (k >= lo && k <= hi) hist_add((int)((hi - k) >> shift), mass ? weight(l, ph) : 0, mass);
+          if (k >= lo && k <= hi) {
+            const int s = (int)((hi - k) >> shift);
+            atomicAdd(&sh.cnt[s], 1u);
+            mass_add(s, weight(l));
+          }
         }
       });
-      hist_sum();
-      Border s;
-      find(target, by_mass, b.n_above, b.m_above, s);
-      b.n_above = s.n_above;
-      b.m_above = s.m_above;
-      b.n_in = s.n_in;
-      b.m_in = s.m_in;
-      b.khi = hi - ((uint64_t)s.bin << shift);
+      hist_sum(true, true);
+      const int s = find(target, by_mass, b.n_above, b.m_above);
+      b.n_above = sh.f_above_n;
+      b.m_above = sh.f_above_m;
+      b.n_in = sh.f_in_n;
+      b.khi = hi - ((uint64_t)s << shift);
       const uint64_t width = (1ull << shift) - 1;
       b.klo = b.khi - lo < width ? lo : b.khi - width;
-    }
-    b.bin = bin;
-    return did;
+      if (b.n_in > (uint32_t)kList && b.klo == b.khi && tid == 0) {  // one key: all of it is kept
+        sh.tkey = b.klo;
+        sh.zk = b.m_above + sh.f_in_m;
+      }
+    } while (b.n_in > (uint32_t)kList && b.klo < b.khi);
+    __syncthreads();
   }
 
-  // Sums the kept-for-certain columns' masses and sends the undecided ones to every block.
-  __device__ void gather(int buf, const Border& b) {
-    const bool collapsed = b.n_in > kCand;  // one key: all of it is kept
+  // The border at `target` in the row's histogram (which has what it needs), and then in its bin:
+  // leaves tkey, zk; returns the columns in the list. cdef[buf] has the blocks' masses above it
+  // as far as min_p keeps them.
+  __device__ int row_border(int buf, uint64_t target, bool by_mass, bool mass) {
+    Border b;
+    b.bin = find(target, by_mass, 0, 0);
+    b.klo = 0;
+    b.khi = ~0ull;
+    b.n_above = sh.f_above_n;
+    b.m_above = sh.f_above_m;
+    // this block's mass above: from its histogram, or column by column where min_p has a say
     uint64_t sum = 0;
-    each([&](int col, float l) {
+    const bool from_hist = mass && minw == 0;
+    if (from_hist)
+      for (int i = tid; i < b.bin; i += kT) sum += own_mass(i);
+    const float lo = logit_at(-(float)(b.bin + 1) / binscale, true);
+    const float hi = from_hist ? logit_at(-(float)b.bin / binscale, false) : INFINITY;
+    each_in(b.bin == kBins - 1 ? -INFINITY : lo, hi, [&](int col, float l) {
       const float ph = lead(l);
       if (!alive(ph)) return;
       const int bn = bin_of(ph);
-      if (bn > b.bin) return;
-      const uint64_t w = weight(l, ph);
-      uint64_t k = 0;
-      bool sure = bn < b.bin;
-      if (!sure) {
-        k = key_of(l, col);
-        if (k < b.klo) return;
-        sure = collapsed || k > b.khi;
-      }
-      if (sure) {
+      if (bn == b.bin) list_add(col, l);
+      if (!from_hist && bn < b.bin) {
+        const uint64_t w = weight(l);
         if (w >= minw) sum += w;
-        return;
-      }
-      const uint32_t slot = atomicAdd(cl.map_shared_rank(&sh.ccount[buf], 0), 1u);
-      for (int r = 0; r < C; ++r) {
-        *cl.map_shared_rank(&sh.ckey[buf][slot], r) = k;
-        *cl.map_shared_rank(&sh.cw[buf][slot], r) = w;
-        *cl.map_shared_rank(&sh.ccol[buf][slot], r) = (uint32_t)col;
       }
     });
-    sum = warp_sum64(sum);
-    if (lane == 0) sh.wdef[warp] = sum;
-    __syncthreads();
-    if (tid < C) {
-      uint64_t t = 0;
-      for (int w = 0; w < kW; ++w) t += sh.wdef[w];
-      *cl.map_shared_rank(&sh.cdef[buf][rank], tid) = t;
+    uint32_t cnt = list_send(buf, block_sum(sum));
+    if (cnt <= (uint32_t)kList) {
+      list_weigh((int)cnt);
+      list_border((int)cnt, (float)b.bin, (float)kBins, b.n_above, b.m_above, target, by_mass);
+      return (int)cnt;
     }
-    cl.sync();
+    // too many: split the bin, then send what is left of it
+    refine(b, target, by_mass);
+    const bool one_key = b.n_in > (uint32_t)kList;
+    sum = 0;
+    each([&](int col, float l) {
+      const float ph = lead(l);
+      if (!alive(ph) || bin_of(ph) > b.bin) return;
+      bool sure = bin_of(ph) < b.bin;
+      if (!sure) {
+        const uint64_t k = key_of(l, col);
+        if (k < b.klo) return;
+        sure = one_key || k > b.khi;
+      }
+      if (!sure) {
+        list_add(col, l);
+      } else {
+        const uint64_t w = weight(l);
+        if (w >= minw) sum += w;
+      }
+    });
+    __syncthreads();
+    if (tid == 0) sh.ltotal[buf] = 0;
+    cl.sync();  // every block has cleared its total and is done with the first list
+    cnt = list_send(buf, block_sum(sum));
+    if (one_key) return 0;
+    list_weigh((int)cnt);
+    list_border((int)cnt, (float)b.bin, (float)kBins, b.n_above, b.m_above, target, by_mass);
+    return (int)cnt;
   }
 
-  // The last kept key among the candidates: the need-th column, or the one whose running mass
-  // reaches the target. Also the mass up to and with it.
-  __device__ void resolve(int buf, const Border& b, uint64_t target, bool by_mass) {
-    if (b.n_in > kCand) {
-      __syncthreads();
-      if (tid == 0) {
-        sh.tkey = b.klo;
-        sh.zk = b.m_above + b.m_in;
-      }
-      __syncthreads();
-      return;
-    }
+  // Sum over the block, in every thread; the warps' sums stay in wsum.
+  __device__ uint64_t block_sum(uint64_t v) {
+    v = warp_sum64(v);
     __syncthreads();
-    for (int i = tid; i < (int)b.n_in; i += kT) {
-      const uint64_t k = sh.ckey[buf][i], w = sh.cw[buf][i];
-      const uint32_t col = sh.ccol[buf][i];
-      uint32_t above = b.n_above;
-      uint64_t before = b.m_above;
-      for (int j = 0; j < (int)b.n_in; ++j) {
-        const uint64_t kj = sh.ckey[buf][j];
-        if (kj > k || (kj == k && sh.ccol[buf][j] < col)) {
-          ++above;
-          before += sh.cw[buf][j];
-        }
-      }
-      const bool hit = by_mass ? (before < target && before + w >= target)
-                               : (uint64_t)above + 1 == target;
-      if (hit) {
-        sh.tkey = k;
-        sh.zk = before + w;
-      }
-    }
+    if (lane == 0) sh.wsum[warp] = v;
     __syncthreads();
+    uint64_t t = 0;
+#pragma unroll
+    for (int w = 0; w < kW; ++w) t += sh.wsum[w];
+    return t;
   }
 
   __device__ void nothing() {  // no column to draw from, or bad parameters
@@ -475,125 +682,216 @@ struct Sampler {
 
   __device__ void run() {
     if (tid < 128) sh.tab[tid] = kExp2Table[tid];
-    if (tid < 2) sh.ccount[tid] = 0;
+    if (tid < 2) sh.ltotal[tid] = 0;
+    if (tid == 2) sh.n_out = 0;
+    hist_zero();
+    cl.barrier_arrive();  // waited for in extremes()
     float t = a.temperature ? a.temperature[row] : 1.0f;
     int k = a.top_k ? a.top_k[row] : 0;
     const float p = a.top_p ? a.top_p[row] : 1.0f;
-    minp = a.min_p ? a.min_p[row] : 0.0f;
+    const float minp = a.min_p ? a.min_p[row] : 0.0f;
     const float u = a.u[row];
     const bool good = t >= 0.0f && t < INFINITY && p == p && minp == minp && u >= 0.0f && u < 1.0f;
     if (t == 0.0f) {
       t = 1.0f;
       k = 1;
     }
-    cl.sync();  // every block runs and has cleared its counters
-    float mn;
-    extremes(mn);
+    float mn, mt, own;
+    extremes(mn, mt, own);
     if (!good && rank == 0 && tid == 0) set_dev_status(a.dev_status, TFD_ERR_DEVICE_DATA);
     if (!good || m == -INFINITY) {
       nothing();
       return;
     }
+    if (m == INFINITY) {
+      inf = true;
+      m = mn = 0.0f;
+      mt = 0.0f;
+      own = own == INFINITY ? 0.0f : -INFINITY;
+      if (KEEP)
+        for (int v = vbeg + lane; v < vend; v += 32) keep[v - vcta] = only_inf(keep[v - vcta]);
+    }
     sc = scale_of(t);
-    minw = __float2ull_ru(fminf(fmaxf(minp, 0.0f), 1.0f) * 8796093022208.0f);
+    const float mp = fminf(fmaxf(minp, 0.0f), 1.0f);
+    minw = __float2ull_ru(mp * 8796093022208.0f);
+    lfloor = logit_at(fmaxf(kCutLog2, minw ? __log2f(mp) - 1e-3f : kCutLog2), true);
     const bool use_k = k > 0 && k < n, use_p = p < 1.0f;
     uint64_t tkey = 0;
     int buf = 0, ncand = 0;
-    if (use_k || use_p) {
-      const float span = fminf(-lead(mn) * 1.0001f, -kCutLog2 + 0.01f);
+    bool all_listed = false;  // every kept column is in the list
+
+    auto p_target = [&](uint64_t z) {
+      return max((uint64_t)1, mul_frac(fmaxf(p, 0.0f), z, true));
+    };
+    auto spread = [&](float lowest) {  // bins from the largest logit down to this one or the cut
+      const float span = fminf(-lead(lowest) * 1.0001f, -kCutLog2 + 0.01f);
       binscale = (float)kBins / fmaxf(span, 1e-30f);
-      hist_rows(use_p);
-      Border bk, bp;
-      bool gathered = false, dirty = false;
-      uint64_t zk = 0;
-      if (use_k && find((uint64_t)k, false, 0, 0, bk)) {
-        dirty = refine(bk, (uint64_t)k, false, use_p);
-        gather(0, bk);
-        resolve(0, bk, (uint64_t)k, false);
+    };
+
+    bool open = use_k || use_p;  // a filter is left to resolve
+    if (use_k && k <= kList && (int64_t)k <= (int64_t)kT * C) {
+      spread(mt);
+      const float ph = lead(own);
+      const int mine = alive(ph) ? bin_of(ph) : kBins;
+      if (mine < kBins) atomicAdd(&sh.cnt[mine], 1u);
+      hist_sum(true, false);
+      zero_masses();
+      const int b = find((uint64_t)k, false, 0, 0);
+      if (b < kBins) {
+        if (mine <= b)
+          for (int v = vbeg + lane; v < vend; v += 32) {
+            const uint4 r = get(v);
+#pragma unroll
+            for (int j = 0; j < VE; ++j) {
+              const float l = elem(r, j), q = lead(l);
+              if (alive(q) && bin_of(q) <= b) list_add(v * VE + j - off, l);
+            }
+          }
+        const uint32_t cnt = list_send(0, 0);
+        if (cnt <= (uint32_t)kList) {
+          ncand = (int)cnt;
+          list_weigh(ncand);
+          const float mul = (float)kBins / (float)(b + 1);
+          list_border(ncand, 0.0f, mul, 0, 0, (uint64_t)k, false);
+          if (use_p) list_border(ncand, 0.0f, mul, 0, 0, p_target(sh.zk), true);
+          tkey = sh.tkey;
+          all_listed = true;
+          open = false;
+        }
+      }
+      if (open) {  // the columns' own histogram, from scratch
+        buf = 1;
+        __syncthreads();
+        hist_zero();
+        __syncthreads();
+      }
+    }
+    if (open) {
+      spread(mn);
+      hist_row(use_k, use_p);
+      if (!use_k) zero_counts();
+      if (!use_p) zero_masses();
+      uint32_t total = 0;
+      uint64_t z = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        total += sh.rcnt[tid * kPer + i];
+        z += sh.rmass[tid * kPer + i];
+      }
+      z = block_sum(z);
+      total = (uint32_t)block_sum(total);
+      const bool by_k = use_k && total > (uint32_t)k;
+      if (by_k) {
+        ncand = row_border(buf, (uint64_t)k, false, use_p);
         tkey = sh.tkey;
-        zk = sh.zk;
-        gathered = true;
-        ncand = bk.n_in > kCand ? 0 : (int)bk.n_in;
-      } else if (use_p) {
-        uint64_t w = 0;
-        for (int i = 0; i < kPer; ++i) w += sh.rmass[tid * kPer + i];
-        w = warp_sum64(w);
-        __syncthreads();
-        if (lane == 0) sh.w64[warp] = w;
-        __syncthreads();
-        for (int q = 0; q < kW; ++q) zk += sh.w64[q];
+        z = sh.zk;
       }
       if (use_p) {
-        const uint64_t target = max((uint64_t)1, mul_frac(fmaxf(p, 0.0f), zk, true));
-        if (dirty) hist_rows(true);
-        find(target, true, 0, 0, bp);
-        const bool split = refine(bp, target, true, true);
-        if (!gathered || dirty || split || bp.bin != bk.bin) {
-          buf = gathered ? 1 : 0;
-          gather(buf, bp);
-          ncand = bp.n_in > kCand ? 0 : (int)bp.n_in;
+        if (by_k) {  // the lists and the histogram once more
+          __syncthreads();
+          hist_zero();
+          if (tid == 0) sh.ltotal[buf] = 0;
+          cl.sync();
+          hist_row(false, true);
+          zero_counts();
         }
-        resolve(buf, bp, target, true);
+        ncand = row_border(buf, p_target(z), true, true);
         tkey = sh.tkey;
-        gathered = true;
       }
-      if (!gathered) {
-        Border all = {kBins, 0, ~0ull, 0, 0, 0, 0};
-        gather(0, all);
+      open = by_k || use_p;
+    }
+    if (!all_listed && !open) {  // everything that min_p keeps
+      uint64_t sum = 0;
+      for (int v = vbeg + lane; v < vend; v += 32) {
+        const uint4 r = get(v);
+        bool any = false;
+#pragma unroll
+        for (int j = 0; j < VE; ++j) any |= elem(r, j) >= lfloor;
+        if (!any) continue;
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+          const uint64_t w = weight(elem(r, j));
+          sum += w >= minw ? w : 0;
+        }
       }
-    } else {
-      binscale = 0.0f;
-      Border all = {kBins, 0, ~0ull, 0, 0, 0, 0};
-      gather(0, all);
+      sum = block_sum(sum);
+      if (tid < C) *cl.map_shared_rank(&sh.cdef[buf][rank], tid) = sum;
+      cl.sync();
     }
 
-    // kept mass of every block, and of this block's warps
-    __syncthreads();
-    if (tid < C) sh.cmass[tid] = sh.cdef[buf][tid];
+    // the kept mass of every block, and of this block's warps
+    if (tid < kMaxC * 3) (&sh.cw3[0][0])[tid] = 0u;
+    if (tid < kW * 3) (&sh.ww3[0][0])[tid] = 0u;
     __syncthreads();
     for (int i = tid; i < ncand; i += kT) {
-      if (sh.ckey[buf][i] >= tkey && sh.cw[buf][i] >= minw) {
-        const int v = ((int)sh.ccol[buf][i] + off) / VE, c = v / nvc;
-        atomicAdd((unsigned long long*)&sh.cmass[c], (unsigned long long)sh.cw[buf][i]);
-        if (c == rank)
-          atomicAdd((unsigned long long*)&sh.wdef[(v - vcta) / nvw],
-                    (unsigned long long)sh.cw[buf][i]);
+      const uint64_t w = sh.lw[i];
+      if (sh.lkey[i] >= tkey && w >= minw) {
+        const int v = ((int)(uint32_t)sh.lent[i] + off) / VE, c = v / nvc;
+        pieces_add(&sh.cw3[0][c], &sh.cw3[1][c], &sh.cw3[2][c], w);
+        if (c == rank) {
+          const int q = (v - vcta) / nvw;
+          pieces_add(&sh.ww3[0][q], &sh.ww3[1][q], &sh.ww3[2][q], w);
+        }
       }
     }
     __syncthreads();
-    uint64_t z = 0;
-    for (int c = 0; c < C; ++c) z += sh.cmass[c];
+    uint64_t z = 0, before = 0, mine = 0;
+    for (int c = 0; c < C; ++c) {
+      const uint64_t x = (all_listed ? 0 : sh.cdef[buf][c]) +
+                         pieces(sh.cw3[0][c], sh.cw3[1][c], sh.cw3[2][c]);
+      if (c < rank) before += x;
+      if (c == rank) mine = x;
+      z += x;
+    }
     const uint64_t target = mul_frac(u, z, false);
     const float zf = 1.0f / (__ull2float_rn(z) * (1.0f / 8796093022208.0f));
-    uint64_t before = 0;
-    for (int c = 0; c < rank; ++c) before += sh.cmass[c];
-    if (target >= before && target < before + sh.cmass[rank]) {
-      for (int w = 0; w < warp; ++w) before += sh.wdef[w];
-      if (target >= before && target < before + sh.wdef[warp]) search(before, target, tkey, zf);
+    const float tval = tkey ? key_value(tkey) : -INFINITY;
+    lfloor = fmaxf(lfloor, tval);
+    if (target >= before && target < before + mine) {
+      if (open) {  // way C: the warps' kept masses, column by column
+        uint64_t sum = 0;
+        for (int v = vbeg + lane; v < vend; v += 32) sum += kept_weights(v, tval, tkey, nullptr);
+        block_sum(sum);
+      }
+      uint64_t w0 = before;
+      for (int w = 0; w < warp; ++w)
+        w0 += all_listed ? pieces(sh.ww3[0][w], sh.ww3[1][w], sh.ww3[2][w]) : sh.wsum[w];
+      const uint64_t ws =
+          all_listed ? pieces(sh.ww3[0][warp], sh.ww3[1][warp], sh.ww3[2][warp]) : sh.wsum[warp];
+      if (target >= w0 && target < w0 + ws) search(w0, target, tval, tkey, zf);
     }
-    if (a.probs) write_probs(tkey, zf);
+    if (a.probs) write_probs(tval, tkey, zf);
+  }
+
+  __device__ __forceinline__ bool above(float l, int col, float tval, uint64_t tkey) const {
+    return l > tval || (l == tval && key_of(l, col) >= tkey);
+  }
+  // The kept weights of 16 bytes of columns, and their sum.
+  __device__ __forceinline__ uint64_t kept_weights(int v, float tval, uint64_t tkey,
+                                                   uint64_t* w) const {
+    const uint4 r = get(v);
+    uint64_t sum = 0;
+#pragma unroll
+    for (int j = 0; j < VE; ++j) {
+      const float l = elem(r, j);
+      uint64_t x = 0;
+      if (l >= lfloor && above(l, v * VE + j - off, tval, tkey)) {
+        x = weight(l);
+        if (x < minw) x = 0;
+      }
+      if (w) w[j] = x;
+      sum += x;
+    }
+    return sum;
   }
 
   // One warp: the first of its columns whose running kept mass exceeds the target.
-  __device__ void search(uint64_t before, uint64_t target, uint64_t tkey, float zf) {
+  __device__ void search(uint64_t before, uint64_t target, float tval, uint64_t tkey, float zf) {
     for (int v0 = vbeg; v0 < vend; v0 += 32) {
       const int v = v0 + lane;
       uint64_t w[VE], sum = 0;
-      uint4 r = make_uint4(0, 0, 0, 0);
-      if (v < vend) r = get(v);
-#pragma unroll
-      for (int j = 0; j < VE; ++j) {
-        w[j] = 0;
-        if (v < vend) {
-          const float l = elem(r, j);
-          const float ph = lead(l);
-          if (alive(ph) && at_least(l, v * VE + j - off, tkey)) {
-            const uint64_t x = weight(l, ph);
-            if (x >= minw) w[j] = x;
-          }
-        }
-        sum += w[j];
-      }
+      if (v < vend) sum = kept_weights(v, tval, tkey, w);
+      if (!__any_sync(0xffffffffu, sum != 0)) continue;
       uint64_t incl = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -611,11 +909,10 @@ struct Sampler {
             if (!done && run > target) {
               done = true;
               const int col = v * VE + j - off;
-              const float l = elem(r, j);
-              int e;
-              const uint64_t mant = weight_mant(l, m, sc, lead(l), sh.tab, e);
+              const float l = elem(get(v), j);
               a.ids[(int64_t)row * a.ldt] = a.id_map ? a.id_map[col] : col;
-              if (a.prob) a.prob[(int64_t)row * a.ldt] = weight_float(mant, e) * zf;
+              if (a.prob)
+                a.prob[(int64_t)row * a.ldt] = weight_float(l, m, sc, lead(l)) * zf;
             }
           }
         }
@@ -625,7 +922,7 @@ struct Sampler {
     }
   }
 
-  __device__ void write_probs(uint64_t tkey, float zf) {
+  __device__ void write_probs(float tval, uint64_t tkey, float zf) {
     float* out = a.probs + (int64_t)row * a.ldp;
     const bool vec = (((uintptr_t)(out - off)) & 15) == 0;
     for (int v = vbeg + lane; v < vend; v += 32) {
@@ -634,12 +931,10 @@ struct Sampler {
 #pragma unroll
       for (int j = 0; j < VE; ++j) {
         const float l = elem(r, j);
-        const float ph = lead(l);
         q[j] = 0.0f;
-        if (alive(ph) && at_least(l, v * VE + j - off, tkey)) {
-          int e;
-          const uint64_t mant = weight_mant(l, m, sc, ph, sh.tab, e);
-          if (weight_fix(mant, e) >= minw) q[j] = weight_float(mant, e) * zf;
+        if (l >= lfloor && above(l, v * VE + j - off, tval, tkey)) {
+          const float ph = lead(l);
+          if (alive(ph) && (minw == 0 || weight(l) >= minw)) q[j] = weight_float(l, m, sc, ph) * zf;
         }
       }
       const int c0 = v * VE - off;
@@ -657,7 +952,7 @@ struct Sampler {
 };
 
 template <bool BF16, bool KEEP>
-__global__ void __launch_bounds__(kT) sample_kernel(const Args a) {
+__global__ void __launch_bounds__(kT, 2) sample_kernel(const Args a) {
   extern __shared__ __align__(16) unsigned char smem[];
   Shared& sh = *reinterpret_cast<Shared*>(smem);
   uint4* keep = reinterpret_cast<uint4*>(smem + ((sizeof(Shared) + 15) / 16) * 16);
@@ -691,23 +986,25 @@ extern "C" tfd_status tfd_sample(const void* logits, int lfmt, int rows, int64_t
   const char* p0 = (const char*)probs;
   if (probs && p0 < l1 && l0 < p0 + (((int64_t)rows - 1) * ldp + n) * 4) return TFD_ERR_INVALID;
 
+  // Blocks a row: until every SM has one, a block's columns leave room for two blocks an SM, or a
+  // block would have less than a few thousand columns.
   const int64_t nv = (n + ve - 1) / ve + 1;  // one more where a row starts off a 16-byte boundary
   const size_t fixed = (sizeof(Shared) + 15) / 16 * 16;
-  const size_t room = 227 * 1024 - fixed;
   int dev = 0;
   const int sms = tfd_host::device_sms(dev);
   int c = 1;
-  while (c < kMaxC && n / c > 2048 && ((int64_t)rows * c * 2 <= sms || nv / c * 16 > 100 * 1024))
+  auto part = [&](int blocks) { return (size_t)((nv + blocks - 1) / blocks + 1) * 16; };
+  while (c < kMaxC && ((n / c > 2048 && (int64_t)rows * c * 2 <= sms) ||
+                       fixed + part(c) > 112 * 1024 || n / c >= kMaxPart))
     c *= 2;
-  const size_t part = (size_t)((nv + c - 1) / c + 1) * 16;
-  const bool keep = part <= room;
-  const size_t smem = fixed + (keep ? part : 0);
+  const bool keep = fixed + part(c) <= (size_t)tfd_host::kSmemLimit;
+  const size_t smem = fixed + (keep ? part(c) : 0);
   Args a = {logits, n, ld, temperature, top_k, top_p, min_p, u, id_map, ids, prob, ldt, probs, ldp,
             dev_status};
   cudaStream_t st = tfd_host::as_stream(stream);
-#define TFD_SAMPLE_CASE(B, K) \
-  if (bf16 == B && keep == K) \
-    return tfd_host::launch_clusters<sample_kernel<B, K>>(a, rows, c, kT, smem, \
+#define TFD_SAMPLE_CASE(B, K)                                                           \
+  if (bf16 == B && keep == K)                                                           \
+    return tfd_host::launch_clusters<sample_kernel<B, K>>(a, rows, c, kT, smem,         \
                                                           tfd_host::kSmemLimit, st);
   TFD_SAMPLE_CASE(true, true) TFD_SAMPLE_CASE(true, false)
   TFD_SAMPLE_CASE(false, true) TFD_SAMPLE_CASE(false, false)

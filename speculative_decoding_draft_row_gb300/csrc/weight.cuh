@@ -6,7 +6,7 @@
 // 2^20 of them sum below 2^63). A drawn token changes where u * total falls within the error of the
 // running mass of a border between two tokens. With fp32 exponentials (2^-22 relative) over 163840
 // columns that is a row in a few dozen; here s is carried in two floats and 2^s to about 2^-39
-// relative, which makes it one in millions, for about 45 instructions an element. FP64 would do
+// relative, which makes it one in millions, for about 50 instructions an element. FP64 would do
 // too, but its rate here is 1/64 of FP32's.
 //
 // 2^s = 2^e * 2^(j/128) * 2^g with 128 s = 128 e + j + 128 g, |g| <= 2^-8: the table holds
@@ -49,64 +49,79 @@ __constant__ const unsigned long long kExp2Table[128] = {
     0xfd3e0c0cf48ull, 0xfe9e115c7b9ull,
 };
 
-// log2(e) / T in two floats.
+// log2(e) / T in two floats; T below 1e-30 counts as 1e-30 (the quotient has to be a float).
 struct Scale {
   float hi, lo;
 };
 __device__ __forceinline__ Scale scale_of(float t) {
   const float lh = 1.44269502e+00f, ll = 1.92596299e-08f;  // log2(e) = lh + ll to 2^-50
+  t = fmaxf(t, 1e-30f);
   Scale c;
   c.hi = __fdiv_rn(lh, t);
-  const float r = __fmaf_rn(-c.hi, t, lh) + ll;
-  c.lo = (c.hi < 3.0e38f) ? __fdiv_rn(r, t) : 0.0f;  // T too small for a float scale: hi decides
+  c.lo = __fdiv_rn(__fmaf_rn(-c.hi, t, lh) + ll, t);
   return c;
 }
 
 // The leading part of s, monotone in l (one subtraction, one product, both rounded): what bins and
-// the zero cut go by. l == m gives 0 also at m = +inf.
+// the zero cut go by.
 __device__ __forceinline__ float lead_log2(float l, float m, const Scale& c) {
-  return l == m ? 0.0f : __fmul_rn(__fsub_rn(l, m), c.hi);
+  return __fmul_rn(__fsub_rn(l, m), c.hi);
 }
 // Whether a column has a weight at all: NaN and what lies below the cut have none.
 __device__ __forceinline__ bool alive(float ph) { return ph >= kCutLog2; }
 
-// Weight of a column with lead_log2 ph >= kCutLog2, before the final shift: mantissa in
-// [2^43 (1 - 2^-8), 2^44) units and the exponent e <= 0.
-__device__ __forceinline__ uint64_t weight_mant(float l, float m, const Scale& c, float ph,
-                                                const unsigned long long* tab, int& e) {
-  // l - m in two floats (exact), times c in two floats
+// s = ph + pl: l - m in two floats (exact) times c in two floats. Finite for an alive column.
+__device__ __forceinline__ float tail_log2(float l, float m, const Scale& c, float ph) {
   const float dh = __fsub_rn(l, m);
   const float bb = __fsub_rn(dh, l);
   const float dl = __fsub_rn(__fsub_rn(l, __fsub_rn(dh, bb)), __fadd_rn(m, bb));
   float pl = __fmaf_rn(dh, c.hi, -ph);
   pl = __fmaf_rn(dh, c.lo, pl);
-  pl = __fmaf_rn(dl, c.hi, pl);
-  if (l == m) pl = 0.0f;
+  return __fmaf_rn(dl, c.hi, pl);
+}
+
+// The weight 2^(ph + pl) of an alive column before its final shift: the mantissa in
+// [2^43 (1 - 2^-8), 2^44) and the exponent e <= 0.
+__device__ __forceinline__ uint64_t weight_mant(float ph, float pl, const unsigned long long* tab,
+                                                int& e) {
   const float magic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an integer in the low bits
   const float kk = __fmaf_rn(ph, 128.0f, magic);
   const int ki = (int)(__float_as_uint(kk) - 0x4B400000u);
   const float kf = __fsub_rn(kk, magic);
   const float gh = __fmaf_rn(kf, -0.0078125f, ph);  // exact
   const float u = gh + pl;
-  const float t = u * u * (0.240226507f + u * (0.0555041087f + u * 0.00961812911f));
-  const float ln2h = 0.693147182f, ln2l = -1.90465421e-09f;
+  // 2^g - 1 in units of 2^-39 (the factors carry them), |.| < 2^31
+  const float unit = 549755813888.0f;
+  const float ln2h = 0.693147182f * unit, ln2l = -1.90465421e-09f * unit;
+  const float t =
+      u * u * (0.240226507f * unit + u * (0.0555041087f * unit + u * (0.00961812911f * unit)));
   const float a = __fmul_rn(gh, ln2h);
   float al = __fmaf_rn(gh, ln2h, -a);
   al = __fmaf_rn(gh, ln2l, al);
   al = __fmaf_rn(pl, ln2h, al);
-  // 2^g - 1 in units of 2^-39, |.| < 2^31
-  const int pi = __float2int_rn(a * 549755813888.0f) + __float2int_rn((al + t) * 549755813888.0f);
+  const float low = __fadd_rn(al + t, magic);  // |al + t| < 2^22
+  const int pi = __float2int_rn(a) + (int)(__float_as_uint(low) - 0x4B400000u);
   const unsigned long long tj = tab[ki & 127];
   e = ki >> 7;
   return tj + (uint64_t)(((int64_t)(int32_t)(uint32_t)((tj + 4096) >> 13) * (int64_t)pi) >> 26);
 }
 
-__device__ __forceinline__ uint64_t weight_fix(uint64_t mant, int e) {
-  return e == 0 ? mant : (mant + (1ull << (-e - 1))) >> -e;
+// The weight of any logit, without branches: 0 where it is not alive.
+__device__ __forceinline__ uint64_t weight_of(float l, float m, const Scale& c,
+                                              const unsigned long long* tab) {
+  const float ph = lead_log2(l, m, c);
+  const bool on = alive(ph);
+  const float pl = tail_log2(l, m, c, ph);
+  int e;
+  const uint64_t mant = weight_mant(on ? ph : 0.0f, on ? pl : 0.0f, tab, e);
+  const uint64_t w = (mant + ((1ull << -e) >> 1)) >> -e;
+  return on ? w : 0;
 }
-// The weight as a float (24 bits of it, also where the fixed-point form has fewer left).
-__device__ __forceinline__ float weight_float(uint64_t mant, int e) {
-  return __uint2float_rn((uint32_t)(mant >> 13)) * __uint_as_float((uint32_t)(127 + e - 30) << 23);
+// An alive column's weight as a float: the hardware's 2^x (2^-22 relative) of the leading part.
+__device__ __forceinline__ float weight_float(float l, float m, const Scale& c, float ph) {
+  float x;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(x) : "f"(ph));
+  return __fmaf_rn(x, tail_log2(l, m, c, ph) * 0.693147182f, x);
 }
 
 // ceil(f * z) and floor(f * z) for 0 <= f <= 1 in fp32 and z < 2^63, exact.
