@@ -281,6 +281,6 @@ extern "C" tfd_status tfd_accept_sampled(const float* p, int64_t ldp, const floa
   Args a = {p, ldp, q, ldq, n, nq, q_map, drafts, n_asked, u, u_next, win, n_kept, next_ids,
             next_prob, reinterpret_cast<unsigned long long*>(asked_hist),
             reinterpret_cast<unsigned long long*>(kept_hist), dev_status};
-  return tfd_host::launch_clusters<accept_sampled_kernel>(a, streams, c, kT, 0, 0,
+  return tfd_host::launch_clusters<accept_sampled_kernel>(a, dev, streams, c, kT, 0, 0,
                                                           tfd_host::as_stream(stream));
 }

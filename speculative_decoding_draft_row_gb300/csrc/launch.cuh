@@ -22,24 +22,59 @@ inline int device_sms(int& dev) {
   return n;
 }
 
-// Launches Kernel(args) on `clusters` clusters of c blocks. The first launch on a device allows the
-// kernel `max_smem` bytes of dynamic shared memory and clusters of up to 16 blocks there.
-template <auto Kernel, class Args>
-tfd_status launch_clusters(const Args& args, int64_t clusters, int c, int threads, size_t smem,
-                           int max_smem, cudaStream_t stream) {
-  static std::atomic<bool> ready[kMaxDevices];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return TFD_ERR_CUDA;
-  if (!ready[dev].load(std::memory_order_relaxed)) {
-    if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem) !=
-            cudaSuccess ||
-        cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
-            cudaSuccess) {
+// How many clusters of c blocks of a kernel run at once on the current device (asked of the runtime
+// once a device, for a launch with `smem` bytes): clusters do not cross the GPU's partitions of SMs,
+// so for large c it is well below (SMs * blocks an SM) / c (c = 16 at two blocks an SM: 14, not 19).
+constexpr int kMaxCluster = 16;
+template <auto Kernel>
+int clusters_at_once(int dev, int c, int threads, size_t smem) {
+  static std::atomic<int> count[kMaxDevices][kMaxCluster + 1];
+  if (dev < 0 || dev >= kMaxDevices) return 1;
+  int n = count[dev][c].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)c);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = c;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, Kernel, &cfg) != cudaSuccess) {
       cudaGetLastError();
-      return TFD_ERR_CUDA;
+      n = 0;
     }
-    ready[dev].store(true, std::memory_order_relaxed);
+    n = n > 0 ? n : 1;
+    count[dev][c].store(n, std::memory_order_relaxed);
   }
+  return n;
+}
+
+// The first use of a kernel on a device: allows it `max_smem` bytes of dynamic shared memory and
+// clusters of up to 16 blocks there.
+template <auto Kernel>
+bool allow_clusters(int dev, int max_smem) {
+  static std::atomic<bool> ready[kMaxDevices];
+  if (dev < 0 || dev >= kMaxDevices) return false;
+  if (ready[dev].load(std::memory_order_relaxed)) return true;
+  if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem) !=
+          cudaSuccess ||
+      cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+          cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  ready[dev].store(true, std::memory_order_relaxed);
+  return true;
+}
+
+// Launches Kernel(args) on `clusters` clusters of c blocks on the current device, `dev`.
+template <auto Kernel, class Args>
+tfd_status launch_clusters(const Args& args, int dev, int64_t clusters, int c, int threads,
+                           size_t smem, int max_smem, cudaStream_t stream) {
+  if (!allow_clusters<Kernel>(dev, max_smem)) return TFD_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(clusters * c));
   cfg.blockDim = dim3(threads);

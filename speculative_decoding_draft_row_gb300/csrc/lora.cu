@@ -360,12 +360,12 @@ __global__ void __launch_bounds__(kT, 2) lora_kernel(const Args a) {
 }
 
 template <int RT, int NT>
-tfd_status launch(const Args& a, int c, int64_t units, cudaStream_t stream) {
+tfd_status launch(const Args& a, int dev, int c, int64_t units, cudaStream_t stream) {
   constexpr int TM = 8 * NT, R = 16 * RT, RP = R + 4, HT = (TM + 15) / 16 * 16;
   size_t smem = (size_t)(kW + 1) * TM * RP * 4 + (size_t)3 * HT * (R + 8) * 2;
   const size_t counts = (size_t)4 * (a.rows <= kSmallRows ? kSmallRows : a.n_adapters + 1);
   if (smem < counts) smem = counts;
-  return tfd_host::launch_clusters<lora_kernel<RT, NT>>(a, units, c, kT, smem, 112 * 1024, stream);
+  return tfd_host::launch_clusters<lora_kernel<RT, NT>>(a, dev, units, c, kT, smem, 112 * 1024, stream);
 }
 
 }  // namespace
@@ -427,7 +427,7 @@ extern "C" tfd_status tfd_lora(const void* x, int rows, int64_t k, int64_t ldx, 
   const int64_t units = tiles * splits;
   if (units * c > 0x7fffffff) return TFD_ERR_UNSUPPORTED;
 #define TFD_LORA_CASE(RT, NT) \
-  if (rt == RT && nt == NT) return launch<RT, NT>(a, c, units, st);
+  if (rt == RT && nt == NT) return launch<RT, NT>(a, dev, c, units, st);
   TFD_LORA_CASE(1, 1) TFD_LORA_CASE(1, 2) TFD_LORA_CASE(1, 8)
   TFD_LORA_CASE(2, 1) TFD_LORA_CASE(2, 2) TFD_LORA_CASE(2, 8)
   TFD_LORA_CASE(4, 1) TFD_LORA_CASE(4, 2) TFD_LORA_CASE(4, 4)

@@ -73,6 +73,7 @@ struct Shared {
   uint32_t ltotal[2];             // columns sent to this block's list
   float4 cext[kMaxC];             // every block's largest and smallest logit, smallest thread maximum
   uint64_t cdef[2][kMaxC];        // every block's mass above the border bin
+  uint64_t ctail[kMaxC];          // and below the histogram
   uint64_t klo[kMaxC], khi[kMaxC];
   uint64_t wsum[kW];              // this block's warps
   uint64_t w64[kW], x64[kW];
@@ -106,9 +107,10 @@ struct Sampler {
   uint4* keep;  // this block's logits, where they fit
   cg::cluster_group cl = cg::this_cluster();
   const int tid = threadIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int C, rank, row, off, n, nvc, nvw, vcta, vbeg, vend;
+  int C, rank, row, off, n, nvc, nvw, vcta, vbeg, vend, nvrow;
   const char* base;
   float m, binscale, lfloor;  // largest logit; bins per unit of log2; no logit below has a say
+  float log2_minp;
   bool inf;                   // the largest logit is +inf
   Scale sc;
   uint64_t minw;
@@ -124,6 +126,7 @@ struct Sampler {
     off = (int)((uintptr_t)p & 15) / es;
     base = p - off * es;
     const int nv = (off + n + VE - 1) / VE;
+    nvrow = nv;
     nvc = (nv + C - 1) / C;
     nvw = (nvc + kW - 1) / kW;
     vcta = rank * nvc;
@@ -301,31 +304,38 @@ struct Sampler {
   // The blocks' histograms summed into every block's rcnt, rmass: a share of the bins by each.
   __device__ void hist_sum(bool count, bool mass) {
     cl.sync();
-    const int per = kBins / C;
-    for (int i = tid; i < per; i += kT) {
-      const int b = rank * per + i;
-      if (count) {
-        uint32_t c = 0;
-#pragma unroll 4
-        for (int r = 0; r < C; ++r) c += *cl.map_shared_rank(&sh.cnt[b], r);
-        for (int r = 0; r < C; ++r) *cl.map_shared_rank(&sh.rcnt[b], r) = c;
+    const int per = (kBins + C - 1) / C;
+    int g = 1;
+    while (4 * g <= C) g *= 2;
+    const int sub = tid & (g - 1);
+#pragma unroll 1
+    for (int i0 = 0; i0 < per; i0 += kT / g) {
+      const int i = i0 + tid / g, b = min(rank * per + i, kBins - 1);
+      uint32_t c = 0;
+      uint64_t w = 0;
+      for (int r = sub; r < C; r += g) {
+        const Shared* p = cl.map_shared_rank(&sh, r);
+        if (count) c += p->cnt[b];
+        if (mass) w += pieces(p->w.lo[b], p->w.mid[b], p->w.top[b]);
       }
-      if (mass) {
-        uint64_t lo = 0, mid = 0, top = 0;
-#pragma unroll 4
-        for (int r = 0; r < C; ++r) {
-          lo += *cl.map_shared_rank(&sh.w.lo[b], r);
-          mid += *cl.map_shared_rank(&sh.w.mid[b], r);
-          top += *cl.map_shared_rank(&sh.w.top[b], r);
+      for (int o = 1; o < g; o <<= 1) {
+        if (count) c += __shfl_xor_sync(0xffffffffu, c, o);
+        if (mass) w += __shfl_xor_sync(0xffffffffu, (unsigned long long)w, o);
+      }
+      if (i < per)
+        for (int r = sub; r < C; r += g) {
+          Shared* p = cl.map_shared_rank(&sh, r);
+          if (count) p->rcnt[b] = c;
+          if (mass) p->rmass[b] = w;
         }
-        const uint64_t w = lo + (mid << 15) + (top << 30);
-        for (int r = 0; r < C; ++r) *cl.map_shared_rank(&sh.rmass[b], r) = w;
-      }
     }
     cl.sync();
   }
-  // The whole row's histogram.
-  __device__ void hist_row(bool count, bool mass) {
+  // The row's histogram, of the columns down to `cut` (log2 of the weight). Returns the mass of those
+  // below, summed over the row: they are many, and no bin of theirs is wanted where the border lies
+  // above them.
+  __device__ uint64_t hist_row(bool count, bool mass, float cut) {
+    uint64_t tail = 0;
     for (int v = vbeg + lane; v < vend; v += 32) {
       const uint4 r = get(v);
 #pragma unroll
@@ -338,15 +348,25 @@ struct Sampler {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float ph = lead(elem(r, j0 + j));
-          if (alive(ph)) {
+          if (ph >= cut) {
             const int b = bin_of(ph);
             if (count) atomicAdd(&sh.cnt[b], 1u);
             if (mass) mass_add(b, w[j]);
+          } else if (mass) {
+            tail += w[j];
           }
         }
       }
     }
+    if (mass) {
+      tail = block_sum(tail);
+      if (tid < C) *cl.map_shared_rank(&sh.ctail[rank], tid) = tail;
+    }
     hist_sum(count, mass);
+    tail = 0;
+    if (mass)
+      for (int c = 0; c < C; ++c) tail += sh.ctail[c];
+    return tail;
   }
 
   // The first bin at which the running count (or mass) from bin 0 on, n0 and m0 before it, reaches
@@ -448,27 +468,70 @@ struct Sampler {
     }
     __syncthreads();
   }
+  // Counts a column of the list in its bin. Equal logits share a bin, and adds to one address go one
+  // by one: where the warp has a single bin, one lane adds the sums.
+  __device__ __forceinline__ void list_count(int b, uint64_t w) {
+    const unsigned on = __activemask();
+    int same;
+    __match_all_sync(on, b, &same);
+    if (!same) {
+      atomicAdd(&sh.cnt[b], 1u);
+      mass_add(b, w);
+      return;
+    }
+    const uint32_t lo = __reduce_add_sync(on, (uint32_t)w & 0x7FFFu);
+    const uint32_t mid = __reduce_add_sync(on, ((uint32_t)w >> 15) & 0x7FFFu);
+    const uint32_t top = __reduce_add_sync(on, (uint32_t)(w >> 30));
+    if (lane == __ffs(on) - 1) {
+      atomicAdd(&sh.cnt[b], (uint32_t)__popc(on));
+      atomicAdd(&sh.w.lo[b], lo);
+      atomicAdd(&sh.w.mid[b], mid);
+      atomicAdd(&sh.w.top[b], top);
+    }
+  }
   // The last kept key among the list's columns (n0 columns of mass m0 rank above all of them): the
   // target-th column, or the one at which the running mass reaches the target; and the mass up to
-  // and with it. t0 and mul spread the list's places in the histogram over the bins.
+  // and with it. A list too long to rank outright is cut down to one bin of a histogram: first over
+  // its places (t0 and mul spread them over the bins), then, for equal logits, over its keys.
   __device__ void list_border(int cnt, float t0, float mul, uint32_t n0, uint64_t m0,
                               uint64_t target, bool by_mass) {
     int mem = cnt;
     uint32_t na = n0;
-    uint64_t ma = m0;
-    const bool split = cnt > kRank;
-    if (split) {
-      auto sub = [&](int i) {
-        const float l = __uint_as_float((uint32_t)(sh.lent[i] >> 32));
-        return max(0, min(kBins - 1, (int)((place(lead(l)) - t0) * mul)));
-      };
+    uint64_t ma = m0, lo = 0, hi = ~0ull;
+    bool split = false;
+#pragma unroll 1
+    for (int level = 0; mem > kRank && lo < hi; ++level) {
+      int shift = 0;
+      if (level > 0) {  // the keys left, least and largest
+        lo = ~0ull;
+        hi = 0;
+        for (int j = tid; j < mem; j += kT) {
+          const uint64_t k = sh.lkey[sh.lmem[j]];
+          lo = min(lo, k);
+          hi = max(hi, k);
+        }
+        block_range(lo, hi);
+        shift = max(0, 64 - __clzll((long long)(hi - lo)) - 10);  // (hi - lo) >> shift < 1024
+      }
       hist_zero();
-      if (tid == 0) sh.n_mem = 0;
       __syncthreads();
-      for (int i = tid; i < cnt; i += kT) {
-        const int b = sub(i);
-        atomicAdd(&sh.cnt[b], 1u);
-        mass_add(b, sh.lw[i]);
+      // this thread's entries: their bins, then, with the border bin known, which stay
+      int entry[kList / kT], bin[kList / kT], got = 0;
+#pragma unroll
+      for (int q = 0; q < kList / kT; ++q) {
+        const int j = tid + q * kT;
+        entry[q] = bin[q] = -1;
+        if (j < mem) {
+          const int i = split ? sh.lmem[j] : j;
+          entry[q] = i;
+          if (level > 0) {
+            bin[q] = (int)((hi - sh.lkey[i]) >> shift);
+          } else {
+            const float l = __uint_as_float((uint32_t)(sh.lent[i] >> 32));
+            bin[q] = max(0, min(kBins - 1, (int)((place(lead(l)) - t0) * mul)));
+          }
+          list_count(bin[q], sh.lw[i]);
+        }
       }
       __syncthreads();
 #pragma unroll
@@ -477,14 +540,20 @@ struct Sampler {
         sh.rcnt[b] = sh.cnt[b];
         sh.rmass[b] = own_mass(b);
       }
+      if (tid == 0) sh.n_mem = 0;
       __syncthreads();
-      const int b = find(target, by_mass, n0, m0);
+      const int b = find(target, by_mass, na, ma);
       na = sh.f_above_n;
       ma = sh.f_above_m;
-      for (int i = tid; i < cnt; i += kT)
-        if (sub(i) == b) sh.lmem[atomicAdd(&sh.n_mem, 1u)] = (uint16_t)i;
+#pragma unroll
+      for (int q = 0; q < kList / kT; ++q) got += bin[q] == b;
+      uint32_t at = got ? atomicAdd(&sh.n_mem, (uint32_t)got) : 0;
+#pragma unroll
+      for (int q = 0; q < kList / kT; ++q)
+        if (bin[q] == b) sh.lmem[at++] = (uint16_t)entry[q];
       __syncthreads();
       mem = (int)sh.n_mem;
+      split = true;
     }
     // 2^g threads rank a column together
     int g = 0;
@@ -604,6 +673,12 @@ struct Sampler {
     b.khi = ~0ull;
     b.n_above = sh.f_above_n;
     b.m_above = sh.f_above_m;
+    // min_p's cut clearly above this bin: it alone decides. Clearly below: it has no say.
+    if (minw) {
+      const float at = -log2_minp * binscale;
+      if (at < (float)b.bin - 1.0f) return -1;
+      if (at > (float)b.bin + 2.0f && b.bin < kBins - 1) minw = 0;
+    }
     // this block's mass above: from its histogram, or column by column where min_p has a say
     uint64_t sum = 0;
     const bool from_hist = mass && minw == 0;
@@ -655,6 +730,25 @@ struct Sampler {
     list_weigh((int)cnt);
     list_border((int)cnt, (float)b.bin, (float)kBins, b.n_above, b.m_above, target, by_mass);
     return (int)cnt;
+  }
+
+  // The block's least and largest, in every thread.
+  __device__ void block_range(uint64_t& lo, uint64_t& hi) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      lo = min(lo, (uint64_t)__shfl_xor_sync(0xffffffffu, (unsigned long long)lo, o));
+      hi = max(hi, (uint64_t)__shfl_xor_sync(0xffffffffu, (unsigned long long)hi, o));
+    }
+    __syncthreads();
+    if (lane == 0) {
+      sh.w64[warp] = lo;
+      sh.x64[warp] = hi;
+    }
+    __syncthreads();
+    for (int w = 0; w < kW; ++w) {
+      lo = min(lo, sh.w64[w]);
+      hi = max(hi, sh.x64[w]);
+    }
   }
 
   // Sum over the block, in every thread; the warps' sums stay in wsum.
@@ -714,7 +808,8 @@ struct Sampler {
     sc = scale_of(t);
     const float mp = fminf(fmaxf(minp, 0.0f), 1.0f);
     minw = __float2ull_ru(mp * 8796093022208.0f);
-    lfloor = logit_at(fmaxf(kCutLog2, minw ? __log2f(mp) - 1e-3f : kCutLog2), true);
+    log2_minp = minw ? __log2f(mp) : 0.0f;
+    lfloor = logit_at(fmaxf(kCutLog2, minw ? log2_minp - 1e-3f : kCutLog2), true);
     const bool use_k = k > 0 && k < n, use_p = p < 1.0f;
     uint64_t tkey = 0;
     int buf = 0, ncand = 0;
@@ -723,14 +818,14 @@ struct Sampler {
     auto p_target = [&](uint64_t z) {
       return max((uint64_t)1, mul_frac(fmaxf(p, 0.0f), z, true));
     };
-    auto spread = [&](float lowest) {  // bins from the largest logit down to this one or the cut
-      const float span = fminf(-lead(lowest) * 1.0001f, -kCutLog2 + 0.01f);
+    auto spread = [&](float lowest, float cut) {  // bins from the largest logit to this one or the cut
+      const float span = fminf(-lead(lowest) * 1.0001f, 0.01f - cut);
       binscale = (float)kBins / fmaxf(span, 1e-30f);
     };
 
     bool open = use_k || use_p;  // a filter is left to resolve
     if (use_k && k <= kList && (int64_t)k <= (int64_t)kT * C) {
-      spread(mt);
+      spread(mt, kCutLog2);
       const float ph = lead(own);
       const int mine = alive(ph) ? bin_of(ph) : kBins;
       if (mine < kBins) atomicAdd(&sh.cnt[mine], 1u);
@@ -767,8 +862,11 @@ struct Sampler {
       }
     }
     if (open) {
-      spread(mn);
-      hist_row(use_k, use_p);
+      // top-p alone: the columns of a weight under 2^-20 add up to under 2^-20 n, seldom more than
+      // the share that top-p cuts off
+      float cut = use_k ? kCutLog2 : -20.0f;
+      spread(mn, cut);
+      uint64_t tail = hist_row(use_k, use_p, cut);
       if (!use_k) zero_counts();
       if (!use_p) zero_masses();
       uint32_t total = 0;
@@ -779,26 +877,41 @@ struct Sampler {
         z += sh.rmass[tid * kPer + i];
       }
       z = block_sum(z);
-      total = (uint32_t)block_sum(total);
+      if (use_k) total = (uint32_t)block_sum(total);
       const bool by_k = use_k && total > (uint32_t)k;
+      bool again = false;  // the histogram has to be taken once more
       if (by_k) {
+        const uint64_t given = minw;
+        if (use_p) minw = 0;  // top-p goes by the mass of all columns that top-k leaves
         ncand = row_border(buf, (uint64_t)k, false, use_p);
+        if (use_p) minw = given;
         tkey = sh.tkey;
         z = sh.zk;
+        again = use_p;
       }
       if (use_p) {
-        if (by_k) {  // the lists and the histogram once more
+        if (!by_k) {
+          again = p_target(z + tail) > z;  // the border lies below the cut
+          z += tail;
+        }
+        if (again) {
           __syncthreads();
           hist_zero();
           if (tid == 0) sh.ltotal[buf] = 0;
           cl.sync();
-          hist_row(false, true);
+          spread(mn, kCutLog2);
+          hist_row(false, true, kCutLog2);
           zero_counts();
         }
         ncand = row_border(buf, p_target(z), true, true);
         tkey = sh.tkey;
       }
       open = by_k || use_p;
+      if (ncand < 0) {  // min_p is the stricter one
+        ncand = 0;
+        tkey = 0;
+        open = false;
+      }
     }
     if (!all_listed && !open) {  // everything that min_p keeps
       uint64_t sum = 0;
@@ -853,12 +966,19 @@ struct Sampler {
         for (int v = vbeg + lane; v < vend; v += 32) sum += kept_weights(v, tval, tkey, nullptr);
         block_sum(sum);
       }
-      uint64_t w0 = before;
-      for (int w = 0; w < warp; ++w)
-        w0 += all_listed ? pieces(sh.ww3[0][w], sh.ww3[1][w], sh.ww3[2][w]) : sh.wsum[w];
-      const uint64_t ws =
-          all_listed ? pieces(sh.ww3[0][warp], sh.ww3[1][warp], sh.ww3[2][warp]) : sh.wsum[warp];
-      if (target >= w0 && target < w0 + ws) search(w0, target, tval, tkey, zf);
+      uint64_t ws = 0;  // the warp whose columns hold it
+      if (lane < kW)
+        ws = all_listed ? pieces(sh.ww3[0][lane], sh.ww3[1][lane], sh.ww3[2][lane]) : sh.wsum[lane];
+      uint64_t incl = ws;
+#pragma unroll
+      for (int o = 1; o < kW; o <<= 1) {
+        const uint64_t x = __shfl_up_sync(0xffffffffu, (unsigned long long)incl, o);
+        if (lane >= o) incl += x;
+      }
+      const int w = __ffs(__ballot_sync(0xffffffffu, before + incl > target)) - 1;
+      before += __shfl_sync(0xffffffffu, (unsigned long long)(incl - ws), w);
+      const int v = vcta + w * nvw;
+      search(v, min(min(v + nvw, vcta + nvc), nvrow), before, target, tval, tkey, zf);
     }
     if (a.probs) write_probs(tval, tkey, zf);
   }
@@ -885,40 +1005,45 @@ struct Sampler {
     return sum;
   }
 
-  // One warp: the first of its columns whose running kept mass exceeds the target.
-  __device__ void search(uint64_t before, uint64_t target, float tval, uint64_t tkey, float zf) {
-    for (int v0 = vbeg; v0 < vend; v0 += 32) {
-      const int v = v0 + lane;
+  // The block, over the 16-byte pieces of one warp's columns: the first column whose running kept
+  // mass exceeds the target. A piece a thread, so it takes one step or two where that warp alone
+  // would take many.
+  __device__ void search(int v0, int v1, uint64_t before, uint64_t target, float tval,
+                         uint64_t tkey, float zf) {
+#pragma unroll 1
+    for (; v0 < v1; v0 += kT) {
+      const int v = v0 + tid;
       uint64_t w[VE], sum = 0;
-      if (v < vend) sum = kept_weights(v, tval, tkey, w);
-      if (!__any_sync(0xffffffffu, sum != 0)) continue;
+#pragma unroll
+      for (int j = 0; j < VE; ++j) w[j] = 0;
+      if (v < v1) sum = kept_weights(v, tval, tkey, w);
       uint64_t incl = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const uint64_t x = __shfl_up_sync(0xffffffffu, (unsigned long long)incl, o);
         if (lane >= o) incl += x;
       }
-      const uint64_t total = __shfl_sync(0xffffffffu, (unsigned long long)incl, 31);
-      if (before + total > target) {
-        uint64_t run = before + incl - sum;
-        if (run <= target && before + incl > target) {
-          bool done = false;
+      __syncthreads();
+      if (lane == 31) sh.w64[warp] = incl;
+      __syncthreads();
+      const uint64_t mine = lane < kW ? sh.w64[lane] : 0;
+      uint64_t run = before + warp_sum64(lane < warp ? mine : 0) + incl - sum;
+      before += warp_sum64(mine);
+      if (run <= target && run + sum > target) {
+        bool done = false;
 #pragma unroll
-          for (int j = 0; j < VE; ++j) {
-            run += w[j];
-            if (!done && run > target) {
-              done = true;
-              const int col = v * VE + j - off;
-              const float l = elem(get(v), j);
-              a.ids[(int64_t)row * a.ldt] = a.id_map ? a.id_map[col] : col;
-              if (a.prob)
-                a.prob[(int64_t)row * a.ldt] = weight_float(l, m, sc, lead(l)) * zf;
-            }
+        for (int j = 0; j < VE; ++j) {
+          run += w[j];
+          if (!done && run > target) {
+            done = true;
+            const int col = v * VE + j - off;
+            const float l = elem(get(v), j);
+            a.ids[(int64_t)row * a.ldt] = a.id_map ? a.id_map[col] : col;
+            if (a.prob) a.prob[(int64_t)row * a.ldt] = weight_float(l, m, sc, lead(l)) * zf;
           }
         }
-        return;
       }
-      before += total;
+      if (before > target) return;
     }
   }
 
@@ -986,25 +1111,42 @@ extern "C" tfd_status tfd_sample(const void* logits, int lfmt, int rows, int64_t
   const char* p0 = (const char*)probs;
   if (probs && p0 < l1 && l0 < p0 + (((int64_t)rows - 1) * ldp + n) * 4) return TFD_ERR_INVALID;
 
-  // Blocks a row: until every SM has one, a block's columns leave room for two blocks an SM, or a
-  // block would have less than a few thousand columns.
   const int64_t nv = (n + ve - 1) / ve + 1;  // one more where a row starts off a 16-byte boundary
   const size_t fixed = (sizeof(Shared) + 15) / 16 * 16;
   int dev = 0;
-  const int sms = tfd_host::device_sms(dev);
-  int c = 1;
+  tfd_host::device_sms(dev);
+  // Blocks a row. A launch runs in rounds of as many clusters as fit at two blocks an SM; a round
+  // costs about as much as 16384 columns besides its blocks' own, and columns that do not fit shared
+  // memory beside another block's are read from L2 by every pass, for about 0.4 of their time more.
   auto part = [&](int blocks) { return (size_t)((nv + blocks - 1) / blocks + 1) * 16; };
-  while (c < kMaxC && ((n / c > 2048 && (int64_t)rows * c * 2 <= sms) ||
-                       fixed + part(c) > 112 * 1024 || n / c >= kMaxPart))
-    c *= 2;
-  const bool keep = fixed + part(c) <= (size_t)tfd_host::kSmemLimit;
+  const size_t half = 112 * 1024;
+  if (!tfd_host::allow_clusters<sample_kernel<false, true>>(dev, tfd_host::kSmemLimit))
+    return TFD_ERR_CUDA;
+  int c = 0;
+  int64_t best = 0;
+  for (int i = 1; i <= kMaxC; ++i) {
+    if (i < kMaxC && n / i >= kMaxPart) continue;
+    const int at_once =
+        tfd_host::clusters_at_once<sample_kernel<false, true>>(dev, i, kT, half);
+    const int64_t rounds = (rows + at_once - 1) / at_once;
+    const int64_t cols = n / i, own = fixed + part(i) <= half ? cols : cols * 14 / 10;
+    const int64_t cost = rounds * (16384 + 256 * i + own);
+    if (c == 0 || cost < best) {
+      best = cost;
+      c = i;
+    }
+  }
+#ifdef SAMPLE_C
+  if (SAMPLE_C >= 1) c = SAMPLE_C;
+#endif
+  const bool keep = fixed + part(c) <= half;
   const size_t smem = fixed + (keep ? part(c) : 0);
   Args a = {logits, n, ld, temperature, top_k, top_p, min_p, u, id_map, ids, prob, ldt, probs, ldp,
             dev_status};
   cudaStream_t st = tfd_host::as_stream(stream);
 #define TFD_SAMPLE_CASE(B, K)                                                           \
   if (bf16 == B && keep == K)                                                           \
-    return tfd_host::launch_clusters<sample_kernel<B, K>>(a, rows, c, kT, smem,         \
+    return tfd_host::launch_clusters<sample_kernel<B, K>>(a, dev, rows, c, kT, smem,         \
                                                           tfd_host::kSmemLimit, st);
   TFD_SAMPLE_CASE(true, true) TFD_SAMPLE_CASE(true, false)
   TFD_SAMPLE_CASE(false, true) TFD_SAMPLE_CASE(false, false)

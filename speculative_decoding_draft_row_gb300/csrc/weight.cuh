@@ -24,7 +24,7 @@ constexpr int kFixBits = 43;               // one = 2^43
 constexpr float kCutLog2 = -44.0f;         // below this s a weight is zero
 constexpr int64_t kMaxDrawCols = 1 << 20;  // sums of this many weights stay at or below 2^63
 
-__constant__ const unsigned long long kExp2Table[128] = {
+__device__ const unsigned long long kExp2Table[128] = {
     0x80000000000ull, 0x80b1ed4fd9aull, 0x8164d1f3bc0ull, 0x8218af43740ull, 0x82cd8698ac3ull, 0x8383594eefbull,
     0x843a28c3aceull, 0x84f1f65637aull, 0x85aac367cc5ull, 0x8664915b924ull, 0x871f61969e9ull, 0x87db357ff6aull,
     0x88980e8092eull, 0x8955ee03619ull, 0x8a14d575497ull, 0x8ad4c6452c7ull, 0x8b95c1e3ea9ull, 0x8c57c9c4647ull,
