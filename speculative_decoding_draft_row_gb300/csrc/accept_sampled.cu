@@ -10,7 +10,7 @@
 // clamped to 0..1 with NaN as 0, so sums do not depend on the order and equal p and q leave exactly
 // zero. One thread-block cluster takes a stream, every block decides its drafts for itself, each
 // warp sums a contiguous part of the columns, and after one cluster barrier the block that holds
-// the drawn column scans the part of one warp.
+// the drawn column scans the part of the warp that holds it with all its threads.
 #include <cooperative_groups.h>
 
 #include "launch.cuh"
@@ -215,38 +215,50 @@ __global__ void __launch_bounds__(kT) accept_sampled_kernel(const Args a) {
   uint64_t before = 0;
   for (int c = 0; c < rank; ++c) before += blocks[c];
   if (target < before || target >= before + blocks[rank]) return;
-  for (int w = 0; w < warp; ++w) before += sh.warps[w];
-  if (target < before || target >= before + sh.warps[warp]) return;
-  for (int c = cbeg; c < cend; ++c) {
+  // The warp whose columns hold the target, then those columns by the whole block, a chunk a warp.
+  uint64_t ws = lane < kW ? sh.warps[lane] : 0, incl = ws;
+#pragma unroll
+  for (int o = 1; o < kW; o <<= 1) {
+    const uint64_t x = __shfl_up_sync(0xffffffffu, (unsigned long long)incl, o);
+    if (lane >= o) incl += x;
+  }
+  const int at = __ffs(__ballot_sync(0xffffffffu, before + incl > target)) - 1;
+  before += __shfl_sync(0xffffffffu, (unsigned long long)(incl - ws), at);
+  const int c0 = rank * per_c + at * per_w;
+  const int c1 = min(min(c0 + per_w, (rank + 1) * per_c), chunks);
+#pragma unroll 1
+  for (int c = c0 + warp; c - warp < c1; c += kW) {
     float4 p, q;
-    load(c, p, q);
+    p = q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (c < c1) load(c, p, q);
     const uint64_t r[kCols] = {rest_fix(p.x, q.x), rest_fix(p.y, q.y), rest_fix(p.z, q.z),
                                rest_fix(p.w, q.w)};
     const uint64_t sum = r[0] + r[1] + r[2] + r[3];
-    uint64_t incl = sum;
+    incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint64_t x = __shfl_up_sync(0xffffffffu, (unsigned long long)incl, o);
       if (lane >= o) incl += x;
     }
-    const uint64_t chunk = __shfl_sync(0xffffffffu, (unsigned long long)incl, 31);
-    if (before + chunk > target) {
-      uint64_t run = before + incl - sum;
-      if (run <= target && before + incl > target) {
-        bool done = false;
+    __syncthreads();
+    if (lane == 31) sh.warps[warp] = incl;
+    __syncthreads();
+    const uint64_t mine = lane < kW ? sh.warps[lane] : 0;
+    uint64_t run = before + warp_sum64(lane < warp ? mine : 0) + incl - sum;
+    before += warp_sum64(mine);
+    if (run <= target && run + sum > target) {
+      bool done = false;
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) {
-          run += r[j];
-          if (!done && run > target) {
-            done = true;
-            a.next_ids[s] = c * 32 * kCols + lane * kCols - off + j;
-            if (a.next_prob) a.next_prob[s] = __ull2float_rn(r[j]) / __ull2float_rn(total);
-          }
+      for (int j = 0; j < kCols; ++j) {
+        run += r[j];
+        if (!done && run > target) {
+          done = true;
+          a.next_ids[s] = c * 32 * kCols + lane * kCols - off + j;
+          if (a.next_prob) a.next_prob[s] = __ull2float_rn(r[j]) / __ull2float_rn(total);
         }
       }
-      return;
     }
-    before += chunk;
+    if (before > target) return;
   }
 }
 
@@ -273,11 +285,22 @@ extern "C" tfd_status tfd_accept_sampled(const float* p, int64_t ldp, const floa
                         (const void*)next_ids, (const void*)next_prob, (const void*)dev_status})
     if (x && !aligned(x, 4)) return TFD_ERR_INVALID;
   if (asked_hist && (!aligned(asked_hist, 8) || !aligned(kept_hist, 8))) return TFD_ERR_INVALID;
-  // blocks a stream: enough to load every SM with a few, each at least 1024 columns
+  // blocks a stream: the fewest rounds of what the device holds at once, each costing about as much
+  // as 4096 columns besides its blocks' own
   int dev = 0;
-  const int sms = tfd_host::device_sms(dev);
+  tfd_host::device_sms(dev);
+  if (!tfd_host::allow_clusters<accept_sampled_kernel>(dev, 0)) return TFD_ERR_CUDA;
   int c = 1;
-  while (c < kMaxC && n / c > 1024 && (int64_t)streams * c * 2 <= 4 * (int64_t)sms) c *= 2;
+  int64_t best = INT64_MAX;
+  for (int i = 1; i <= kMaxC; ++i) {
+    const int at_once = tfd_host::clusters_at_once<accept_sampled_kernel>(dev, i, kT, 0);
+    const int64_t rounds = (streams + at_once - 1) / at_once;
+    const int64_t cost = rounds * (4096 + 64 * i + n / i);
+    if (cost < best) {
+      best = cost;
+      c = i;
+    }
+  }
   Args a = {p, ldp, q, ldq, n, nq, q_map, drafts, n_asked, u, u_next, win, n_kept, next_ids,
             next_prob, reinterpret_cast<unsigned long long*>(asked_hist),
             reinterpret_cast<unsigned long long*>(kept_hist), dev_status};
