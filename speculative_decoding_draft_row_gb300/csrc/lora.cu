@@ -20,32 +20,13 @@
 // three (fp32 outputs: all 24 bits) bf16 parts, whose products are exact in the fp32 accumulators.
 #include <cooperative_groups.h>
 
-#include "launch.cuh"
+#include "lora.cuh"
 
 namespace {
 
 using namespace tfd;
+using namespace tfd_adapters;
 namespace cg = cooperative_groups;
-
-constexpr int kT = 256;
-constexpr int kW = kT / 32;
-constexpr int kMaxAdapters = 4096;
-constexpr int kSmallRows = 256;  // up to here one thread a row groups the rows
-
-struct Args {
-  const __nv_bfloat16* x;
-  int64_t ldx;
-  const __nv_bfloat16* a;
-  const __nv_bfloat16* b;
-  const int32_t* ids;
-  const float* scales;
-  const char* base;
-  char* y;
-  int64_t ldb, ldy;
-  int32_t* dev_status;
-  int rows, k, n, rank, n_adapters, splits;
-  bool f32, vec;
-};
 
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                     uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -54,104 +35,6 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Which adapter (n_adapters = none) and which rows tile `t` has; 0 rows when there is no such tile.
-template <int TM>
-__device__ int find_tile(const Args& a, int t, int32_t* rows_out, int32_t* cnt, int& key) {
-  __shared__ int s_key, s_first, s_n, s_warp[kW];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) s_n = 0;
-  auto key_of = [&](int r) {
-    const int id = a.ids[r];
-    if (id >= 0 && id < a.n_adapters) return id;
-    if (id != -1) set_dev_status(a.dev_status, TFD_ERR_DEVICE_DATA);
-    return a.n_adapters;
-  };
-  if (a.rows <= kSmallRows) {
-    int mine = -1, c = 0;
-    if (tid < a.rows) cnt[tid] = mine = key_of(tid);
-    __syncthreads();
-    for (int j = 0; j < tid && tid < a.rows; ++j) c += cnt[j] == mine;
-    const bool first = tid < a.rows && c % TM == 0;
-    const unsigned bal = __ballot_sync(0xffffffffu, first);
-    if (lane == 0) s_warp[warp] = __popc(bal);
-    __syncthreads();
-    int no = __popc(bal & ((1u << lane) - 1));
-    for (int w = 0; w < warp; ++w) no += s_warp[w];
-    if (first && no == t) {
-      s_key = mine;
-      s_first = c;
-      s_n = 1;
-    }
-    __syncthreads();
-    if (s_n == 0) return 0;
-    key = s_key;
-    const int at = c - s_first;
-    const bool member = tid < a.rows && mine == key && at >= 0 && at < TM;
-    if (member) rows_out[at] = tid;
-    const int n = __syncthreads_count(member);
-    return n;
-  }
-  // counts of every adapter, the tiles before and of each, then the members in row order
-  for (int i = tid; i <= a.n_adapters; i += kT) cnt[i] = 0;
-  __syncthreads();
-  for (int r0 = 0; r0 < a.rows; r0 += kT) {
-    const int r = r0 + tid;
-    const int kk = r < a.rows ? key_of(r) : -1;
-    const unsigned same = __match_any_sync(0xffffffffu, kk);
-    if (kk >= 0 && lane == __ffs(same) - 1) atomicAdd(&cnt[kk], __popc(same));
-  }
-  __syncthreads();
-  if (warp == 0) {
-    int before = 0;
-    for (int i0 = 0; i0 <= a.n_adapters; i0 += 32) {
-      const int i = i0 + lane;
-      const int m = i <= a.n_adapters ? (cnt[i] + TM - 1) / TM : 0;
-      int incl = m;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      if (t >= before + incl - m && t < before + incl) {
-        s_key = i;
-        s_first = (t - (before + incl - m)) * TM;
-        s_n = min(TM, cnt[i] - s_first);
-      }
-      before += __shfl_sync(0xffffffffu, incl, 31);
-    }
-  }
-  __syncthreads();
-  const int n = s_n;
-  if (n == 0) return 0;
-  key = s_key;
-  const int per = (a.rows + kT - 1) / kT, r0 = tid * per, r1 = min(a.rows, r0 + per);
-  int c = 0;
-  for (int r = r0; r < r1; ++r) {
-    const int id = a.ids[r];
-    c += (id >= 0 && id < a.n_adapters ? id : a.n_adapters) == key;
-  }
-  int incl = c;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) s_warp[warp] = incl;
-  __syncthreads();
-  int at = incl - c - s_first;
-  for (int w = 0; w < warp; ++w) at += s_warp[w];
-  if (at < TM && at + c > 0) {
-    for (int r = r0; r < r1; ++r) {
-      const int id = a.ids[r];
-      if ((id >= 0 && id < a.n_adapters ? id : a.n_adapters) != key) continue;
-      if (at >= 0 && at < TM) rows_out[at] = r;
-      ++at;
-    }
-  }
-  __syncthreads();
-  return n;
 }
 
 __device__ __forceinline__ uint4 zero4() { return make_uint4(0u, 0u, 0u, 0u); }
@@ -424,6 +307,9 @@ extern "C" tfd_status tfd_lora(const void* x, int rows, int64_t k, int64_t ldx, 
             adapter_ids, scales, (const char*)base, (char*)y, ldb, ldy, dev_status, rows, (int)k,
             (int)n, rank, n_adapters, splits, es == 4, vec};
   cudaStream_t st = tfd_host::as_stream(stream);
+  bool taken = false;
+  const tfd_status tc = launch_tc(a, dev, st, &taken);
+  if (taken || tc != TFD_OK) return tc;
   const int64_t units = tiles * splits;
   if (units * c > 0x7fffffff) return TFD_ERR_UNSUPPORTED;
 #define TFD_LORA_CASE(RT, NT) \

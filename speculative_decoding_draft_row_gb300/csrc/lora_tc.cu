@@ -1,0 +1,452 @@
+// lora_tc.cu - low-rank adapters over prompts: y_r = base_r + s_a B_a (A_a x_r) for tiles of 128 rows of
+// one adapter, on the tensor cores with their accumulators in tensor memory.
+//
+// A 4096-wide projection of a 128-row tile reads 1 MB of x, 1 MB of base, writes 1 MB of y and, at rank
+// 64, takes 1 MB of the adapter from L2: enough rows a tile keep the adapter's share small (at 32
+// rows it was twice all the rest), and at that size warp-level MMAs would bound it (21 us of 12.9
+// GFLOP for 4099 rows at rank 64, against 16 us for the bytes); tcgen05.mma does not.
+//
+// A thread-block cluster takes a tile. Shrink: D1 = x A^T (128 rows x rank), the k range split over the
+// cluster's blocks; x rows (gathered by index) and A come through a ring of shared-memory stages of
+// 64 k by asynchronous 16-byte copies, placed in the 128-byte swizzle that the matrix descriptors
+// name. The blocks' partial sums are added in block order through distributed shared memory, scaled,
+// and split into bf16 parts that add up to them (two where y is bf16: 2^-17 relative, under its 2^-9
+// rounding; three, all 24 bits, where it is fp32). Expand: D2 = h B^T in chunks of outputs that are
+// 128 bytes of a row of y, the parts' products added in the same fp32 accumulators; a chunk's B and base
+// rows are copied two chunks ahead, the base chunk takes the sums and is written out from shared
+// memory in whole 128-byte rows.
+#include <cooperative_groups.h>
+
+#include "lora.cuh"
+
+namespace {
+
+using namespace tfd;
+using namespace tfd_adapters;
+namespace cg = cooperative_groups;
+
+constexpr int kTM = 128;           // rows of a tile: tensor-memory lanes
+constexpr int kKB = 64;            // k of a stage: 128 bytes of a row
+constexpr int kXBytes = kTM * 128;  // x of a stage; a chunk of base rows; h's 64 ranks of one part
+constexpr int kStages = 3;
+constexpr int kBufs = 3;           // chunks of the expand in shared memory
+constexpr int kTmemCols = 256;     // D1 in the first 128, two D2 buffers of 64 behind it
+
+__device__ __forceinline__ uint32_t sa(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// What threads wrote to shared memory becomes visible to the tensor cores' reads.
+__device__ __forceinline__ void fence_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void bar_init(uint32_t bar) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar) : "memory");
+}
+// Bounded wait for the phase of parity `par` (about a second of global time); false on timeout.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t par) {
+  uint64_t t0 = 0;
+  for (int it = 0;; ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(par)
+        : "memory");
+    if (ok) return true;
+    uint64_t now;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+    if (it == 0) t0 = now;
+    else if (now - t0 > 1000000000ull) return false;
+  }
+}
+// Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t sdesc(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// Instruction descriptor of kind::f16: fp32 accumulator, bf16 operands, both K-major, 128 x n.
+__device__ __forceinline__ uint32_t idesc(int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(kTM >> 4) << 24);
+}
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(desc), "r"((uint32_t)acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      : "memory");
+}
+// 16 consecutive accumulator columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+struct Layout {
+  int r16;         // rank rounded up to 16
+  int atoms;       // 64-rank pieces of h and B
+  int parts;       // bf16 parts of h
+  int cols;        // outputs of a chunk
+  uint32_t h, ring, bars;  // offsets: h parts; the stages, and what takes their place; barriers
+  uint32_t stage;  // bytes of a stage
+  uint32_t chunk;  // bytes of a chunk's B
+  uint32_t bytes;
+};
+__host__ __device__ inline Layout layout(int rank, bool f32) {
+  Layout l;
+  l.r16 = (rank + 15) / 16 * 16;
+  l.atoms = (rank + 63) / 64;
+  l.parts = f32 ? 3 : 2;
+  l.cols = f32 ? 32 : 64;
+  l.h = 0;
+  l.ring = (uint32_t)(l.parts * l.atoms * kXBytes);
+  l.stage = kXBytes + (uint32_t)l.r16 * 128;
+  l.chunk = (uint32_t)(l.atoms * l.cols * 128);
+  const uint32_t shrink = kStages * l.stage, expand = kBufs * (l.chunk + kXBytes);
+  const uint32_t sums = (uint32_t)(kTM * (l.r16 + 4) * 4);  // this block's share of D1
+  uint32_t most = shrink > expand ? shrink : expand;
+  most = most > sums ? most : sums;
+  l.bars = l.ring + (most + 1023) / 1024 * 1024;
+  l.bytes = l.bars + 128;
+  return l;
+}
+
+__global__ void __launch_bounds__(kT, 2) lora_tc_kernel(const Args a) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  __shared__ int32_t tile_rows[kTM];
+  cg::cluster_group cl = cg::this_cluster();
+  const int C = (int)cl.num_blocks(), rank_c = (int)cl.block_rank();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const Layout l = layout(a.rank, a.f32);
+  int key = 0;
+  const int m =
+      find_tile<kTM>(a, blockIdx.x / C, tile_rows, reinterpret_cast<int32_t*>(smem), key);
+  if (m == 0) return;  // all blocks of the cluster alike
+  const bool none = key == a.n_adapters;
+  if (none && a.base == a.y) return;
+  __syncthreads();  // the counts are done with
+
+  const int es = a.f32 ? 4 : 2, per = 16 / es;  // outputs in 16 bytes
+  const int chunks = (a.n + l.cols - 1) / l.cols;
+  const int j0 = (int)((int64_t)chunks * rank_c / C), j1 = (int)((int64_t)chunks * (rank_c + 1) / C);
+  // a thread copies 16 bytes of 4 rows, 32 apart: piece tid % 8 of each
+  const int piece = tid & 7, row0 = tid >> 3;
+
+  if (none) {  // y = base, or zeros
+    for (int j = j0; j < j1; ++j)
+      for (int i = 0; i < 4; ++i) {
+        const int row = row0 + 32 * i, o = j * l.cols + piece * per;
+        if (row >= m || o >= a.n) continue;
+        const char* b = a.base ? a.base + (tile_rows[row] * a.ldb + o) * es : nullptr;
+        char* y = a.y + (tile_rows[row] * a.ldy + o) * es;
+        if (o + per <= a.n) {
+          *reinterpret_cast<uint4*>(y) =
+              b ? *reinterpret_cast<const uint4*>(b) : make_uint4(0u, 0u, 0u, 0u);
+        } else {
+          for (int e = 0; e < (a.n - o) * es; ++e) y[e] = b ? b[e] : 0;
+        }
+      }
+    return;
+  }
+
+  const uint32_t s_h = sa(smem + l.h), s_ring = sa(smem + l.ring), bars = sa(smem + l.bars);
+  auto empty = [&](int s) { return bars + 8u * s; };              // stage s has been read
+  const uint32_t shrunk = bars + 8u * kStages;                    // D1 is complete
+  auto done = [&](int b) { return bars + 8u * (kStages + 1 + b); };  // D2 buffer b is complete
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + l.bars + 64);
+  if (tid == 0) {
+    for (int s = 0; s < kStages + 3; ++s) bar_init(bars + 8u * s);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     sa(tmem_slot)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+  bool ok = true;
+
+  // ---- shrink -----------------------------------------------------------------------------------
+  const int kblocks = (a.k + kKB - 1) / kKB;
+  const int k0 = (int)((int64_t)kblocks * rank_c / C), k1 = (int)((int64_t)kblocks * (rank_c + 1) / C);
+  const int nk = k1 - k0;
+  const __nv_bfloat16* xr[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)  // rows past the tile's last repeat it; their sums are not used
+    xr[i] = a.x + (int64_t)tile_rows[min(row0 + 32 * i, m - 1)] * a.ldx + piece * 8;
+  const __nv_bfloat16* aw = a.a + ((int64_t)key * a.rank + row0) * a.k + piece * 8;
+  auto swz = [&](int row) { return (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4)); };
+  auto load_stage = [&](int i) {
+    if (i < nk) {
+      const uint32_t st = s_ring + (uint32_t)(i % kStages) * l.stage;
+      const int kk = (k0 + i) * kKB;
+      const uint32_t bytes = kk + piece * 8 < a.k ? 16u : 0u;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        copy16(st + swz(row0 + 32 * q), bytes ? (const void*)(xr[q] + kk) : (const void*)a.x, bytes);
+      for (int row = row0; row < l.r16; row += 32) {
+        const uint32_t in = row < a.rank ? bytes : 0u;
+        copy16(st + kXBytes + swz(row),
+               in ? (const void*)(aw + (int64_t)(row - row0) * a.k + kk) : (const void*)a.a, in);
+      }
+    }
+    copy_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) load_stage(i);
+  const uint32_t desc1 = idesc(l.r16);
+  for (int i = 0; i < nk; ++i) {
+    copy_wait<kStages - 2>();
+    fence_async();
+    __syncthreads();
+    if (tid == 0) {
+      fence_after();
+      const uint32_t st = s_ring + (uint32_t)(i % kStages) * l.stage;
+      const uint64_t da = sdesc(st), db = sdesc(st + kXBytes);
+#pragma unroll
+      for (int kk = 0; kk < kKB / 16; ++kk) mma(tmem, da + 2u * kk, db + 2u * kk, desc1, (i | kk) != 0);
+      mma_commit(empty(i % kStages));
+    }
+    if (i >= 1 && i + kStages - 1 < nk && ok)  // the stage to fill next was read by step i - 1
+      ok = bar_wait(empty((i - 1) % kStages), (uint32_t)((i - 1) / kStages) & 1u);
+    load_stage(i + kStages - 1);
+  }
+  if (nk > 0) {
+    if (tid == 0) mma_commit(shrunk);
+    if (ok) ok = bar_wait(shrunk, 0);
+  }
+  copy_wait<0>();
+  fence_after();
+  __syncthreads();
+
+  // this block's sums, a row a thread, then all blocks' in order
+  const int rp = l.r16 + 4;  // floats of a row: 16-byte pieces of 8 rows in different banks
+  float* sums = reinterpret_cast<float*>(smem + l.ring);
+  if (warp < 4) {
+    const int row = 32 * warp + lane;
+    for (int c = 0; c < l.r16; c += 16) {
+      float v[16];
+      tmem_ld16(tmem + ((uint32_t)(32 * warp) << 16) + (uint32_t)c, v);
+#pragma unroll
+      for (int e = 0; e < 16; e += 4)
+        *reinterpret_cast<float4*>(sums + row * rp + c + e) =
+            nk > 0 ? make_float4(v[e], v[e + 1], v[e + 2], v[e + 3])
+                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+  }
+  fence_before();
+  cl.sync();
+  const float scale = a.scales ? a.scales[key] : 1.0f;
+  for (int i = tid; i < kTM * (l.r16 / 8); i += kT) {
+    const int row = i / (l.r16 / 8), c = i % (l.r16 / 8) * 8;
+    float v[8] = {};
+    for (int r = 0; r < C; ++r) {
+      const float4* p = reinterpret_cast<const float4*>(cl.map_shared_rank(sums, r) + row * rp + c);
+      const float4 x = p[0], y = p[1];
+      v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+      v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= scale;
+    for (int part = 0; part < l.parts; ++part) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const __nv_bfloat16 x = __float2bfloat16_rn(v[2 * e]), y = __float2bfloat16_rn(v[2 * e + 1]);
+        w[e] = (uint32_t)__bfloat16_as_ushort(x) | ((uint32_t)__bfloat16_as_ushort(y) << 16);
+        v[2 * e] -= __bfloat162float(x);
+        v[2 * e + 1] -= __bfloat162float(y);
+      }
+      unsigned char* at = smem + l.h + (part * l.atoms + c / 64) * kXBytes + row * 128 +
+                          (((c % 64 / 8) ^ (row & 7)) << 4);
+      *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  fence_async();
+  // the ring is free again once every block has read this one's sums
+  cl.sync();
+
+  // ---- expand -----------------------------------------------------------------------------------
+  const __nv_bfloat16* bw = a.b + (int64_t)key * a.n * a.rank;
+  auto b_of = [&](int buf) { return l.ring + (uint32_t)buf * (l.chunk + kXBytes); };
+  auto load_chunk = [&](int j) {
+    if (j < j1) {
+      const uint32_t st = s_ring + (uint32_t)((j - j0) % kBufs) * (l.chunk + kXBytes);
+      const int o0 = j * l.cols;
+      // B: 16-byte pieces of the chunk's rows, a row's 64 ranks after another's
+      const int pieces = l.r16 / 8;
+      for (int i = tid; i < l.cols * pieces; i += kT) {
+        const int row = i / pieces, p = i % pieces;
+        const bool in = o0 + row < a.n && p * 8 < a.rank;
+        copy16(st + (uint32_t)((p / 8) * l.cols * 128 + row * 128 + (((p % 8) ^ (row & 7)) << 4)),
+               in ? (const void*)(bw + (int64_t)(o0 + row) * a.rank + p * 8) : (const void*)bw,
+               in ? 16u : 0u);
+      }
+      if (a.base) {
+        const int o = o0 + piece * per;
+        const int left = (a.n - o) * es;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int row = row0 + 32 * q;
+          const uint32_t bytes = row < m && left > 0 ? (uint32_t)min(left, 16) : 0u;
+          copy16(st + l.chunk + swz(row),
+                 bytes ? (const void*)(a.base + ((int64_t)tile_rows[row] * a.ldb + o) * es)
+                       : (const void*)a.base,
+                 bytes);
+        }
+      }
+    }
+    copy_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kBufs - 1; ++i) load_chunk(j0 + i);
+  const uint32_t desc2 = idesc(l.cols);
+  for (int j = j0; j < j1; ++j) {
+    const int i = j - j0, buf = i % kBufs, d = i & 1;
+    copy_wait<kBufs - 2>();
+    fence_async();
+    __syncthreads();  // the chunk is here; the last one's rows have been written from their buffer
+    if (tid == 0) {
+      fence_after();
+      const uint32_t st = s_ring + (uint32_t)buf * (l.chunk + kXBytes);
+      const uint32_t acc = tmem + 128u + (uint32_t)(d * 64);
+      bool more = false;
+      for (int part = 0; part < l.parts; ++part)
+        for (int kk = 0; kk < l.r16 / 16; ++kk) {
+          mma(acc, sdesc(s_h + (uint32_t)((part * l.atoms + kk / 4) * kXBytes)) + 2u * (kk % 4),
+              sdesc(st + (uint32_t)(kk / 4 * l.cols * 128)) + 2u * (kk % 4), desc2, more);
+          more = true;
+        }
+      mma_commit(done(d));
+    }
+    load_chunk(j + kBufs - 1);  // into the buffer of the chunk before this one
+    if (ok) ok = bar_wait(done(d), (uint32_t)(i >> 1) & 1u);
+    fence_after();
+    // two warps a quarter of the rows, half a row a thread: 64 bytes of the base, in place
+    const int row = 32 * (warp & 3) + lane, half = warp >> 2;
+    const uint32_t acc =
+        tmem + 128u + (uint32_t)(d * 64 + half * (l.cols / 2)) + ((uint32_t)(32 * (warp & 3)) << 16);
+    unsigned char* rows = smem + b_of(buf) + l.chunk + row * 128;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      if (a.f32 && g == 1) break;
+      float v[16];
+      tmem_ld16(acc + 16u * g, v);
+      if (a.f32) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float4* p = reinterpret_cast<float4*>(rows + (((half * 4 + c) ^ (row & 7)) << 4));
+          float4 x = a.base ? *p : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          x.x += v[4 * c], x.y += v[4 * c + 1], x.z += v[4 * c + 2], x.w += v[4 * c + 3];
+          *p = x;
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint4* p = reinterpret_cast<uint4*>(rows + (((half * 4 + 2 * g + c) ^ (row & 7)) << 4));
+          uint4 x = a.base ? *p : make_uint4(0u, 0u, 0u, 0u);
+          uint32_t* w = &x.x;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = (uint32_t)f32_to_bf16_bits(bf16_lo(w[e]) + v[8 * c + 2 * e]) |
+                   ((uint32_t)f32_to_bf16_bits(bf16_hi(w[e]) + v[8 * c + 2 * e + 1]) << 16);
+          *p = x;
+        }
+      }
+    }
+    fence_before();
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int r = row0 + 32 * q, o = j * l.cols + piece * per;
+      if (r >= m || o >= a.n) continue;
+      const uint4 x = *reinterpret_cast<const uint4*>(smem + b_of(buf) + l.chunk + swz(r));
+      char* y = a.y + ((int64_t)tile_rows[r] * a.ldy + o) * es;
+      if (o + per <= a.n) {
+        *reinterpret_cast<uint4*>(y) = x;
+      } else if (a.f32) {
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (o + e < a.n) reinterpret_cast<uint32_t*>(y)[e] = w[e];
+      } else {
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (o + e < a.n) reinterpret_cast<uint16_t*>(y)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+      }
+    }
+  }
+  copy_wait<0>();
+  __syncthreads();
+  if (!ok) set_dev_status(a.dev_status, TFD_ERR_TIMEOUT);
+  if (warp == 0) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols)
+                 : "memory");
+  }
+}
+
+}  // namespace
+
+tfd_status tfd_adapters::launch_tc(const Args& a, int dev, cudaStream_t stream, bool* taken) {
+  *taken = false;
+  const int each = (a.rows + a.n_adapters - 1) / a.n_adapters;
+  if (!a.vec || each < 96 || a.rows <= kSmallRows || a.k < kKB) return TFD_OK;
+  const Layout l = layout(a.rank, a.f32);
+  size_t smem = l.bytes + 1024;
+  const size_t counts = (size_t)4 * (a.n_adapters + 1) + 1024;
+  if (smem < counts) smem = counts;
+  const int most = 226 * 1024;  // with the static part: 227 KB
+  if (smem > (size_t)most || !tfd_host::allow_clusters<lora_tc_kernel>(dev, most)) return TFD_OK;
+  // blocks a tile: the fewest rounds, each costing about as much as 2048 columns of k and n
+  const int64_t likely = (a.rows + kTM - 1) / kTM + a.n_adapters / 2;
+  const int64_t tiles = (int64_t)a.rows / kTM + a.n_adapters + 1;
+  int c = 1;
+  int64_t best = INT64_MAX;
+  for (int i = 1; i <= 8; i *= 2) {
+    const int at_once = tfd_host::clusters_at_once<lora_tc_kernel>(dev, i, kT, smem);
+    const int64_t cost = (likely + at_once - 1) / at_once * (2048 + ((int64_t)a.k + 2 * a.n) / i);
+    if (cost < best) {
+      best = cost;
+      c = i;
+    }
+  }
+  *taken = true;
+  return tfd_host::launch_clusters<lora_tc_kernel>(a, dev, tiles, c, kT, smem, most, stream);
+}

@@ -164,3 +164,33 @@ def test_binding_refuses_wrong_tensors():
     flat = torch.zeros(4 * 64 + 8, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(tfd.TfdError):                 # y overlaps base, shifted
         tfd.tfd_lora(x, a, b, ids, base=flat[:256].view(4, 64), y=flat[8:264].view(4, 64))
+
+
+@pytest.mark.parametrize("R,k,n,rank,na", [
+    (300, 64, 64, 8, 1), (513, 72, 77, 16, 1), (640, 264, 200, 24, 2), (1000, 1032, 130, 40, 3),
+    (777, 4096, 520, 64, 2), (1500, 512, 1000, 128, 5), (400, 128, 33, 96, 1)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("sort", [True, False])
+def test_prompts(R, k, n, rank, na, dtype, sort):
+    """Tiles of many rows of one adapter, whole rows of y 16-byte aligned and n at any size; rows
+    without an adapter; nothing beyond n is written; in place gives the same bits."""
+    need_gpu()
+    x, a, b, ids, base, s = make(R, k, n, rank, na, dtype, seed=5, sort=sort)
+    wide = (n + 8 + 7) // 8 * 8
+    bw = torch.full((R, wide), 5.0, dtype=dtype, device="cuda")
+    yw = torch.full((R, wide), -7.0, dtype=dtype, device="cuda")
+    bw[:, :n] = base
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = tfd.tfd_lora(x, a, b, ids, base=bw[:, :n], y=yw[:, :n], scales=s, dev_status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    check(y, x, a, b, ids, base, s)
+    assert (yw[:, n:] == -7).all() and torch.equal(y[ids == -1], base[ids == -1])
+    tfd.tfd_lora(x, a, b, ids, base=bw[:, :n], y=bw[:, :n], scales=s)
+    torch.cuda.synchronize()
+    assert torch.equal(bw[:, :n], y) and (bw[:, n:] == 5).all()
+    z = torch.empty_like(yw)
+    tfd.tfd_lora(x, a, b, ids, y=z[:, :n])
+    torch.cuda.synchronize()
+    check(z[:, :n], x, a, b, ids, None, None, "no base")
+    assert not z[:, :n][ids == -1].any()
