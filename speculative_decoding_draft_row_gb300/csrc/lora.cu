@@ -243,11 +243,12 @@ __global__ void __launch_bounds__(kT, 2) lora_kernel(const Args a) {
 }
 
 template <int RT, int NT>
-tfd_status launch(const Args& a, int dev, int c, int64_t units, cudaStream_t stream) {
+tfd_status launch(Args a, int dev, int c, int64_t units, cudaStream_t stream) {
   constexpr int TM = 8 * NT, R = 16 * RT, RP = R + 4, HT = (TM + 15) / 16 * 16;
   size_t smem = (size_t)(kW + 1) * TM * RP * 4 + (size_t)3 * HT * (R + 8) * 2;
   const size_t counts = (size_t)4 * (a.rows <= kSmallRows ? kSmallRows : a.n_adapters + 1);
   if (smem < counts) smem = counts;
+  a.smem = (int)smem;
   return tfd_host::launch_clusters<lora_kernel<RT, NT>>(a, dev, units, c, kT, smem, 112 * 1024, stream);
 }
 
@@ -305,7 +306,7 @@ extern "C" tfd_status tfd_lora(const void* x, int rows, int64_t k, int64_t ldx, 
       splits *= 2;
   Args a = {(const __nv_bfloat16*)x, ldx, (const __nv_bfloat16*)a_w, (const __nv_bfloat16*)b_w,
             adapter_ids, scales, (const char*)base, (char*)y, ldb, ldy, dev_status, rows, (int)k,
-            (int)n, rank, n_adapters, splits, es == 4, vec};
+            (int)n, rank, n_adapters, splits, 0, es == 4, vec};
   cudaStream_t st = tfd_host::as_stream(stream);
   bool taken = false;
   const tfd_status tc = launch_tc(a, dev, st, &taken);

@@ -24,13 +24,14 @@ struct Args {
   int64_t ldb, ldy;
   int32_t* dev_status;
   int rows, k, n, rank, n_adapters, splits;
+  int smem;  // bytes of shared memory that the tile search may use
   bool f32, vec;
 };
 
 // Which adapter (n_adapters = none) and which rows tile `t` has; 0 rows when there is no such tile.
-template <int TM>
+template <int TM, int T = kT>
 __device__ int find_tile(const Args& a, int t, int32_t* rows_out, int32_t* cnt, int& key) {
-  __shared__ int s_key, s_first, s_n, s_warp[kW];
+  __shared__ int s_key, s_first, s_n, s_warp[T / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) s_n = 0;
   auto key_of = [&](int r) {
@@ -64,14 +65,36 @@ __device__ int find_tile(const Args& a, int t, int32_t* rows_out, int32_t* cnt, 
     const int n = __syncthreads_count(member);
     return n;
   }
-  // counts of every adapter, the tiles before and of each, then the members in row order
-  for (int i = tid; i <= a.n_adapters; i += kT) cnt[i] = 0;
+  // counts of every adapter, the tiles before and of each, then the members in row order; the keys
+  // stay in shared memory where they fit
+  for (int i = tid; i <= a.n_adapters; i += T) cnt[i] = 0;
+  uint16_t* keys = reinterpret_cast<uint16_t*>(cnt + a.n_adapters + 1);
+  const bool kept = a.rows <= (a.smem - 4 * (a.n_adapters + 1)) / 2;
   __syncthreads();
-  for (int r0 = 0; r0 < a.rows; r0 += kT) {
-    const int r = r0 + tid;
-    const int kk = r < a.rows ? key_of(r) : -1;
-    const unsigned same = __match_any_sync(0xffffffffu, kk);
-    if (kk >= 0 && lane == __ffs(same) - 1) atomicAdd(&cnt[kk], __popc(same));
+#pragma unroll 1
+  for (int r0 = 0; r0 < a.rows; r0 += 4 * T) {
+    int id[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {  // the loads first
+      const int r = r0 + q * T + tid;
+      id[q] = r < a.rows ? a.ids[r] : -2;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int r = r0 + q * T + tid;
+      const bool in = r < a.rows;
+      const bool good = id[q] >= 0 && id[q] < a.n_adapters;
+      if (in && !good && id[q] != -1) set_dev_status(a.dev_status, TFD_ERR_DEVICE_DATA);
+      const int kk = in ? (good ? id[q] : a.n_adapters) : -1;
+      if (kept && in) keys[r] = (uint16_t)kk;
+      int same;
+      __match_all_sync(0xffffffffu, kk, &same);
+      if (same) {  // a prompt's rows adjoin
+        if (kk >= 0 && lane == 0) atomicAdd(&cnt[kk], 32);
+      } else if (kk >= 0) {
+        atomicAdd(&cnt[kk], 1);
+      }
+    }
   }
   __syncthreads();
   if (warp == 0) {
@@ -97,12 +120,15 @@ __device__ int find_tile(const Args& a, int t, int32_t* rows_out, int32_t* cnt, 
   const int n = s_n;
   if (n == 0) return 0;
   key = s_key;
-  const int per = (a.rows + kT - 1) / kT, r0 = tid * per, r1 = min(a.rows, r0 + per);
-  int c = 0;
-  for (int r = r0; r < r1; ++r) {
+  const int per = (a.rows + T - 1) / T, r0 = tid * per, r1 = min(a.rows, r0 + per);
+  auto is_mine = [&](int r) {
+    if (kept) return (int)keys[r] == key;
     const int id = a.ids[r];
-    c += (id >= 0 && id < a.n_adapters ? id : a.n_adapters) == key;
-  }
+    return (id >= 0 && id < a.n_adapters ? id : a.n_adapters) == key;
+  };
+  int c = 0;
+#pragma unroll 4
+  for (int r = r0; r < r1; ++r) c += is_mine(r);
   int incl = c;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -113,10 +139,9 @@ __device__ int find_tile(const Args& a, int t, int32_t* rows_out, int32_t* cnt, 
   __syncthreads();
   int at = incl - c - s_first;
   for (int w = 0; w < warp; ++w) at += s_warp[w];
-  if (at < TM && at + c > 0) {
+  if (c > 0 && at < TM && at + c > 0) {
     for (int r = r0; r < r1; ++r) {
-      const int id = a.ids[r];
-      if ((id >= 0 && id < a.n_adapters ? id : a.n_adapters) != key) continue;
+      if (!is_mine(r)) continue;
       if (at >= 0 && at < TM) rows_out[at] = r;
       ++at;
     }
@@ -126,6 +151,6 @@ __device__ int find_tile(const Args& a, int t, int32_t* rows_out, int32_t* cnt, 
 }
 
 // The tensor-memory form for many rows an adapter (lora_tc.cu). *taken says whether it applies.
-tfd_status launch_tc(const Args& a, int dev, cudaStream_t stream, bool* taken);
+tfd_status launch_tc(Args a, int dev, cudaStream_t stream, bool* taken);
 
 }  // namespace tfd_adapters

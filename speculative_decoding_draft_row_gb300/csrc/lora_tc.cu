@@ -25,11 +25,13 @@ using namespace tfd;
 using namespace tfd_adapters;
 namespace cg = cooperative_groups;
 
+constexpr int kNT = 512;           // threads
+constexpr int kRows = 128 * 8 / kNT;  // rows of a 128-byte-wide tile that a thread copies 16 bytes of
 constexpr int kTM = 128;           // rows of a tile: tensor-memory lanes
 constexpr int kKB = 64;            // k of a stage: 128 bytes of a row
 constexpr int kXBytes = kTM * 128;  // x of a stage; a chunk of base rows; h's 64 ranks of one part
-constexpr int kStages = 3;
-constexpr int kBufs = 3;           // chunks of the expand in shared memory
+constexpr int kStages = 4;
+constexpr int kBufs = 3;            // chunks of the expand in shared memory
 constexpr int kTmemCols = 256;     // D1 in the first 128, two D2 buffers of 64 behind it
 
 __device__ __forceinline__ uint32_t sa(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -111,12 +113,27 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// 8 of them.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Shared memory. The shrink's stages take all of it; then come the blocks' sums, the h parts, in the
+// sums' place where a rank of at most 64 lets a thread hold its share of them in between, and the
+// expand's chunks.
 struct Layout {
   int r16;         // rank rounded up to 16
   int atoms;       // 64-rank pieces of h and B
   int parts;       // bf16 parts of h
   int cols;        // outputs of a chunk
-  uint32_t h, ring, bars;  // offsets: h parts; the stages, and what takes their place; barriers
+  uint32_t h, sums, bufs, bars;  // offsets
   uint32_t stage;  // bytes of a stage
   uint32_t chunk;  // bytes of a chunk's B
   uint32_t bytes;
@@ -127,20 +144,20 @@ __host__ __device__ inline Layout layout(int rank, bool f32) {
   l.atoms = (rank + 63) / 64;
   l.parts = f32 ? 3 : 2;
   l.cols = f32 ? 32 : 64;
+  const uint32_t h = (uint32_t)(l.parts * l.atoms * kXBytes);
+  const uint32_t sums = ((uint32_t)(kTM * (l.r16 + 4) * 4) + 1023) / 1024 * 1024;
   l.h = 0;
-  l.ring = (uint32_t)(l.parts * l.atoms * kXBytes);
+  l.sums = l.atoms == 1 ? 0 : h;
+  l.bufs = l.atoms == 1 ? (h > sums ? h : sums) : h + sums;
   l.stage = kXBytes + (uint32_t)l.r16 * 128;
   l.chunk = (uint32_t)(l.atoms * l.cols * 128);
-  const uint32_t shrink = kStages * l.stage, expand = kBufs * (l.chunk + kXBytes);
-  const uint32_t sums = (uint32_t)(kTM * (l.r16 + 4) * 4);  // this block's share of D1
-  uint32_t most = shrink > expand ? shrink : expand;
-  most = most > sums ? most : sums;
-  l.bars = l.ring + (most + 1023) / 1024 * 1024;
+  const uint32_t shrink = kStages * l.stage, expand = l.bufs + kBufs * (l.chunk + kXBytes);
+  l.bars = shrink > expand ? shrink : expand;
   l.bytes = l.bars + 128;
   return l;
 }
 
-__global__ void __launch_bounds__(kT, 2) lora_tc_kernel(const Args a) {
+__global__ void __launch_bounds__(kNT, 2) lora_tc_kernel(const Args a) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -151,7 +168,7 @@ __global__ void __launch_bounds__(kT, 2) lora_tc_kernel(const Args a) {
   const Layout l = layout(a.rank, a.f32);
   int key = 0;
   const int m =
-      find_tile<kTM>(a, blockIdx.x / C, tile_rows, reinterpret_cast<int32_t*>(smem), key);
+      find_tile<kTM, kNT>(a, blockIdx.x / C, tile_rows, reinterpret_cast<int32_t*>(smem), key);
   if (m == 0) return;  // all blocks of the cluster alike
   const bool none = key == a.n_adapters;
   if (none && a.base == a.y) return;
@@ -160,13 +177,13 @@ __global__ void __launch_bounds__(kT, 2) lora_tc_kernel(const Args a) {
   const int es = a.f32 ? 4 : 2, per = 16 / es;  // outputs in 16 bytes
   const int chunks = (a.n + l.cols - 1) / l.cols;
   const int j0 = (int)((int64_t)chunks * rank_c / C), j1 = (int)((int64_t)chunks * (rank_c + 1) / C);
-  // a thread copies 16 bytes of 4 rows, 32 apart: piece tid % 8 of each
+  // a thread copies 16 bytes of kRows rows, 64 apart: piece tid % 8 of each
   const int piece = tid & 7, row0 = tid >> 3;
 
   if (none) {  // y = base, or zeros
     for (int j = j0; j < j1; ++j)
-      for (int i = 0; i < 4; ++i) {
-        const int row = row0 + 32 * i, o = j * l.cols + piece * per;
+      for (int i = 0; i < kRows; ++i) {
+        const int row = row0 + 64 * i, o = j * l.cols + piece * per;
         if (row >= m || o >= a.n) continue;
         const char* b = a.base ? a.base + (tile_rows[row] * a.ldb + o) * es : nullptr;
         char* y = a.y + (tile_rows[row] * a.ldy + o) * es;
@@ -180,7 +197,7 @@ __global__ void __launch_bounds__(kT, 2) lora_tc_kernel(const Args a) {
     return;
   }
 
-  const uint32_t s_h = sa(smem + l.h), s_ring = sa(smem + l.ring), bars = sa(smem + l.bars);
+  const uint32_t s_h = sa(smem + l.h), s_ring = sa(smem), s_bufs = sa(smem + l.bufs), bars = sa(smem + l.bars);
   auto empty = [&](int s) { return bars + 8u * s; };              // stage s has been read
   const uint32_t shrunk = bars + 8u * kStages;                    // D1 is complete
   auto done = [&](int b) { return bars + 8u * (kStages + 1 + b); };  // D2 buffer b is complete
@@ -206,10 +223,10 @@ __global__ void __launch_bounds__(kT, 2) lora_tc_kernel(const Args a) {
   const int kblocks = (a.k + kKB - 1) / kKB;
   const int k0 = (int)((int64_t)kblocks * rank_c / C), k1 = (int)((int64_t)kblocks * (rank_c + 1) / C);
   const int nk = k1 - k0;
-  const __nv_bfloat16* xr[4];
+  const __nv_bfloat16* xr[kRows];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)  // rows past the tile's last repeat it; their sums are not used
-    xr[i] = a.x + (int64_t)tile_rows[min(row0 + 32 * i, m - 1)] * a.ldx + piece * 8;
+  for (int i = 0; i < kRows; ++i)  // rows past the tile's last repeat it; their sums are not used
+    xr[i] = a.x + (int64_t)tile_rows[min(row0 + 64 * i, m - 1)] * a.ldx + piece * 8;
   const __nv_bfloat16* aw = a.a + ((int64_t)key * a.rank + row0) * a.k + piece * 8;
   auto swz = [&](int row) { return (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4)); };
   auto load_stage = [&](int i) {
@@ -218,9 +235,9 @@ __global__ void __launch_bounds__(kT, 2) lora_tc_kernel(const Args a) {
       const int kk = (k0 + i) * kKB;
       const uint32_t bytes = kk + piece * 8 < a.k ? 16u : 0u;
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        copy16(st + swz(row0 + 32 * q), bytes ? (const void*)(xr[q] + kk) : (const void*)a.x, bytes);
-      for (int row = row0; row < l.r16; row += 32) {
+      for (int q = 0; q < kRows; ++q)
+        copy16(st + swz(row0 + 64 * q), bytes ? (const void*)(xr[q] + kk) : (const void*)a.x, bytes);
+      for (int row = row0; row < l.r16; row += 64) {
         const uint32_t in = row < a.rank ? bytes : 0u;
         copy16(st + kXBytes + swz(row),
                in ? (const void*)(aw + (int64_t)(row - row0) * a.k + kk) : (const void*)a.a, in);
@@ -255,35 +272,88 @@ __global__ void __launch_bounds__(kT, 2) lora_tc_kernel(const Args a) {
   fence_after();
   __syncthreads();
 
-  // this block's sums, a row a thread, then all blocks' in order
-  const int rp = l.r16 + 4;  // floats of a row: 16-byte pieces of 8 rows in different banks
-  float* sums = reinterpret_cast<float*>(smem + l.ring);
-  if (warp < 4) {
-    const int row = 32 * warp + lane;
-    for (int c = 0; c < l.r16; c += 16) {
-      float v[16];
-      tmem_ld16(tmem + ((uint32_t)(32 * warp) << 16) + (uint32_t)c, v);
+  // the expand's first chunks are on their way while h is summed
+  auto b_of = [&](int buf) { return l.bufs + (uint32_t)buf * (l.chunk + kXBytes); };
+  // this thread's 16-byte pieces of a chunk's B (rows of r16 ranks), and of its rows of base and y
+  const int b_pieces = l.r16 / 8;
+  const __nv_bfloat16* b_from[2];
+  uint32_t b_to[2];
+  int b_row[2];
 #pragma unroll
-      for (int e = 0; e < 16; e += 4)
-        *reinterpret_cast<float4*>(sums + row * rp + c + e) =
-            nk > 0 ? make_float4(v[e], v[e + 1], v[e + 2], v[e + 3])
-                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int q = 0; q < 2; ++q) {  // at most 64 rows of 16 pieces
+    const int i = tid + q * kNT, row = i / b_pieces, p = i % b_pieces;
+    b_row[q] = p * 8 < a.rank ? row : a.n;  // ranks past the adapter's: zeros
+    if (row >= l.cols) b_row[q] = -1;
+    b_from[q] = a.b + ((int64_t)key * a.n + row) * a.rank + p * 8;
+    b_to[q] = (uint32_t)((p / 8) * l.cols * 128 + row * 128 + (((p % 8) ^ (row & 7)) << 4));
+  }
+  int64_t row_of[kRows];
+#pragma unroll
+  for (int q = 0; q < kRows; ++q) row_of[q] = row0 + 64 * q < m ? tile_rows[row0 + 64 * q] : -1;
+  auto load_chunk = [&](int j) {
+    if (j < j1) {
+      const uint32_t st = s_bufs + (uint32_t)((j - j0) % kBufs) * (l.chunk + kXBytes);
+      const int o0 = j * l.cols;
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        if (b_row[q] >= 0) {
+          const bool in = o0 + b_row[q] < a.n;
+          copy16(st + b_to[q], in ? (const void*)(b_from[q] + (int64_t)o0 * a.rank) : (const void*)a.b,
+                 in ? 16u : 0u);
+        }
+      if (a.base) {
+        const int o = o0 + piece * per, left = (a.n - o) * es;
+#pragma unroll
+        for (int q = 0; q < kRows; ++q) {
+          const uint32_t bytes = row_of[q] >= 0 && left > 0 ? (uint32_t)min(left, 16) : 0u;
+          copy16(st + l.chunk + swz(row0 + 64 * q),
+                 bytes ? (const void*)(a.base + (row_of[q] * a.ldb + o) * es) : (const void*)a.base,
+                 bytes);
+        }
+      }
     }
+    copy_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kBufs - 1; ++i) load_chunk(j0 + i);
+
+  // this block's sums, a row a thread
+  const int rp = l.r16 + 4;  // floats of a row: 16-byte pieces of 8 rows in different banks
+  float* sums = reinterpret_cast<float*>(smem + l.sums);
+  for (int c = 16 * (warp >> 2); c < l.r16; c += 64) {  // four warps a quarter of the rows
+    const int row = 32 * (warp & 3) + lane;
+    float v[16];
+    tmem_ld16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)c, v);
+#pragma unroll
+    for (int e = 0; e < 16; e += 4)
+      *reinterpret_cast<float4*>(sums + row * rp + c + e) =
+          nk > 0 ? make_float4(v[e], v[e + 1], v[e + 2], v[e + 3])
+                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   }
   fence_before();
   cl.sync();
+  // All blocks' sums in order, scaled: each block takes its share of the tile, 8 ranks of a row at a
+  // time, and brings every block the parts of h (reading all of the others' sums took 7 us at rank
+  // 64 and four blocks).
   const float scale = a.scales ? a.scales[key] : 1.0f;
-  for (int i = tid; i < kTM * (l.r16 / 8); i += kT) {
-    const int row = i / (l.r16 / 8), c = i % (l.r16 / 8) * 8;
-    float v[8] = {};
+  const int pieces8 = l.r16 / 8, items = kTM * pieces8;
+  const int i0 = items * rank_c / C, i1 = items * (rank_c + 1) / C;
+  auto sum_of = [&](int i, float (&v)[8]) {
+    const int at = i / pieces8 * rp + i % pieces8 * 8;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+#pragma unroll 4
     for (int r = 0; r < C; ++r) {
-      const float4* p = reinterpret_cast<const float4*>(cl.map_shared_rank(sums, r) + row * rp + c);
+      const float4* p = reinterpret_cast<const float4*>(cl.map_shared_rank(sums, r) + at);
       const float4 x = p[0], y = p[1];
       v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
       v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= scale;
+  };
+  auto put_h = [&](int i, float (&v)[8]) {
+    const int row = i / pieces8, c = i % pieces8 * 8;
     for (int part = 0; part < l.parts; ++part) {
       uint32_t w[4];
 #pragma unroll
@@ -295,47 +365,29 @@ __global__ void __launch_bounds__(kT, 2) lora_tc_kernel(const Args a) {
       }
       unsigned char* at = smem + l.h + (part * l.atoms + c / 64) * kXBytes + row * 128 +
                           (((c % 64 / 8) ^ (row & 7)) << 4);
-      *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int r = 0; r < C; ++r)
+        *reinterpret_cast<uint4*>(cl.map_shared_rank(at, r)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  };
+  if (l.atoms == 1) {
+    float v[kRows][8];  // at most 8 items a row
+#pragma unroll
+    for (int q = 0; q < kRows; ++q)
+      if (i0 + tid + q * kNT < i1) sum_of(i0 + tid + q * kNT, v[q]);
+    cl.sync();  // every block has read all sums: h takes their place
+#pragma unroll
+    for (int q = 0; q < kRows; ++q)
+      if (i0 + tid + q * kNT < i1) put_h(i0 + tid + q * kNT, v[q]);
+  } else {
+    for (int i = i0 + tid; i < i1; i += kNT) {
+      float v[8];
+      sum_of(i, v);
+      put_h(i, v);
     }
   }
-  fence_async();
-  // the ring is free again once every block has read this one's sums
-  cl.sync();
+  cl.sync();  // h is here, and no block writes another's memory from now on
 
   // ---- expand -----------------------------------------------------------------------------------
-  const __nv_bfloat16* bw = a.b + (int64_t)key * a.n * a.rank;
-  auto b_of = [&](int buf) { return l.ring + (uint32_t)buf * (l.chunk + kXBytes); };
-  auto load_chunk = [&](int j) {
-    if (j < j1) {
-      const uint32_t st = s_ring + (uint32_t)((j - j0) % kBufs) * (l.chunk + kXBytes);
-      const int o0 = j * l.cols;
-      // B: 16-byte pieces of the chunk's rows, a row's 64 ranks after another's
-      const int pieces = l.r16 / 8;
-      for (int i = tid; i < l.cols * pieces; i += kT) {
-        const int row = i / pieces, p = i % pieces;
-        const bool in = o0 + row < a.n && p * 8 < a.rank;
-        copy16(st + (uint32_t)((p / 8) * l.cols * 128 + row * 128 + (((p % 8) ^ (row & 7)) << 4)),
-               in ? (const void*)(bw + (int64_t)(o0 + row) * a.rank + p * 8) : (const void*)bw,
-               in ? 16u : 0u);
-      }
-      if (a.base) {
-        const int o = o0 + piece * per;
-        const int left = (a.n - o) * es;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int row = row0 + 32 * q;
-          const uint32_t bytes = row < m && left > 0 ? (uint32_t)min(left, 16) : 0u;
-          copy16(st + l.chunk + swz(row),
-                 bytes ? (const void*)(a.base + ((int64_t)tile_rows[row] * a.ldb + o) * es)
-                       : (const void*)a.base,
-                 bytes);
-        }
-      }
-    }
-    copy_commit();
-  };
-#pragma unroll
-  for (int i = 0; i < kBufs - 1; ++i) load_chunk(j0 + i);
   const uint32_t desc2 = idesc(l.cols);
   for (int j = j0; j < j1; ++j) {
     const int i = j - j0, buf = i % kBufs, d = i & 1;
@@ -344,13 +396,14 @@ __global__ void __launch_bounds__(kT, 2) lora_tc_kernel(const Args a) {
     __syncthreads();  // the chunk is here; the last one's rows have been written from their buffer
     if (tid == 0) {
       fence_after();
-      const uint32_t st = s_ring + (uint32_t)buf * (l.chunk + kXBytes);
+      const uint32_t st = s_bufs + (uint32_t)buf * (l.chunk + kXBytes);
       const uint32_t acc = tmem + 128u + (uint32_t)(d * 64);
       bool more = false;
+      const uint64_t dh = sdesc(s_h), db = sdesc(st);  // advanced by units of 16 bytes
       for (int part = 0; part < l.parts; ++part)
         for (int kk = 0; kk < l.r16 / 16; ++kk) {
-          mma(acc, sdesc(s_h + (uint32_t)((part * l.atoms + kk / 4) * kXBytes)) + 2u * (kk % 4),
-              sdesc(st + (uint32_t)(kk / 4 * l.cols * 128)) + 2u * (kk % 4), desc2, more);
+          mma(acc, dh + (uint32_t)((part * l.atoms + (kk >> 2)) * (kXBytes / 16) + 2 * (kk & 3)),
+              db + (uint32_t)((kk >> 2) * l.cols * 8 + 2 * (kk & 3)), desc2, more);
           more = true;
         }
       mma_commit(done(d));
@@ -358,46 +411,49 @@ __global__ void __launch_bounds__(kT, 2) lora_tc_kernel(const Args a) {
     load_chunk(j + kBufs - 1);  // into the buffer of the chunk before this one
     if (ok) ok = bar_wait(done(d), (uint32_t)(i >> 1) & 1u);
     fence_after();
-    // two warps a quarter of the rows, half a row a thread: 64 bytes of the base, in place
-    const int row = 32 * (warp & 3) + lane, half = warp >> 2;
-    const uint32_t acc =
-        tmem + 128u + (uint32_t)(d * 64 + half * (l.cols / 2)) + ((uint32_t)(32 * (warp & 3)) << 16);
+    // four warps a quarter of the rows, a quarter of a row a thread: two pieces of the base, in place
+    const int row = 32 * (warp & 3) + lane, w4 = warp >> 2;
+    const uint32_t acc = tmem + 128u + (uint32_t)(d * 64 + w4 * (l.cols / 4)) +
+                         ((uint32_t)(32 * (warp & 3)) << 16);
     unsigned char* rows = smem + b_of(buf) + l.chunk + row * 128;
+    uint4* p0 = reinterpret_cast<uint4*>(rows + (((2 * w4) ^ (row & 7)) << 4));
+    uint4* p1 = reinterpret_cast<uint4*>(rows + (((2 * w4 + 1) ^ (row & 7)) << 4));
+    uint4 x[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+    if (a.base) {
+      x[0] = *p0;
+      x[1] = *p1;
+    }
+    float v[16];
+    if (a.f32) {
+      tmem_ld8(acc, v);
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      if (a.f32 && g == 1) break;
-      float v[16];
-      tmem_ld16(acc + 16u * g, v);
-      if (a.f32) {
+      for (int c = 0; c < 2; ++c) {
+        x[c].x = __float_as_uint(__uint_as_float(x[c].x) + v[4 * c]);
+        x[c].y = __float_as_uint(__uint_as_float(x[c].y) + v[4 * c + 1]);
+        x[c].z = __float_as_uint(__uint_as_float(x[c].z) + v[4 * c + 2]);
+        x[c].w = __float_as_uint(__uint_as_float(x[c].w) + v[4 * c + 3]);
+      }
+    } else {
+      tmem_ld16(acc, v);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float4* p = reinterpret_cast<float4*>(rows + (((half * 4 + c) ^ (row & 7)) << 4));
-          float4 x = a.base ? *p : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          x.x += v[4 * c], x.y += v[4 * c + 1], x.z += v[4 * c + 2], x.w += v[4 * c + 3];
-          *p = x;
-        }
-      } else {
+      for (int c = 0; c < 2; ++c) {
+        uint32_t* w = &x[c].x;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint4* p = reinterpret_cast<uint4*>(rows + (((half * 4 + 2 * g + c) ^ (row & 7)) << 4));
-          uint4 x = a.base ? *p : make_uint4(0u, 0u, 0u, 0u);
-          uint32_t* w = &x.x;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[e] = (uint32_t)f32_to_bf16_bits(bf16_lo(w[e]) + v[8 * c + 2 * e]) |
-                   ((uint32_t)f32_to_bf16_bits(bf16_hi(w[e]) + v[8 * c + 2 * e + 1]) << 16);
-          *p = x;
-        }
+        for (int e = 0; e < 4; ++e)
+          w[e] = (uint32_t)f32_to_bf16_bits(bf16_lo(w[e]) + v[8 * c + 2 * e]) |
+                 ((uint32_t)f32_to_bf16_bits(bf16_hi(w[e]) + v[8 * c + 2 * e + 1]) << 16);
       }
     }
+    *p0 = x[0];
+    *p1 = x[1];
     fence_before();
     __syncthreads();
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int r = row0 + 32 * q, o = j * l.cols + piece * per;
-      if (r >= m || o >= a.n) continue;
-      const uint4 x = *reinterpret_cast<const uint4*>(smem + b_of(buf) + l.chunk + swz(r));
-      char* y = a.y + ((int64_t)tile_rows[r] * a.ldy + o) * es;
+    for (int q = 0; q < kRows; ++q) {
+      const int o = j * l.cols + piece * per;
+      if (row_of[q] < 0 || o >= a.n) continue;
+      const uint4 x = *reinterpret_cast<const uint4*>(smem + b_of(buf) + l.chunk + swz(row0 + 64 * q));
+      char* y = a.y + (row_of[q] * a.ldy + o) * es;
       if (o + per <= a.n) {
         *reinterpret_cast<uint4*>(y) = x;
       } else if (a.f32) {
@@ -424,7 +480,7 @@ __global__ void __launch_bounds__(kT, 2) lora_tc_kernel(const Args a) {
 
 }  // namespace
 
-tfd_status tfd_adapters::launch_tc(const Args& a, int dev, cudaStream_t stream, bool* taken) {
+tfd_status tfd_adapters::launch_tc(Args a, int dev, cudaStream_t stream, bool* taken) {
   *taken = false;
   const int each = (a.rows + a.n_adapters - 1) / a.n_adapters;
   if (!a.vec || each < 96 || a.rows <= kSmallRows || a.k < kKB) return TFD_OK;
@@ -433,20 +489,22 @@ tfd_status tfd_adapters::launch_tc(const Args& a, int dev, cudaStream_t stream, 
   const size_t counts = (size_t)4 * (a.n_adapters + 1) + 1024;
   if (smem < counts) smem = counts;
   const int most = 226 * 1024;  // with the static part: 227 KB
+  a.smem = (int)smem - 1024;
   if (smem > (size_t)most || !tfd_host::allow_clusters<lora_tc_kernel>(dev, most)) return TFD_OK;
-  // blocks a tile: the fewest rounds, each costing about as much as 2048 columns of k and n
-  const int64_t likely = (a.rows + kTM - 1) / kTM + a.n_adapters / 2;
+  // Blocks a tile: as many as give every block an SM of its own (two on one slow each other down
+  // here, 4099 rows at rank 64: 4 blocks 48 us, 7 84), within one round of clusters.
+  const int64_t likely = (a.rows + kTM - 1) / kTM + a.n_adapters - 1;
   const int64_t tiles = (int64_t)a.rows / kTM + a.n_adapters + 1;
+  const int sms = tfd_host::device_sms(dev);
   int c = 1;
-  int64_t best = INT64_MAX;
-  for (int i = 1; i <= 8; i *= 2) {
-    const int at_once = tfd_host::clusters_at_once<lora_tc_kernel>(dev, i, kT, smem);
-    const int64_t cost = (likely + at_once - 1) / at_once * (2048 + ((int64_t)a.k + 2 * a.n) / i);
-    if (cost < best) {
-      best = cost;
-      c = i;
-    }
-  }
+  while (c < 8 && likely * (c + 1) <= sms &&
+         likely <= (smem <= 112 * 1024  // two blocks an SM, or one
+                        ? tfd_host::clusters_at_once<lora_tc_kernel, 0>(dev, c + 1, kNT, smem)
+                        : tfd_host::clusters_at_once<lora_tc_kernel, 1>(dev, c + 1, kNT, smem)))
+    ++c;
+#ifdef LTC_C
+  c = LTC_C;
+#endif
   *taken = true;
-  return tfd_host::launch_clusters<lora_tc_kernel>(a, dev, tiles, c, kT, smem, most, stream);
+  return tfd_host::launch_clusters<lora_tc_kernel>(a, dev, tiles, c, kNT, smem, most, stream);
 }
