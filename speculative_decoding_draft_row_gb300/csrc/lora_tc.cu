@@ -502,9 +502,6 @@ tfd_status tfd_adapters::launch_tc(Args a, int dev, cudaStream_t stream, bool* t
                         ? tfd_host::clusters_at_once<lora_tc_kernel, 0>(dev, c + 1, kNT, smem)
                         : tfd_host::clusters_at_once<lora_tc_kernel, 1>(dev, c + 1, kNT, smem)))
     ++c;
-#ifdef LTC_C
-  c = LTC_C;
-#endif
   *taken = true;
   return tfd_host::launch_clusters<lora_tc_kernel>(a, dev, tiles, c, kNT, smem, most, stream);
 }
