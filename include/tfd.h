@@ -86,6 +86,7 @@ typedef enum { TFD_OUT_NONE = 0, TFD_OUT_F32 = 1, TFD_OUT_BF16 = 2, TFD_OUT_ADD_
 #define TFD_MAX_TOPK 512    /* [TFE] commit "... ocabulary head": cand_k from 1 to 512 */
 #define TFD_MAX_WINDOW 511  /* [TFE] commit "... ocabulary head": window up to 511 (512 keys) */
 #define TFD_MAX_RANK 128     /* rank of a low-rank adapter */
+#define TFD_MAX_LORA_ROWS 262144  /* rows of one tfd_lora call (every tile's search reads all ids) */
 #define TFD_MAX_DRAW_COLS 1048576 /* columns of a row that a token is drawn from (exact sums) */
 
 /* A static string naming a status. Never NULL. */
@@ -334,7 +335,8 @@ tfd_status tfd_absorb(const void* k_rows, const void* v_rows, const void* k_gamm
  *   The token is the first column, in column order, at which the running mass of the kept columns
  *   exceeds u times their total. temperature 0 takes the largest logit (ties to the lower id).
  *   NaN and -inf logits, and weights below 2^-44 of the largest, have no mass; where logits are
- *   +inf, those share the mass. A row without any mass gets id -1 and probability 0.
+ *   +inf, those share the mass. Positive temperatures below 1e-30 count as 1e-30. A row without any
+ *   mass gets id -1 and probability 0.
  *   Masses are summed as integers (multiples of 2^-43 of the largest weight), so a row's token
  *   does not depend on the other rows, the launch or the order of the sums. The pages take the
  *   round's draws as inputs; this call makes them, and has no counterpart there.
@@ -401,7 +403,7 @@ tfd_status tfd_accept_sampled(const float* p, int64_t ldp, const float* q, int64
  *   (y[r] = base[r]). One row up to whole prompts. The pages run one set of weights for all
  *   streams; this call has no counterpart there.
  * Args:
- *   x        device bf16 [rows][ldx], ldx >= k, ldx % 8 == 0; rows >= 1.
+ *   x        device bf16 [rows][ldx], ldx >= k, ldx % 8 == 0; rows 1..TFD_MAX_LORA_ROWS.
  *   a_w, b_w device bf16 [n_adapters][rank][k] and [n_adapters][n][rank]; k >= 8, k % 8 == 0;
  *            rank 8..TFD_MAX_RANK, rank % 8 == 0 (smaller ones padded with zeros); n >= 1;
  *            n_adapters 1..4096. x, a_w and b_w 16-byte aligned.
@@ -411,6 +413,8 @@ tfd_status tfd_accept_sampled(const float* p, int64_t ldp, const float* q, int64
  *   base     device [rows][ldb], ldb >= n, or NULL (zeros); y device [rows][ldy], ldy >= n: any
  *            element-aligned base and stride (16-byte aligned rows are faster). y may be base
  *            itself (same stride); it overlaps nothing else the call reads.
+ *   dev_status also takes TFD_ERR_TIMEOUT: tiles of many rows wait, bounded to about a second, for
+ *            their own matrix products; outputs are then undefined.
  */
 tfd_status tfd_lora(const void* x, int rows, int64_t k, int64_t ldx, const void* a_w,
                     const void* b_w, int n_adapters, int rank, int64_t n,

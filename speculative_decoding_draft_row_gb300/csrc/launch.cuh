@@ -23,8 +23,9 @@ inline int device_sms(int& dev) {
 }
 
 // How many clusters of c blocks of a kernel run at once on the current device (asked of the runtime
-// once a device and Class of launches, for one with `smem` bytes): clusters do not cross the GPU's partitions of SMs,
-// so for large c it is well below (SMs * blocks an SM) / c (c = 16 at two blocks an SM: 14, not 19).
+// once a device and Class of launches, for one with `smem` bytes): clusters do not cross the GPU's
+// partitions of SMs, so for large c it is well below (SMs * blocks an SM) / c (c = 16 at two blocks
+// an SM: 14, not 19).
 constexpr int kMaxCluster = 16;
 template <auto Kernel, int Class = 0>
 int clusters_at_once(int dev, int c, int threads, size_t smem) {

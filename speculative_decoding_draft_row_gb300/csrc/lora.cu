@@ -299,7 +299,7 @@ extern "C" tfd_status tfd_lora(const void* x, int rows, int64_t k, int64_t ldx, 
     return TFD_ERR_INVALID;
   if (ldx < k || ldx % 8 || ldy < n || (base && ldb < n)) return TFD_ERR_INVALID;
   if (rank > TFD_MAX_RANK || n_adapters > kMaxAdapters || k > (1 << 24) || n > (1 << 24) ||
-      rows > (1 << 22))
+      rows > TFD_MAX_LORA_ROWS)
     return TFD_ERR_UNSUPPORTED;
   const int es = out_mode == TFD_OUT_F32 ? 4 : 2;
   if (!aligned(x, 16) || !aligned(a_w, 16) || !aligned(b_w, 16) || !aligned(y, es) ||
@@ -310,7 +310,10 @@ extern "C" tfd_status tfd_lora(const void* x, int rows, int64_t k, int64_t ldx, 
     return (const char*)p < (const char*)q + qbytes && (const char*)q < (const char*)p + bytes;
   };
   const int64_t ybytes = (((int64_t)rows - 1) * ldy + n) * es;
-  if (overlap(y, ybytes, x, (((int64_t)rows - 1) * ldx + k) * 2)) return TFD_ERR_INVALID;
+  if (overlap(y, ybytes, x, (((int64_t)rows - 1) * ldx + k) * 2) ||
+      overlap(y, ybytes, a_w, (int64_t)n_adapters * rank * k * 2) ||
+      overlap(y, ybytes, b_w, (int64_t)n_adapters * rank * n * 2))
+    return TFD_ERR_INVALID;
   if (base && !(base == y && ldb == ldy) &&
       overlap(y, ybytes, base, (((int64_t)rows - 1) * ldb + n) * es))
     return TFD_ERR_INVALID;

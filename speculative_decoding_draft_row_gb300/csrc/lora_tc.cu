@@ -31,7 +31,6 @@ constexpr int kTM = 128;           // rows of a tile: tensor-memory lanes
 constexpr int kKB = 64;            // k of a stage: 128 bytes of a row
 constexpr int kXBytes = kTM * 128;  // x of a stage; a chunk of base rows; h's 64 ranks of one part
 constexpr int kStages = 4;
-constexpr int kBufs = 3;            // chunks of the expand in shared memory
 constexpr int kTmemCols = 256;     // D1 in the first 128, two D2 buffers of 64 behind it
 
 __device__ __forceinline__ uint32_t sa(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -125,9 +124,9 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
   for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// Shared memory. The shrink's stages take all of it; then come the blocks' sums, the h parts, in the
-// sums' place where a rank of at most 64 lets a thread hold its share of them in between, and the
-// expand's chunks.
+// Shared memory. The shrink's stages take all of it; then come the blocks' sums, the h parts and the
+// expand's chunks. The sums lie where h comes later if the rank is at most 64, so that a thread can
+// hold its share of h in between, and else where the chunks come later.
 struct Layout {
   int r16;         // rank rounded up to 16
   int atoms;       // 64-rank pieces of h and B
@@ -138,7 +137,7 @@ struct Layout {
   uint32_t chunk;  // bytes of a chunk's B
   uint32_t bytes;
 };
-__host__ __device__ inline Layout layout(int rank, bool f32) {
+__host__ __device__ inline Layout layout(int rank, bool f32, int bufs) {
   Layout l;
   l.r16 = (rank + 15) / 16 * 16;
   l.atoms = (rank + 63) / 64;
@@ -148,15 +147,18 @@ __host__ __device__ inline Layout layout(int rank, bool f32) {
   const uint32_t sums = ((uint32_t)(kTM * (l.r16 + 4) * 4) + 1023) / 1024 * 1024;
   l.h = 0;
   l.sums = l.atoms == 1 ? 0 : h;
-  l.bufs = l.atoms == 1 ? (h > sums ? h : sums) : h + sums;
+  l.bufs = l.atoms == 1 && sums > h ? sums : h;
   l.stage = kXBytes + (uint32_t)l.r16 * 128;
   l.chunk = (uint32_t)(l.atoms * l.cols * 128);
-  const uint32_t shrink = kStages * l.stage, expand = l.bufs + kBufs * (l.chunk + kXBytes);
+  const uint32_t shrink = kStages * l.stage, expand = l.bufs + bufs * (l.chunk + kXBytes);
   l.bars = shrink > expand ? shrink : expand;
+  if (l.bars < l.sums + sums) l.bars = l.sums + sums;
   l.bytes = l.bars + 128;
   return l;
 }
 
+// kBufs: chunks of the expand in shared memory.
+template <int kBufs>
 __global__ void __launch_bounds__(kNT, 2) lora_tc_kernel(const Args a) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -165,7 +167,7 @@ __global__ void __launch_bounds__(kNT, 2) lora_tc_kernel(const Args a) {
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), rank_c = (int)cl.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const Layout l = layout(a.rank, a.f32);
+  const Layout l = layout(a.rank, a.f32, kBufs);
   int key = 0;
   const int m =
       find_tile<kTM, kNT>(a, blockIdx.x / C, tile_rows, reinterpret_cast<int32_t*>(smem), key);
@@ -272,7 +274,6 @@ __global__ void __launch_bounds__(kNT, 2) lora_tc_kernel(const Args a) {
   fence_after();
   __syncthreads();
 
-  // the expand's first chunks are on their way while h is summed
   auto b_of = [&](int buf) { return l.bufs + (uint32_t)buf * (l.chunk + kXBytes); };
   // this thread's 16-byte pieces of a chunk's B (rows of r16 ranks), and of its rows of base and y
   const int b_pieces = l.r16 / 8;
@@ -314,8 +315,11 @@ __global__ void __launch_bounds__(kNT, 2) lora_tc_kernel(const Args a) {
     }
     copy_commit();
   };
+  auto first_chunks = [&]() {
 #pragma unroll
-  for (int i = 0; i < kBufs - 1; ++i) load_chunk(j0 + i);
+    for (int i = 0; i < kBufs - 1; ++i) load_chunk(j0 + i);
+  };
+  if (l.atoms == 1) first_chunks();  // on their way while h is summed
 
   // this block's sums, a row a thread
   const int rp = l.r16 + 4;  // floats of a row: 16-byte pieces of 8 rows in different banks
@@ -385,29 +389,37 @@ __global__ void __launch_bounds__(kNT, 2) lora_tc_kernel(const Args a) {
       put_h(i, v);
     }
   }
-  cl.sync();  // h is here, and no block writes another's memory from now on
+  asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");  // for the MMAs that read h
+  cl.sync();  // h is here, and no block reads or writes another's memory from now on
+  if (l.atoms > 1) first_chunks();
 
   // ---- expand -----------------------------------------------------------------------------------
+  // The products of a chunk run while the one before it is added to its base and written.
   const uint32_t desc2 = idesc(l.cols);
+  auto multiply = [&](int i) {
+    fence_after();
+    const uint32_t st = s_bufs + (uint32_t)(i % kBufs) * (l.chunk + kXBytes);
+    const uint32_t acc = tmem + 128u + (uint32_t)((i & 1) * 64);
+    bool more = false;
+    const uint64_t dh = sdesc(s_h), db = sdesc(st);  // advanced by units of 16 bytes
+    for (int part = 0; part < l.parts; ++part)
+      for (int kk = 0; kk < l.r16 / 16; ++kk) {
+        mma(acc, dh + (uint32_t)((part * l.atoms + (kk >> 2)) * (kXBytes / 16) + 2 * (kk & 3)),
+            db + (uint32_t)((kk >> 2) * l.cols * 8 + 2 * (kk & 3)), desc2, more);
+        more = true;
+      }
+    mma_commit(done(i & 1));
+  };
+  copy_wait<kBufs - 2>();
+  fence_async();
+  __syncthreads();
+  if (tid == 0 && j0 < j1) multiply(0);
   for (int j = j0; j < j1; ++j) {
     const int i = j - j0, buf = i % kBufs, d = i & 1;
-    copy_wait<kBufs - 2>();
+    copy_wait<kBufs - 3>();
     fence_async();
-    __syncthreads();  // the chunk is here; the last one's rows have been written from their buffer
-    if (tid == 0) {
-      fence_after();
-      const uint32_t st = s_bufs + (uint32_t)buf * (l.chunk + kXBytes);
-      const uint32_t acc = tmem + 128u + (uint32_t)(d * 64);
-      bool more = false;
-      const uint64_t dh = sdesc(s_h), db = sdesc(st);  // advanced by units of 16 bytes
-      for (int part = 0; part < l.parts; ++part)
-        for (int kk = 0; kk < l.r16 / 16; ++kk) {
-          mma(acc, dh + (uint32_t)((part * l.atoms + (kk >> 2)) * (kXBytes / 16) + 2 * (kk & 3)),
-              db + (uint32_t)((kk >> 2) * l.cols * 8 + 2 * (kk & 3)), desc2, more);
-          more = true;
-        }
-      mma_commit(done(d));
-    }
+    __syncthreads();  // the next chunk is here; the last one's rows have been written from its buffer
+    if (tid == 0 && j + 1 < j1) multiply(i + 1);
     load_chunk(j + kBufs - 1);  // into the buffer of the chunk before this one
     if (ok) ok = bar_wait(done(d), (uint32_t)(i >> 1) & 1u);
     fence_after();
@@ -480,17 +492,18 @@ __global__ void __launch_bounds__(kNT, 2) lora_tc_kernel(const Args a) {
 
 }  // namespace
 
-tfd_status tfd_adapters::launch_tc(Args a, int dev, cudaStream_t stream, bool* taken) {
-  *taken = false;
-  const int each = (a.rows + a.n_adapters - 1) / a.n_adapters;
-  if (!a.vec || each < 96 || a.rows <= kSmallRows || a.k < kKB) return TFD_OK;
-  const Layout l = layout(a.rank, a.f32);
+namespace {
+
+template <int kBufs>
+tfd_status launch(Args a, int dev, cudaStream_t stream, bool* taken) {
+  const Layout l = layout(a.rank, a.f32, kBufs);
   size_t smem = l.bytes + 1024;
   const size_t counts = (size_t)4 * (a.n_adapters + 1) + 1024;
   if (smem < counts) smem = counts;
   const int most = 226 * 1024;  // with the static part: 227 KB
   a.smem = (int)smem - 1024;
-  if (smem > (size_t)most || !tfd_host::allow_clusters<lora_tc_kernel>(dev, most)) return TFD_OK;
+  if (smem > (size_t)most || !tfd_host::allow_clusters<lora_tc_kernel<kBufs>>(dev, most))
+    return TFD_OK;
   // Blocks a tile: as many as give every block an SM of its own (two on one slow each other down
   // here, 4099 rows at rank 64: 4 blocks 48 us, 7 84), within one round of clusters.
   const int64_t likely = (a.rows + kTM - 1) / kTM + a.n_adapters - 1;
@@ -499,9 +512,22 @@ tfd_status tfd_adapters::launch_tc(Args a, int dev, cudaStream_t stream, bool* t
   int c = 1;
   while (c < 8 && likely * (c + 1) <= sms &&
          likely <= (smem <= 112 * 1024  // two blocks an SM, or one
-                        ? tfd_host::clusters_at_once<lora_tc_kernel, 0>(dev, c + 1, kNT, smem)
-                        : tfd_host::clusters_at_once<lora_tc_kernel, 1>(dev, c + 1, kNT, smem)))
+                        ? tfd_host::clusters_at_once<lora_tc_kernel<kBufs>, 0>(dev, c + 1, kNT, smem)
+                        : tfd_host::clusters_at_once<lora_tc_kernel<kBufs>, 1>(dev, c + 1, kNT, smem)))
     ++c;
   *taken = true;
-  return tfd_host::launch_clusters<lora_tc_kernel>(a, dev, tiles, c, kNT, smem, most, stream);
+  return tfd_host::launch_clusters<lora_tc_kernel<kBufs>>(a, dev, tiles, c, kNT, smem, most, stream);
+}
+
+}  // namespace
+
+tfd_status tfd_adapters::launch_tc(Args a, int dev, cudaStream_t stream, bool* taken) {
+  *taken = false;
+  const int each = (a.rows + a.n_adapters - 1) / a.n_adapters;
+  if (!a.vec || each < 96 || a.rows <= kSmallRows || a.k < kKB) return TFD_OK;
+  // Three chunks let two blocks share an SM, which pays once there are more tiles than SMs (32768 rows
+  // at rank 64: 264 us, with four 328); a block alone hides more behind four (16384 rows: 147 and 156).
+  const int64_t likely = (a.rows + kTM - 1) / kTM + a.n_adapters - 1;
+  if (likely > tfd_host::device_sms(dev)) return launch<3>(a, dev, stream, taken);
+  return launch<4>(a, dev, stream, taken);
 }

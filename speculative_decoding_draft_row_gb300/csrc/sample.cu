@@ -1136,17 +1136,14 @@ extern "C" tfd_status tfd_sample(const void* logits, int lfmt, int rows, int64_t
       c = i;
     }
   }
-#ifdef SAMPLE_C
-  if (SAMPLE_C >= 1) c = SAMPLE_C;
-#endif
   const bool keep = fixed + part(c) <= half;
   const size_t smem = fixed + (keep ? part(c) : 0);
   Args a = {logits, n, ld, temperature, top_k, top_p, min_p, u, id_map, ids, prob, ldt, probs, ldp,
             dev_status};
   cudaStream_t st = tfd_host::as_stream(stream);
-#define TFD_SAMPLE_CASE(B, K)                                                           \
-  if (bf16 == B && keep == K)                                                           \
-    return tfd_host::launch_clusters<sample_kernel<B, K>>(a, dev, rows, c, kT, smem,         \
+#define TFD_SAMPLE_CASE(B, K)                                                        \
+  if (bf16 == B && keep == K)                                                        \
+    return tfd_host::launch_clusters<sample_kernel<B, K>>(a, dev, rows, c, kT, smem, \
                                                           tfd_host::kSmemLimit, st);
   TFD_SAMPLE_CASE(true, true) TFD_SAMPLE_CASE(true, false)
   TFD_SAMPLE_CASE(false, true) TFD_SAMPLE_CASE(false, false)

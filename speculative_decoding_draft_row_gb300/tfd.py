@@ -93,10 +93,10 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _stream(stream):
+def _stream(stream, dev=None):
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(_current_device())
+            return _raw_stream(_current_device() if dev is None else dev)
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -347,11 +347,12 @@ def _vec(t, dtype, count, dev, name):
 
 def _rows_of(t, rows, cols, dtype, dev, name):
     """Row stride of a matrix [rows][cols] with contiguous columns on the device."""
+    stride, step = t.stride()
     if t.dtype is not dtype or t.get_device() != dev or t.shape != (rows, cols) or \
-            (cols > 1 and t.stride(1) != 1):
+            (step != 1 and cols > 1):
         raise ValueError(f"{name}: {dtype} [{rows}][{cols}] with contiguous columns on the current "
                          "CUDA device is wanted")
-    return t.stride(0) if rows > 1 else max(cols, t.stride(0))
+    return stride if rows > 1 else max(cols, stride)
 
 
 def tfd_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, id_map=None,
@@ -361,37 +362,38 @@ def tfd_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, 
     u [rows] after temperature, top_k, top_p and min_p (each [rows] or None). ``ids`` [rows] may be
     a column of a larger array (``prob`` then with the same stride); ``probs`` [rows][n] (or
     want_probs) receives the filtered distribution. Returns (ids, prob, probs)."""
-    f32, i32, dev = torch.float32, torch.int32, _current_device()
+    f32, i32, dev, vec = torch.float32, torch.int32, _current_device(), _vec
     rows, cols = logits.shape
-    if logits.dtype is f32:
-        fmt = X_F32
-    elif logits.dtype is torch.bfloat16:
-        fmt = X_BF16
-    else:
+    kind = logits.dtype
+    if kind is not f32 and kind is not torch.bfloat16:
         raise ValueError("logits: float32 or bfloat16 is wanted")
-    ld = _rows_of(logits, rows, cols, logits.dtype, dev, "logits")
-    n = cols if n is None else n
-    if n > cols:
+    ld = _rows_of(logits, rows, cols, kind, dev, "logits")
+    if n is None:
+        n = cols
+    elif n > cols:
         raise ValueError("logits have fewer than n columns")
     if ids is None:
         ids = torch.empty(rows, dtype=i32, device=logits.device)
         if prob is None:
             prob = torch.empty(rows, dtype=f32, device=logits.device)
-    if ids.dtype is not i32 or ids.shape != (rows,) or ids.get_device() != dev:
+    ldt, = ids.stride() if ids.dim() == 1 else (0,)
+    if ids.dtype is not i32 or ids.shape != (rows,) or ids.get_device() != dev or \
+            (ldt < 1 and rows > 1):
         raise ValueError("ids: an int32 vector of one id a row is wanted")
-    ldt = ids.stride(0) if rows > 1 else 1
     if prob is not None and (prob.dtype is not f32 or prob.shape != (rows,) or
                              prob.get_device() != dev or (rows > 1 and prob.stride(0) != ldt)):
         raise ValueError("prob: a float32 vector with the stride of ids is wanted")
     if probs is None and want_probs:
         probs = torch.empty((rows, n), dtype=f32, device=logits.device)
     ldp = 0 if probs is None else _rows_of(probs, rows, n, f32, dev, "probs")
-    st = library().tfd_sample(
-        logits.data_ptr(), fmt, rows, n, ld, _vec(temperature, f32, rows, dev, "temperature"),
-        _vec(top_k, i32, rows, dev, "top_k"), _vec(top_p, f32, rows, dev, "top_p"),
-        _vec(min_p, f32, rows, dev, "min_p"), _vec(u, f32, rows, dev, "u"),
-        _vec(id_map, i32, n, dev, "id_map"), ids.data_ptr(), _p(prob), ldt, _p(probs), ldp,
-        _vec(dev_status, i32, 1, dev, "dev_status"), _stream(stream))
+    st = (_lib or library()).tfd_sample(
+        logits.data_ptr(), X_F32 if kind is f32 else X_BF16, rows, n, ld,
+        vec(temperature, f32, rows, dev, "temperature"), vec(top_k, i32, rows, dev, "top_k"),
+        vec(top_p, f32, rows, dev, "top_p"), vec(min_p, f32, rows, dev, "min_p"),
+        vec(u, f32, rows, dev, "u"), vec(id_map, i32, n, dev, "id_map"), ids.data_ptr(),
+        None if prob is None else prob.data_ptr(), ldt if rows > 1 else 1,
+        None if probs is None else probs.data_ptr(), ldp,
+        vec(dev_status, i32, 1, dev, "dev_status"), _stream(stream, dev))
     if st:
         _check("tfd_sample", st)
     return ids, prob, probs
@@ -404,34 +406,37 @@ def tfd_accept_sampled(p, q, drafts, n_asked, u, u_next, q_map=None, n_kept=None
     target's p [streams][win + 1][n], with the random numbers u [streams][win], and the next token
     drawn with u_next [streams]. q_map [n] gives a token's column in q (-1: none). The streams and
     steps of p and q are contiguous but for the row stride. Returns (n_kept, next_ids, next_prob)."""
-    f32, i32, dev = torch.float32, torch.int32, _current_device()
+    f32, i32, dev, vec = torch.float32, torch.int32, _current_device(), _vec
     streams, win = drafts.shape
-    n, nq = p.shape[2], q.shape[2]
-    lds = []
-    for t, steps, name in ((p, win + 1, "p"), (q, win, "q")):
-        cols = t.shape[2]
-        s0, s1, s2 = t.stride()
-        if t.dtype is not f32 or t.get_device() != dev or t.shape != (streams, steps, cols) or \
-                (cols > 1 and s2 != 1) or (streams > 1 and s0 != steps * s1):
-            raise ValueError(f"{name}: float32 [{streams}][{steps}][columns] with evenly spaced "
-                             "rows on the current CUDA device is wanted")
-        lds.append(max(cols, s1) if steps * streams == 1 else s1)
+    ps, pw, n = p.shape
+    qs, qw, nq = q.shape
+    p0, ldp, p2 = p.stride()
+    q0, ldq, q2 = q.stride()
+    if p.dtype is not f32 or p.get_device() != dev or ps != streams or pw != win + 1 or \
+            (p2 != 1 and n > 1) or (p0 != pw * ldp and streams > 1):
+        raise ValueError(f"p: float32 [{streams}][{win + 1}][columns] with evenly spaced rows on the "
+                         "current CUDA device is wanted")
+    if q.dtype is not f32 or q.get_device() != dev or qs != streams or qw != win or \
+            (q2 != 1 and nq > 1) or (q0 != qw * ldq and streams > 1):
+        raise ValueError(f"q: float32 [{streams}][{win}][columns] with evenly spaced rows on the "
+                         "current CUDA device is wanted")
+    if streams * win == 1:                               # a stride of one row says nothing
+        ldq = max(ldq, nq)
     if n_kept is None:
         n_kept = torch.empty(streams, dtype=i32, device=p.device)
     if next_ids is None:
         next_ids = torch.empty(streams, dtype=i32, device=p.device)
         if next_prob is None:
             next_prob = torch.empty(streams, dtype=f32, device=p.device)
-    st = library().tfd_accept_sampled(
-        p.data_ptr(), lds[0], q.data_ptr(), lds[1], n, nq, _vec(q_map, i32, n, dev, "q_map"),
-        _vec(drafts, i32, streams * win, dev, "drafts"),
-        _vec(n_asked, i32, streams, dev, "n_asked"), _vec(u, f32, streams * win, dev, "u"),
-        _vec(u_next, f32, streams, dev, "u_next"), streams, win,
-        _vec(n_kept, i32, streams, dev, "n_kept"), _vec(next_ids, i32, streams, dev, "next_ids"),
-        _vec(next_prob, f32, streams, dev, "next_prob"),
-        _vec(asked_hist, torch.int64, win, dev, "asked_hist"),
-        _vec(kept_hist, torch.int64, win, dev, "kept_hist"),
-        _vec(dev_status, i32, 1, dev, "dev_status"), _stream(stream))
+    st = (_lib or library()).tfd_accept_sampled(
+        p.data_ptr(), ldp, q.data_ptr(), ldq, n, nq, vec(q_map, i32, n, dev, "q_map"),
+        vec(drafts, i32, streams * win, dev, "drafts"), vec(n_asked, i32, streams, dev, "n_asked"),
+        vec(u, f32, streams * win, dev, "u"), vec(u_next, f32, streams, dev, "u_next"), streams, win,
+        vec(n_kept, i32, streams, dev, "n_kept"), vec(next_ids, i32, streams, dev, "next_ids"),
+        vec(next_prob, f32, streams, dev, "next_prob"),
+        vec(asked_hist, torch.int64, win, dev, "asked_hist"),
+        vec(kept_hist, torch.int64, win, dev, "kept_hist"),
+        vec(dev_status, i32, 1, dev, "dev_status"), _stream(stream, dev))
     if st:
         _check("tfd_accept_sampled", st)
     return n_kept, next_ids, next_prob
@@ -442,27 +447,27 @@ def tfd_lora(x, a, b, adapter_ids, base=None, y=None, scales=None, out_mode=OUT_
     """y[r] = base[r] + scales[i] * b[i] (a[i] x[r]), i = adapter_ids[r] (-1: none), for bf16 x
     [rows][k], a [adapters][rank][k], b [adapters][n][rank]. base (or None for zeros) and y have one
     type, float32 or bfloat16 (base's or y's, else out_mode); y may be base. Returns y."""
-    f32, bf, dev = torch.float32, torch.bfloat16, _current_device()
+    f32, bf, dev, vec = torch.float32, torch.bfloat16, _current_device(), _vec
     rows, k = x.shape
     na, rank, ka = a.shape
-    n = b.shape[1]
+    nb, n, rb = b.shape
+    if ka != k or nb != na or rb != rank:
+        raise ValueError("a [adapters][rank][k] and b [adapters][n][rank] do not fit x")
     like = y if y is not None else base
     if like is not None:
         out_mode = OUT_F32 if like.dtype is f32 else OUT_BF16
     dt = f32 if out_mode == OUT_F32 else bf
-    if ka != k or b.shape != (na, n, rank):
-        raise ValueError("a [adapters][rank][k] and b [adapters][n][rank] do not fit x")
     ldx = _rows_of(x, rows, k, bf, dev, "x")
     if y is None:
         y = torch.empty((rows, n), dtype=dt, device=x.device)
     ldy = _rows_of(y, rows, n, dt, dev, "y")
-    ldb = 0 if base is None else _rows_of(base, rows, n, dt, dev, "base")
-    st = library().tfd_lora(
-        x.data_ptr(), rows, k, ldx, _vec(a, bf, na * rank * k, dev, "a"),
-        _vec(b, bf, na * n * rank, dev, "b"), na, rank, n,
-        _vec(adapter_ids, torch.int32, rows, dev, "adapter_ids"),
-        _vec(scales, f32, na, dev, "scales"), out_mode, _p(base), ldb, y.data_ptr(), ldy,
-        _vec(dev_status, torch.int32, 1, dev, "dev_status"), _stream(stream))
+    ldb = 0 if base is None else ldy if base is y else _rows_of(base, rows, n, dt, dev, "base")
+    st = (_lib or library()).tfd_lora(
+        x.data_ptr(), rows, k, ldx, vec(a, bf, na * rank * k, dev, "a"),
+        vec(b, bf, na * n * rank, dev, "b"), na, rank, n,
+        vec(adapter_ids, torch.int32, rows, dev, "adapter_ids"), vec(scales, f32, na, dev, "scales"),
+        out_mode, None if base is None else base.data_ptr(), ldb, y.data_ptr(), ldy,
+        vec(dev_status, torch.int32, 1, dev, "dev_status"), _stream(stream, dev))
     if st:
         _check("tfd_lora", st)
     return y

@@ -60,7 +60,8 @@ def lora_call(**kw):
     (dict(y=FAKE), 1),                                          # y overlaps x
     (dict(base=FAKE * 2 + 200, ldb=100), 1),                    # y overlaps base, shifted
     (dict(base=FAKE * 2, ldb=104), 1),                          # the same base, another stride
-    (dict(rank=136), 2), (dict(na=4097), 2), (dict(rows=(1 << 22) + 1, y=FAKE << 20), 2),
+    (dict(rank=136), 2), (dict(na=4097), 2), (dict(rows=(1 << 18) + 1, y=FAKE << 20), 2),
+    (dict(a=FAKE * 2 + 16), 1), (dict(b=FAKE * 2 - 16), 1),     # y overlaps an adapter
 ])
 def test_lora_refusals(bad, code):
     assert lora_call(**bad) == code

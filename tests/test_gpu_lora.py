@@ -168,7 +168,8 @@ def test_binding_refuses_wrong_tensors():
 
 @pytest.mark.parametrize("R,k,n,rank,na", [
     (300, 64, 64, 8, 1), (513, 72, 77, 16, 1), (640, 264, 200, 24, 2), (1000, 1032, 130, 40, 3),
-    (777, 4096, 520, 64, 2), (1500, 512, 1000, 128, 5), (400, 128, 33, 96, 1)])
+    (777, 4096, 520, 64, 2), (1500, 512, 1000, 128, 5), (400, 128, 33, 96, 1),
+    (17000, 64, 1500, 64, 1), (24600, 72, 520, 16, 2), (20500, 64, 200, 128, 1)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("sort", [True, False])
 def test_prompts(R, k, n, rank, na, dtype, sort):
