@@ -494,6 +494,9 @@ __global__ void __launch_bounds__(kNT, 2) lora_tc_kernel(const Args a) {
 
 namespace {
 
+// An adapter's last tile is half full if nothing is known of the ids.
+int64_t likely_tiles(const Args& a) { return (a.rows + a.n_adapters * (kTM / 2) + kTM - 1) / kTM; }
+
 template <int kBufs>
 tfd_status launch(Args a, int dev, cudaStream_t stream, bool* taken) {
   const Layout l = layout(a.rank, a.f32, kBufs);
@@ -506,7 +509,7 @@ tfd_status launch(Args a, int dev, cudaStream_t stream, bool* taken) {
     return TFD_OK;
   // Blocks a tile: as many as give every block an SM of its own (two on one slow each other down
   // here, 4099 rows at rank 64: 4 blocks 48 us, 7 84), within one round of clusters.
-  const int64_t likely = (a.rows + kTM - 1) / kTM + a.n_adapters - 1;
+  const int64_t likely = likely_tiles(a);
   const int64_t tiles = (int64_t)a.rows / kTM + a.n_adapters + 1;
   const int sms = tfd_host::device_sms(dev);
   int c = 1;
@@ -527,7 +530,6 @@ tfd_status tfd_adapters::launch_tc(Args a, int dev, cudaStream_t stream, bool* t
   if (!a.vec || each < 96 || a.rows <= kSmallRows || a.k < kKB) return TFD_OK;
   // Three chunks let two blocks share an SM, which pays once there are more tiles than SMs (32768 rows
   // at rank 64: 264 us, with four 328); a block alone hides more behind four (16384 rows: 147 and 156).
-  const int64_t likely = (a.rows + kTM - 1) / kTM + a.n_adapters - 1;
-  if (likely > tfd_host::device_sms(dev)) return launch<3>(a, dev, stream, taken);
+  if (likely_tiles(a) > tfd_host::device_sms(dev)) return launch<3>(a, dev, stream, taken);
   return launch<4>(a, dev, stream, taken);
 }
