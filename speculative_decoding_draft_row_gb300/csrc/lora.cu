@@ -39,9 +39,15 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
 
 __device__ __forceinline__ uint4 zero4() { return make_uint4(0u, 0u, 0u, 0u); }
 
+// Blocks an SM. The expand waits for what it reads: three of the smallest form, whose 80 registers hold
+// without a spill, keep more of it in flight (16 rows over a 163840-row head at rank 16: 15.5 us, two
+// 16.9; four of 64 registers spill, 19.2).
+template <int RT, int NT>
+constexpr int kBlocks = RT == 1 && NT == 1 ? 3 : 2;
+
 // RT: 16-rank tiles (rank <= 16 RT); NT: 8-row tiles of x (TM = 8 NT).
 template <int RT, int NT>
-__global__ void __launch_bounds__(kT, 2) lora_kernel(const Args a) {
+__global__ void __launch_bounds__(kT, kBlocks<RT, NT>) lora_kernel(const Args a) {
   constexpr int TM = 8 * NT, R = 16 * RT, RP = R + 4;  // RP: partial sums without bank conflicts
   constexpr int MT = (TM + 15) / 16, HT = 16 * MT;     // row tiles of the expand
   constexpr int KP = RT == 1 ? 1 : RT / 2;             // 16-byte (RT 1: 8-byte) pieces of a B row
@@ -336,10 +342,16 @@ extern "C" tfd_status tfd_lora(const void* x, int rows, int64_t k, int64_t ldx, 
   const int64_t wide = k > n ? k : n;
   int c = 1, splits = 1;
   while (c < 8 && likely * c * 2 <= 2 * sms && wide / (c * 2) >= 32 * kW) c *= 2;
-  if (c == 8)
-    while (likely * c * splits * 2 <= 2 * sms && n / (c * splits * 2) >= 32 * kW &&
+  if (c == 8) {  // within one round of clusters
+    const size_t room = 16 * 1024;
+    const int at_once =
+        rt == 1 && nt == 1
+            ? tfd_host::clusters_at_once<lora_kernel<1, 1>>(dev, c, kT, room)
+            : tfd_host::clusters_at_once<lora_kernel<4, 1>>(dev, c, kT, room);
+    while (likely * (splits + 1) <= at_once && n / (c * (splits + 1)) >= 32 * kW &&
            n / splits >= 2 * k)
-      splits *= 2;
+      ++splits;
+  }
   Args a = {(const __nv_bfloat16*)x, ldx, (const __nv_bfloat16*)a_w, (const __nv_bfloat16*)b_w,
             adapter_ids, scales, (const char*)base, (char*)y, ldb, ldy, dev_status, rows, (int)k,
             (int)n, rank, n_adapters, splits, 0, es == 4, vec};
