@@ -349,8 +349,9 @@ tfd_status tfd_absorb(const void* k_rows, const void* v_rows, const void* k_gamm
  *   ids      device int32, row r at ids[r * ldt] (ldt 0 = 1), so that the tokens of one step can
  *            land in a column of a [streams][steps] array; prob device float or NULL, the same
  *            stride: the token's probability in the filtered distribution.
- *   probs    device float [rows][ldp] or NULL, ldp >= n, not overlapping the logits: the filtered,
- *            normalised distribution by column (written in full, zeros where nothing is kept).
+ *   probs    device float [rows][ldp] or NULL, ldp >= n: the filtered, normalised distribution by
+ *            column (written in full, zeros where nothing is kept).
+ *   The outputs' ranges (strides included) overlap no input: TFD_ERR_INVALID.
  *   A negative, infinite or NaN temperature, a NaN top_p or min_p, or a u outside [0, 1) sets
  *   TFD_ERR_DEVICE_DATA; that row gets id -1, probability 0 and a distribution of zeros.
  */
@@ -384,7 +385,7 @@ tfd_status tfd_sample(const void* logits, int lfmt, int rows, int64_t n, int64_t
  *            token's probability in the distribution it was drawn from.
  *   asked_hist, kept_hist device int64 [win] or NULL (both or neither), accumulated as in
  *            tfd_accept. streams >= 1; win 1..512; n, nq <= TFD_MAX_DRAW_COLS. p and q at
- *            any element-aligned base and row stride.
+ *            any element-aligned base and row stride. Outputs overlap no input.
  *   An n_asked outside [0, win], an asked draft outside [0, n), or a u outside [0, 1) sets
  *   TFD_ERR_DEVICE_DATA; that stream keeps 0, gets next token -1 and adds nothing.
  */

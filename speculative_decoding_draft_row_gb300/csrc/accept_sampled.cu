@@ -285,6 +285,17 @@ extern "C" tfd_status tfd_accept_sampled(const float* p, int64_t ldp, const floa
                         (const void*)next_ids, (const void*)next_prob, (const void*)dev_status})
     if (x && !aligned(x, 4)) return TFD_ERR_INVALID;
   if (asked_hist && (!aligned(asked_hist, 8) || !aligned(kept_hist, 8))) return TFD_ERR_INVALID;
+  // outputs apart from the inputs: a stream's blocks read them for themselves
+  const int64_t four = (int64_t)streams * 4;
+  const struct { const void* p; int64_t bytes; } outs[] = {
+      {n_kept, four}, {next_ids, four}, {next_prob, four}, {asked_hist, (int64_t)win * 8},
+      {kept_hist, (int64_t)win * 8}},
+      ins[] = {{p, (((int64_t)streams * (win + 1) - 1) * ldp + n) * 4},
+               {q, (((int64_t)streams * win - 1) * ldq + nq) * 4}, {q_map, n * 4},
+               {drafts, four * win}, {n_asked, four}, {u, four * win}, {u_next, four}};
+  for (const auto& o : outs)
+    for (const auto& i : ins)
+      if (tfd_host::overlap(o.p, o.bytes, i.p, i.bytes)) return TFD_ERR_INVALID;
   // blocks a stream: the fewest rounds of what the device holds at once, each costing about as much
   // as 4096 columns besides its blocks' own
   int dev = 0;

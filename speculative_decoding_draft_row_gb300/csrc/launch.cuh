@@ -22,6 +22,12 @@ inline int device_sms(int& dev) {
   return n;
 }
 
+// Whether two ranges of memory share a byte; a null one shares none.
+inline bool overlap(const void* p, int64_t bytes, const void* q, int64_t qbytes) {
+  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+  return p && q && a < b + (uint64_t)qbytes && b < a + (uint64_t)bytes;
+}
+
 // How many clusters of c blocks of a kernel run at once on the current device (asked of the runtime
 // once a device and Class of launches, for one with `smem` bytes): clusters do not cross the GPU's
 // partitions of SMs, so for large c it is well below (SMs * blocks an SM) / c (c = 16 at two blocks

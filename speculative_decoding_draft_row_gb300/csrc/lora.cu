@@ -312,13 +312,13 @@ extern "C" tfd_status tfd_lora(const void* x, int rows, int64_t k, int64_t ldx, 
       !aligned(base, es) || !aligned(adapter_ids, 4) || !aligned(scales, 4) ||
       !aligned(dev_status, 4))
     return TFD_ERR_INVALID;
-  auto overlap = [&](const void* p, int64_t bytes, const void* q, int64_t qbytes) {
-    return (const char*)p < (const char*)q + qbytes && (const char*)q < (const char*)p + bytes;
-  };
+  using tfd_host::overlap;
   const int64_t ybytes = (((int64_t)rows - 1) * ldy + n) * es;
   if (overlap(y, ybytes, x, (((int64_t)rows - 1) * ldx + k) * 2) ||
       overlap(y, ybytes, a_w, (int64_t)n_adapters * rank * k * 2) ||
-      overlap(y, ybytes, b_w, (int64_t)n_adapters * rank * n * 2))
+      overlap(y, ybytes, b_w, (int64_t)n_adapters * rank * n * 2) ||
+      overlap(y, ybytes, adapter_ids, (int64_t)rows * 4) ||
+      overlap(y, ybytes, scales, (int64_t)n_adapters * 4))
     return TFD_ERR_INVALID;
   if (base && !(base == y && ldb == ldy) &&
       overlap(y, ybytes, base, (((int64_t)rows - 1) * ldb + n) * es))

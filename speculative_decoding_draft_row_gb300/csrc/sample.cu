@@ -1106,10 +1106,15 @@ extern "C" tfd_status tfd_sample(const void* logits, int lfmt, int rows, int64_t
   if (ldt == 0) ldt = 1;
   const bool bf16 = lfmt == TFD_X_BF16;
   const int es = bf16 ? 2 : 4, ve = 16 / es;
-  const char* l0 = (const char*)logits;
-  const char* l1 = l0 + (((int64_t)rows - 1) * ld + n) * es;
-  const char* p0 = (const char*)probs;
-  if (probs && p0 < l1 && l0 < p0 + (((int64_t)rows - 1) * ldp + n) * 4) return TFD_ERR_INVALID;
+  // outputs apart from the inputs: a row's blocks read them for themselves
+  const int64_t last = (int64_t)rows - 1, four = (int64_t)rows * 4;
+  const struct { const void* p; int64_t bytes; } outs[] = {
+      {ids, (last * ldt + 1) * 4}, {prob, (last * ldt + 1) * 4}, {probs, (last * ldp + n) * 4}},
+      ins[] = {{logits, (last * ld + n) * es}, {temperature, four}, {top_k, four}, {top_p, four},
+               {min_p, four}, {u, four}, {id_map, n * 4}};
+  for (const auto& o : outs)
+    for (const auto& i : ins)
+      if (tfd_host::overlap(o.p, o.bytes, i.p, i.bytes)) return TFD_ERR_INVALID;
 
   const int64_t nv = (n + ve - 1) / ve + 1;  // one more where a row starts off a 16-byte boundary
   const size_t fixed = (sizeof(Shared) + 15) / 16 * 16;

@@ -24,6 +24,17 @@ def test_sample_refusals(bad, code):
     assert sample_call(**bad) == code
 
 
+@pytest.mark.parametrize("out", ["ids", "prob", "probs"])
+@pytest.mark.parametrize("inp", ["x", "t", "k", "p", "mp", "u", "m"])
+def test_sample_overlaps(out, inp):
+    """An output that shares its last bytes with an input."""
+    a = {name: FAKE * (i + 1) for i, name in
+         enumerate(["x", "t", "k", "p", "mp", "u", "m", "ids", "prob", "probs"])}
+    size = dict(ids=8 * 4, prob=8 * 4, probs=(7 * 120 + 100) * 4)[out]
+    a[inp] = a[out] + size - 4 if inp != "x" else a[out] + size - 16
+    assert sample_call(rows=8, ldp=120, **a) == 1
+
+
 def accept_sampled_call(**kw):
     a = dict(p=FAKE, ldp=100, q=FAKE, ldq=100, n=100, nq=100, m=None, d=FAKE, na=FAKE, u=FAKE,
              un=FAKE, streams=4, win=5, nk=FAKE, nx=FAKE, pr=None, ah=None, kh=None, st=None,
@@ -44,6 +55,16 @@ def test_accept_sampled_refusals(bad, code):
     assert accept_sampled_call(**bad) == code
 
 
+@pytest.mark.parametrize("out", ["nk", "nx", "pr", "ah", "kh"])
+@pytest.mark.parametrize("inp", ["p", "q", "m", "d", "na", "u", "un"])
+def test_accept_sampled_overlaps(out, inp):
+    """An output that is, or ends in, an input."""
+    a = {name: FAKE * (i + 1) for i, name in
+         enumerate(["p", "q", "m", "d", "na", "u", "un", "nk", "nx", "pr", "ah", "kh"])}
+    for at in (a[out], a[out] + (40 if out in ("ah", "kh") else 16) - 4):
+        assert accept_sampled_call(**dict(a, **{inp: at})) == 1
+
+
 def lora_call(**kw):
     a = dict(x=FAKE, rows=2, k=64, ldx=64, a=FAKE, b=FAKE, na=3, rank=8, n=100, ids=FAKE, s=None,
              out=2, base=None, ldb=0, y=FAKE * 2, ldy=100, st=None, stream=None)
@@ -62,6 +83,7 @@ def lora_call(**kw):
     (dict(base=FAKE * 2, ldb=104), 1),                          # the same base, another stride
     (dict(rank=136), 2), (dict(na=4097), 2), (dict(rows=(1 << 18) + 1, y=FAKE << 20), 2),
     (dict(a=FAKE * 2 + 16), 1), (dict(b=FAKE * 2 - 16), 1),     # y overlaps an adapter
+    (dict(ids=FAKE * 2 + 396), 1), (dict(s=FAKE * 2 - 8), 1),   # y overlaps ids, scales
 ])
 def test_lora_refusals(bad, code):
     assert lora_call(**bad) == code
