@@ -13,8 +13,12 @@
 // and split into bf16 parts that add up to them (two where y is bf16: 2^-17 relative, under its 2^-9
 // rounding; three, all 24 bits, where it is fp32). Expand: D2 = h B^T in chunks of outputs that are
 // 128 bytes of a row of y, the parts' products added in the same fp32 accumulators; a chunk's B and base
-// rows are copied two chunks ahead, the base chunk takes the sums and is written out from shared
-// memory in whole 128-byte rows.
+// rows are copied ahead, its products run while the chunk before it is written, its base takes the
+// sums and is written out from shared memory in whole 128-byte rows.
+//
+// Measured, 4096 to 4096 in bf16: 4099 rows of six adapters at rank 64 in 44.6 us, 0.35 of the copy
+// rate (62.7 with the sums read by every block, 54.4 with a chunk's products waited for); 16384 rows 148
+// us, 0.40; 32768 rows 264 us, 0.45. Bound by the latency of the copies in flight, not by the MMAs.
 #include <cooperative_groups.h>
 
 #include "lora.cuh"

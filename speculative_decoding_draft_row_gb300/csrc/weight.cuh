@@ -20,7 +20,6 @@
 
 namespace tfd {
 
-constexpr int kFixBits = 43;               // one = 2^43
 constexpr float kCutLog2 = -44.0f;         // below this s a weight is zero
 constexpr int64_t kMaxDrawCols = 1 << 20;  // sums of this many weights stay at or below 2^63
 
