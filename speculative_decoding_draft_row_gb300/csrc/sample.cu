@@ -40,7 +40,7 @@ constexpr int kW = kT / 32;
 constexpr int kBins = 1024;
 constexpr int kPer = kBins / kT;
 constexpr int kList = 1024;      // columns of a list
-constexpr int kRank = 128;       // lists up to here are ranked outright
+constexpr int kRank = 128;       // lists up to here are ranked outright (256: up to 10 us more)
 constexpr int kMaxC = 16;
 constexpr int kMaxPart = 65536;  // columns of a block, or a few more: 15-bit pieces sum within 32 bits
 
@@ -920,16 +920,17 @@ struct Sampler {
     }
     if (!all_listed && !open) {  // everything that min_p keeps
       uint64_t sum = 0;
-      for (int v = vbeg + lane; v < vend; v += 32) {
-        const uint4 r = get(v);
-        bool any = false;
+      if (minw) {
+        sum = lane_share(-INFINITY, 0);
+      } else {
+        for (int v = vbeg + lane; v < vend; v += 32) {
+          const uint4 r = get(v);
+          bool any = false;
 #pragma unroll
-        for (int j = 0; j < VE; ++j) any |= elem(r, j) >= lfloor;
-        if (!any) continue;
+          for (int j = 0; j < VE; ++j) any |= elem(r, j) >= lfloor;
+          if (!any) continue;
 #pragma unroll
-        for (int j = 0; j < VE; ++j) {
-          const uint64_t w = weight(elem(r, j));
-          sum += w >= minw ? w : 0;
+          for (int j = 0; j < VE; ++j) sum += weight(elem(r, j));
         }
       }
       sum = block_sum(sum);
@@ -967,9 +968,7 @@ struct Sampler {
     lfloor = fmaxf(lfloor, tval);
     if (target >= before && target < before + mine) {
       if (open) {  // way C: the warps' kept masses, column by column
-        uint64_t sum = 0;
-        for (int v = vbeg + lane; v < vend; v += 32) sum += kept_weights(v, tval, tkey, nullptr);
-        block_sum(sum);
+        block_sum(lane_share(tval, tkey));
       }
       uint64_t ws = 0;  // the warp whose columns hold it
       if (lane < kW)
@@ -993,7 +992,7 @@ struct Sampler {
   }
   // The kept weights of 16 bytes of columns, and their sum.
   __device__ __forceinline__ uint64_t kept_weights(int v, float tval, uint64_t tkey,
-                                                   uint64_t* w) const {
+                                                   uint64_t (&w)[VE]) const {
     const uint4 r = get(v);
     uint64_t sum = 0;
 #pragma unroll
@@ -1004,8 +1003,44 @@ struct Sampler {
         x = weight(l);
         if (x < minw) x = 0;
       }
-      if (w) w[j] = x;
+      w[j] = x;
       sum += x;
+    }
+    return sum;
+  }
+
+  // This lane's share of the warp's kept mass. Kept columns are few as a rule, so they queue in shared
+  // memory (the histogram's, done with) and are weighed 32 at a time (96 x 163840: 148 to 140 us).
+  __device__ __forceinline__ uint64_t lane_share(float tval, uint64_t tkey) {
+    float* queue = reinterpret_cast<float*>(sh.w.lo) + warp * 64;
+    uint64_t sum = 0;
+    int cnt = 0;
+#pragma unroll 1
+    for (int v0 = vbeg; v0 < vend; v0 += 32) {
+      const int v = v0 + lane;
+      const uint32_t none = BF16 ? 0x7FC07FC0u : 0x7FC00000u;
+      uint4 r = make_uint4(none, none, none, none);
+      if (v < vend) r = get(v);
+#pragma unroll
+      for (int j = 0; j < VE; ++j) {
+        const float l = elem(r, j);
+        const bool on = l >= lfloor && above(l, v * VE + j - off, tval, tkey);
+        const unsigned who = __ballot_sync(0xffffffffu, on);
+        if (on) queue[cnt + __popc(who & ((1u << lane) - 1))] = l;
+        cnt += __popc(who);
+        if (cnt >= 32) {
+          __syncwarp();
+          const uint64_t w = weight(queue[cnt - 32 + lane]);
+          sum += w >= minw ? w : 0;
+          cnt -= 32;
+          __syncwarp();
+        }
+      }
+    }
+    __syncwarp();
+    if (lane < cnt) {
+      const uint64_t w = weight(queue[lane]);
+      sum += w >= minw ? w : 0;
     }
     return sum;
   }
