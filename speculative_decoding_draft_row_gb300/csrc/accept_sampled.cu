@@ -84,6 +84,7 @@ struct Shared {
 
 __global__ void __launch_bounds__(kT) accept_sampled_kernel(const Args a) {
   __shared__ Shared sh;
+  tfd_host::after_previous();
   cg::cluster_group cl = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();

@@ -62,6 +62,7 @@ __global__ void __launch_bounds__(kT, kBlocks<RT, NT>) lora_kernel(const Args a)
   float* mine = part + kW * TM * RP;                             // [TM][RP], read by the cluster
   __nv_bfloat16* hs = reinterpret_cast<__nv_bfloat16*>(mine + TM * RP);  // [3][HT][HP]
   __shared__ int32_t tile_rows[TM];
+  tfd_host::after_previous();
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), rank_c = (int)cl.block_rank();
   const int unit = blockIdx.x / C, tile = unit / a.splits, split = unit % a.splits;

@@ -168,6 +168,7 @@ __global__ void __launch_bounds__(kNT, 2) lora_tc_kernel(const Args a) {
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   __shared__ int32_t tile_rows[kTM];
+  tfd_host::after_previous();
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), rank_c = (int)cl.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

@@ -1119,6 +1119,7 @@ struct Sampler {
 template <bool BF16, bool KEEP>
 __global__ void __launch_bounds__(kT, 2) sample_kernel(const Args a) {
   extern __shared__ __align__(16) unsigned char smem[];
+  tfd_host::after_previous();
   Shared& sh = *reinterpret_cast<Shared*>(smem);
   uint4* keep = reinterpret_cast<uint4*>(smem + ((sizeof(Shared) + 15) / 16) * 16);
   Sampler<BF16, KEEP> s(a, sh, keep);
