@@ -16,7 +16,7 @@
 // rows are copied ahead, its products run while the chunk before it is written, its base takes the
 // sums and is written out from shared memory in whole 128-byte rows.
 //
-// Measured, 4096 to 4096 in bf16: 4099 rows of six adapters at rank 64 in 44.6 us, 0.35 of the copy
+// Measured, 4096 to 4096 in bf16: 4099 rows of six adapters at rank 64 in 44.1 us, 0.36 of the copy
 // rate (62.7 with the sums read by every block, 54.4 with a chunk's products waited for); 16384 rows 148
 // us, 0.40; 32768 rows 264 us, 0.45. Bound by the latency of the copies in flight, not by the MMAs.
 #include <cooperative_groups.h>

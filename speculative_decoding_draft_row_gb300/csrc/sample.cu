@@ -22,9 +22,9 @@
 // each block for itself and need no further barrier.
 //
 // Bound by the barriers and the block's work between them where rows are few (1 x 4096 with all
-// filters 11.4 us, 4 x 163840 with top-p and distributions 31.9, 16 x 163840 bf16 with mixed filters
-// 39.5), by the weights' instructions where they are many (33 x 50021 without filters 15.1 us, 96 x
-// 163840 with mixed filters and distributions 148, of 19 for the bytes).
+// filters 11.0 us, 4 x 163840 with top-p and distributions 31.7, 16 x 163840 bf16 with mixed filters
+// 37.9), by the weights' instructions where they are many (33 x 50021 without filters 14.3 us, 96 x
+// 163840 with mixed filters and distributions 137, of 19 for the bytes).
 #include <cooperative_groups.h>
 
 #include "launch.cuh"

@@ -195,3 +195,34 @@ def test_prompts(R, k, n, rank, na, dtype, sort):
     torch.cuda.synchronize()
     check(z[:, :n], x, a, b, ids, None, None, "no base")
     assert not z[:, :n][ids == -1].any()
+
+
+@pytest.mark.parametrize("R,k,n,rank,na", [(3, 128, 256, 16, 2), (16, 512, 8000, 16, 4),
+                                           (1000, 256, 512, 64, 2)])
+def test_calls_in_a_row(R, k, n, rank, na):
+    """Each call of a run in one stream reads what the one before it wrote, eager and captured: the
+    launches are placed early and must still wait for each other's results."""
+    need_gpu()
+    x, a, b, ids, base, s = make(R, k, n, rank, na, torch.float32, seed=11)
+    s = 0.1 * s
+    want = base.clone()
+    for _ in range(12):
+        tfd.tfd_lora(x, a, b, ids, base=want, y=want, scales=s)
+        torch.cuda.synchronize()
+    y = base.clone()
+    torch.cuda.synchronize()
+    for _ in range(12):
+        tfd.tfd_lora(x, a, b, ids, base=y, y=y, scales=s)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+    y.copy_(base)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y.copy_(base)
+        for _ in range(12):
+            tfd.tfd_lora(x, a, b, ids, base=y, y=y, scales=s)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)

@@ -156,3 +156,35 @@ def test_unknown_projection_is_refused():
     need_gpu()
     with pytest.raises(ValueError):
         build(("wq",))
+
+
+def test_draw_then_accept_in_a_row():
+    """Drafts drawn into the columns of an array, their distributions written beside, and the accept
+    that reads both, without a wait between the calls: the same as with one."""
+    need_gpu()
+    S, W, n = 3, 4, 9001
+    g = torch.Generator().manual_seed(3)
+    lq = 3 * torch.randn((W, S, n), generator=g).cuda()
+    lp = (2.5 * torch.randn((S * (W + 1), n), generator=g)).cuda()
+    u = torch.rand((2 * W + 3, S), generator=g).cuda()
+    up = torch.rand(S * (W + 1), generator=g).cuda()
+    asked = torch.full((S,), W, dtype=torch.int32, device="cuda")
+
+    def step(sync):
+        drafts = torch.empty((S, W), dtype=torch.int32, device="cuda")
+        q = torch.empty((S, W, n), device="cuda")
+        for t in range(W):
+            tfd.tfd_sample(lq[t], u[t], ids=drafts[:, t], probs=q[:, t])
+            sync()
+        p = tfd.tfd_sample(lp, up, want_probs=True)[2]
+        sync()
+        out = tfd.tfd_accept_sampled(p.view(S, W + 1, n), q, drafts, asked,
+                                     u[W:2 * W].t().contiguous(), u[2 * W])
+        sync()
+        return [drafts, q, p, *out]
+
+    want = step(torch.cuda.synchronize)
+    for _ in range(5):
+        got = step(lambda: None)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
