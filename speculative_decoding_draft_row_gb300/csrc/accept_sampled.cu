@@ -12,7 +12,7 @@
 // warp sums a contiguous part of the columns, and after one cluster barrier the block that holds
 // the drawn column scans the part of the warp that holds it with all its threads.
 //
-// 4 x 5 x 163840 takes 7.5 us, all latency; 48 x 5 x 163840 18.3 us, 0.51 of the copy rate (one row
+// 4 x 5 x 163840 takes 7.5 us, all latency; 48 x 5 x 163840 17.6 us, 0.53 of the copy rate (one row
 // of p and one of q a stream, 63 MB).
 #include <cooperative_groups.h>
 

@@ -77,11 +77,12 @@ bool allow_clusters(int dev, int max_smem) {
   return true;
 }
 
-// First in a kernel that launch_clusters starts: lets the next such kernel of the stream be placed while
-// this one runs, and waits until the one before has ended and its results can be read. Calls in a row
-// without a graph are 1-2 us shorter for it (1 x 4096 drawn 15.0 to 12.8 us), graph nodes 0.4.
+// First in a kernel that launch_clusters starts, whose blocks are placed while the kernel before it in the
+// stream ends: waits until that one has, and its results can be read. Calls in a row without a graph
+// are 1-2 us shorter for it (1 x 4096 drawn 15.0 to 12.5 us), graph nodes 0.4. Placing the blocks
+// earlier still, where the one before has only just begun, cost full launches a third (96 x 163840,
+// top-k 50: 35 to 55 us): they go where room is, not where they would spread best.
 __device__ __forceinline__ void after_previous() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 

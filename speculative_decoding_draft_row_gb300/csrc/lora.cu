@@ -19,8 +19,8 @@
 // h stays in fp32 and enters the MMAs as two (bf16 outputs: 2^-17 relative, under a 2^-9 rounding) or
 // three (fp32 outputs: all 24 bits) bf16 parts, whose products are exact in the fp32 accumulators.
 //
-// Bound by latency: one row 4096 to 4096 at rank 16 takes 5.1 us, 16 rows 11008 to 4096 of eight
-// adapters at rank 32 7.8, 16 rows over a 163840-row head of four adapters at rank 16 15.3 (42 MB,
+// Bound by latency: one row 4096 to 4096 at rank 16 takes 5.3 us, 16 rows 11008 to 4096 of eight
+// adapters at rank 32 7.4, 16 rows over a 163840-row head of four adapters at rank 16 15.3 (42 MB,
 // 0.41 of the copy rate). L2 prefetches of what the expand reads made them slower by 0.6 to 2 us.
 #include <cooperative_groups.h>
 

@@ -22,9 +22,9 @@
 // each block for itself and need no further barrier.
 //
 // Bound by the barriers and the block's work between them where rows are few (1 x 4096 with all
-// filters 11.0 us, 4 x 163840 with top-p and distributions 31.7, 16 x 163840 bf16 with mixed filters
-// 37.9), by the weights' instructions where they are many (33 x 50021 without filters 14.3 us, 96 x
-// 163840 with mixed filters and distributions 137, of 19 for the bytes).
+// filters 10.9 us, 4 x 163840 with top-p and distributions 30.2, 16 x 163840 bf16 with mixed filters
+// 37.3), by the weights' instructions where they are many (33 x 50021 without filters 14.3 us, 96 x
+// 163840 with mixed filters and distributions 133, of 19 for the bytes).
 #include <cooperative_groups.h>
 
 #include "launch.cuh"
@@ -81,6 +81,7 @@ struct Shared {
   uint64_t ctail[kMaxC];          // and below the histogram
   uint64_t klo[kMaxC], khi[kMaxC];
   uint64_t wsum[kW];              // this block's warps
+  uint64_t part[kMaxC][kW];       // and the other blocks' shares of their sums
   uint64_t w64[kW], x64[kW];
   uint32_t w32[kW];
   float wext[3][kW];
@@ -921,7 +922,7 @@ struct Sampler {
     if (!all_listed && !open) {  // everything that min_p keeps
       uint64_t sum = 0;
       if (minw) {
-        sum = lane_share(-INFINITY, 0);
+        sum = lane_share<KEEP>(vbeg, vend, -INFINITY, 0);
       } else {
         for (int v = vbeg + lane; v < vend; v += 32) {
           const uint4 r = get(v);
@@ -954,22 +955,39 @@ struct Sampler {
       }
     }
     __syncthreads();
-    uint64_t z = 0, before = 0, mine = 0;
-    for (int c = 0; c < C; ++c) {
-      const uint64_t x = (all_listed ? 0 : sh.cdef[buf][c]) +
-                         pieces(sh.cw3[0][c], sh.cw3[1][c], sh.cw3[2][c]);
-      if (c < rank) before += x;
-      if (c == rank) mine = x;
-      z += x;
-    }
+    auto block_mass = [&](int c) {
+      return (all_listed ? 0 : sh.cdef[buf][c]) +
+             pieces(sh.cw3[0][c], sh.cw3[1][c], sh.cw3[2][c]);
+    };
+    uint64_t z = 0, before = 0;
+    for (int c = 0; c < C; ++c) z += block_mass(c);
     const uint64_t target = mul_frac(u, z, false);
+    int owner = 0;  // the block that holds the drawn column
+    for (; owner < C - 1; ++owner) {
+      const uint64_t x = block_mass(owner);
+      if (target < before + x) break;
+      before += x;
+    }
     const float zf = 1.0f / (__ull2float_rn(z) * (1.0f / 8796093022208.0f));
     const float tval = tkey ? key_value(tkey) : -INFINITY;
     lfloor = fmaxf(lfloor, tval);
-    if (target >= before && target < before + mine) {
-      if (open) {  // way C: the warps' kept masses, column by column
-        block_sum(lane_share(tval, tkey));
+    // Way C: the kept masses of that block's warps, column by column: a share by every block (96 x 163840
+    // with top-p 0.9: 116 us by that block alone, 107 so).
+    if (open) {
+      const int v0 = owner * nvc + warp * nvw;
+      const int v1 = min(min(v0 + nvw, owner * nvc + nvc), nvrow);
+      const int per = (max(v1 - v0, 0) + C - 1) / C, from = v0 + rank * per;
+      const uint64_t sum = warp_sum64(lane_share<false>(from, min(from + per, v1), tval, tkey));
+      if (lane == 0) *cl.map_shared_rank(&sh.part[rank][warp], owner) = sum;
+      cl.sync();
+      if (tid < kW) {
+        uint64_t t = 0;
+        for (int c = 0; c < C; ++c) t += sh.part[c][tid];
+        sh.wsum[tid] = t;
       }
+      __syncthreads();
+    }
+    if (rank == owner) {
       uint64_t ws = 0;  // the warp whose columns hold it
       if (lane < kW)
         ws = all_listed ? pieces(sh.ww3[0][lane], sh.ww3[1][lane], sh.ww3[2][lane]) : sh.wsum[lane];
@@ -1009,18 +1027,27 @@ struct Sampler {
     return sum;
   }
 
-  // This lane's share of the warp's kept mass. Kept columns are few as a rule, so they queue in shared
+  // This lane's share of the kept mass of the 16-byte pieces from beg to end, which are the warp's (of
+  // this block's own columns or another's). Kept columns are few as a rule, so they queue in shared
   // memory (the histogram's, done with) and are weighed 32 at a time (96 x 163840: 148 to 140 us).
-  __device__ __forceinline__ uint64_t lane_share(float tval, uint64_t tkey) {
+  template <bool OWN>
+  __device__ __forceinline__ uint64_t lane_share(int beg, int end, float tval, uint64_t tkey) {
     float* queue = reinterpret_cast<float*>(sh.w.lo) + warp * 64;
     uint64_t sum = 0;
     int cnt = 0;
 #pragma unroll 1
-    for (int v0 = vbeg; v0 < vend; v0 += 32) {
+    for (int v0 = beg; v0 < end; v0 += 32) {
       const int v = v0 + lane;
       const uint32_t none = BF16 ? 0x7FC07FC0u : 0x7FC00000u;
       uint4 r = make_uint4(none, none, none, none);
-      if (v < vend) r = get(v);
+      if (v < end) {
+        if (OWN) {
+          r = get(v);
+        } else {
+          r = load(v);
+          if (inf) r = only_inf(r);
+        }
+      }
 #pragma unroll
       for (int j = 0; j < VE; ++j) {
         const float l = elem(r, j);
