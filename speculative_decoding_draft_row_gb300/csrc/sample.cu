@@ -18,8 +18,8 @@
 //     it fits (equal logits differ by their ids, so this ends).
 // The blocks' kept masses then name the block that holds the drawn column, which finds the warp,
 // which scans its columns. The histogram is summed across the cluster through distributed shared
-// memory, a share of the bins by each block, into every block, so the steps behind it are done by
-// each block for itself and need no further barrier.
+// memory, a share of the bins by each block, into every block, so each finds the border's bin for
+// itself; the lists and, behind way C, the shares of that block's masses cost a barrier more each.
 //
 // Bound by the barriers and the block's work between them where rows are few (1 x 4096 with all
 // filters 10.9 us, 4 x 163840 with top-p and distributions 30.2, 16 x 163840 bf16 with mixed filters
