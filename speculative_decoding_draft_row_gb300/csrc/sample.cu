@@ -854,7 +854,11 @@ struct Sampler {
           list_weigh(ncand);
           const float mul = (float)kBins / (float)(b + 1);
           list_border(ncand, 0.0f, mul, 0, 0, (uint64_t)k, false);
-          if (use_p) list_border(ncand, 0.0f, mul, 0, 0, p_target(sh.zk), true);
+          if (use_p) {
+            const uint64_t zk = sh.zk;
+            __syncthreads();  // every thread has read it: a short list is ranked, and zk written, at once
+            list_border(ncand, 0.0f, mul, 0, 0, p_target(zk), true);
+          }
           tkey = sh.tkey;
           all_listed = true;
           open = false;
