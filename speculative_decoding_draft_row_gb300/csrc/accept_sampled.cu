@@ -26,7 +26,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kT = 256;
 constexpr int kW = kT / 32;
-constexpr int kMaxC = 16;
+constexpr int kMaxC = tfd_host::kMaxCluster;
 constexpr int kCols = 4;   // columns a lane takes at once
 constexpr int kBatch = 4;  // such loads in flight
 
@@ -305,17 +305,12 @@ extern "C" tfd_status tfd_accept_sampled(const float* p, int64_t ldp, const floa
   int dev = 0;
   tfd_host::device_sms(dev);
   if (!tfd_host::allow_clusters<accept_sampled_kernel>(dev, 0)) return TFD_ERR_CUDA;
-  int c = 1;
-  int64_t best = INT64_MAX;
-  for (int i = 1; i <= kMaxC; ++i) {
-    const int at_once = tfd_host::clusters_at_once<accept_sampled_kernel>(dev, i, kT, 0);
-    const int64_t rounds = (streams + at_once - 1) / at_once;
-    const int64_t cost = rounds * (4096 + 64 * i + n / i);
-    if (cost < best) {
-      best = cost;
-      c = i;
-    }
-  }
+  const int c = tfd_host::cheapest_cluster(
+      streams,
+      [&](int i) { return tfd_host::clusters_at_once<accept_sampled_kernel>(dev, i, kT, 0); },
+      [](int) { return true; },
+      [&](int i, int64_t rounds) { return rounds * (4096 + 64 * i + n / i); });
+  if (c == 0) return TFD_ERR_UNSUPPORTED;
   Args a = {p, ldp, q, ldq, n, nq, q_map, drafts, n_asked, u, u_next, win, n_kept, next_ids,
             next_prob, reinterpret_cast<unsigned long long*>(asked_hist),
             reinterpret_cast<unsigned long long*>(kept_hist), dev_status};

@@ -31,12 +31,14 @@ inline bool overlap(const void* p, int64_t bytes, const void* q, int64_t qbytes)
 // How many clusters of c blocks of a kernel run at once on the current device (asked of the runtime
 // once a device and Class of launches, for one with `smem` bytes): clusters do not cross the GPU's
 // partitions of SMs, so for large c it is well below (SMs * blocks an SM) / c (c = 16 at two blocks
-// an SM: 14, not 19).
+// an SM: 14, not 19). 0 where none can be placed, which is kept as well; -1 where the runtime did
+// not say, which is asked again the next time.
 constexpr int kMaxCluster = 16;
+constexpr int kPortable = 8;  // clusters up to here run on every device of the architecture
 template <auto Kernel, int Class = 0>
 int clusters_at_once(int dev, int c, int threads, size_t smem) {
-  static std::atomic<int> count[kMaxDevices][kMaxCluster + 1];
-  if (dev < 0 || dev >= kMaxDevices) return 1;
+  static std::atomic<int> count[kMaxDevices][kMaxCluster + 1];  // one more than the answer; 0: none yet
+  if (dev < 0 || dev >= kMaxDevices) return -1;
   int n = count[dev][c].load(std::memory_order_relaxed);
   if (n == 0) {
     cudaLaunchConfig_t cfg = {};
@@ -49,14 +51,38 @@ int clusters_at_once(int dev, int c, int threads, size_t smem) {
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, Kernel, &cfg) != cudaSuccess) {
+    int got = 0;
+    if (cudaOccupancyMaxActiveClusters(&got, Kernel, &cfg) != cudaSuccess || got < 0) {
       cudaGetLastError();
-      n = 0;
+      return -1;
     }
-    n = n > 0 ? n : 1;
+    n = got + 1;
     count[dev][c].store(n, std::memory_order_relaxed);
   }
-  return n;
+  return n - 1;
+}
+
+// The blocks a cluster, 1 to 16, at which `units` clusters cost least: cost(c, rounds) for rounds of
+// at_once(c) clusters (clusters_at_once). Sizes that fits(c) turns down or that cannot be placed are
+// left out; where the runtime does not say, a portable size counts as one cluster at a time, and a
+// larger one is taken only when nothing else is left. 0: no size will do.
+template <class AtOnce, class Fits, class Cost>
+int cheapest_cluster(int64_t units, AtOnce at_once, Fits fits, Cost cost) {
+  int c = 0, unknown = 0;
+  int64_t best = 0;
+  for (int i = 1; i <= kMaxCluster; ++i) {
+    if (!fits(i)) continue;
+    int n = at_once(i);
+    if (n < 0 && i > kPortable) unknown = i;
+    if (n == 0 || (n < 0 && i > kPortable)) continue;
+    if (n < 0) n = 1;
+    const int64_t x = cost(i, (units + n - 1) / n);
+    if (c == 0 || x < best) {
+      best = x;
+      c = i;
+    }
+  }
+  return c ? c : unknown;
 }
 
 // The first use of a kernel on a device: allows it `max_smem` bytes of dynamic shared memory and

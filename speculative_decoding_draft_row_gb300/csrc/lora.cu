@@ -347,13 +347,15 @@ extern "C" tfd_status tfd_lora(const void* x, int rows, int64_t k, int64_t ldx, 
   const int64_t wide = k > n ? k : n;
   int c = 1, splits = 1;
   while (c < 8 && likely * c * 2 <= 2 * sms && wide / (c * 2) >= 32 * kW) c *= 2;
+  const size_t room = 16 * 1024;
+  auto at_once = [&](int blocks) {
+    return rt == 1 && nt == 1
+               ? tfd_host::clusters_at_once<lora_kernel<1, 1>>(dev, blocks, kT, room)
+               : tfd_host::clusters_at_once<lora_kernel<4, 1>>(dev, blocks, kT, room);
+  };
+  while (c > 1 && at_once(c) == 0) c /= 2;  // no cluster of that size can be placed
   if (c == 8) {  // within one round of clusters
-    const size_t room = 16 * 1024;
-    const int at_once =
-        rt == 1 && nt == 1
-            ? tfd_host::clusters_at_once<lora_kernel<1, 1>>(dev, c, kT, room)
-            : tfd_host::clusters_at_once<lora_kernel<4, 1>>(dev, c, kT, room);
-    while (likely * (splits + 1) <= at_once && n / (c * (splits + 1)) >= 32 * kW &&
+    while (likely * (splits + 1) <= at_once(c) && n / (c * (splits + 1)) >= 32 * kW &&
            n / splits >= 2 * k)
       ++splits;
   }

@@ -41,7 +41,7 @@ constexpr int kBins = 1024;
 constexpr int kPer = kBins / kT;
 constexpr int kList = 1024;      // columns of a list
 constexpr int kRank = 128;       // lists up to here are ranked outright (256: up to 10 us more)
-constexpr int kMaxC = 16;
+constexpr int kMaxC = tfd_host::kMaxCluster;
 constexpr int kMaxPart = 65536;  // columns of a block, or a few more: 15-bit pieces sum within 32 bits
 
 struct Args {
@@ -1199,20 +1199,17 @@ extern "C" tfd_status tfd_sample(const void* logits, int lfmt, int rows, int64_t
   const size_t half = 112 * 1024;
   if (!tfd_host::allow_clusters<sample_kernel<false, true>>(dev, tfd_host::kSmemLimit))
     return TFD_ERR_CUDA;
-  int c = 0;
-  int64_t best = 0;
-  for (int i = 1; i <= kMaxC; ++i) {
-    if (i < kMaxC && n / i >= kMaxPart) continue;
-    const int at_once =
-        tfd_host::clusters_at_once<sample_kernel<false, true>>(dev, i, kT, half);
-    const int64_t rounds = (rows + at_once - 1) / at_once;
-    const int64_t cols = n / i, own = fixed + part(i) <= half ? cols : cols * 14 / 10;
-    const int64_t cost = rounds * (16384 + 256 * i + own);
-    if (c == 0 || cost < best) {
-      best = cost;
-      c = i;
-    }
-  }
+  const int c = tfd_host::cheapest_cluster(
+      rows,
+      [&](int i) {
+        return tfd_host::clusters_at_once<sample_kernel<false, true>>(dev, i, kT, half);
+      },
+      [&](int i) { return i == kMaxC || n / i < kMaxPart; },
+      [&](int i, int64_t rounds) {
+        const int64_t cols = n / i, own = fixed + part(i) <= half ? cols : cols * 14 / 10;
+        return rounds * (16384 + 256 * i + own);
+      });
+  if (c == 0) return TFD_ERR_UNSUPPORTED;
   const bool keep = fixed + part(c) <= half;
   const size_t smem = fixed + (keep ? part(c) : 0);
   Args a = {logits, n, ld, temperature, top_k, top_p, min_p, u, id_map, ids, prob, ldt, probs, ldp,
