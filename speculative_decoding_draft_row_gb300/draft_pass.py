@@ -23,6 +23,15 @@ import torch
 from . import tfd
 
 
+def unit_f32(v):
+    """Random numbers in [0, 1) as float32, still below 1: a double from 1 - 2^-25 on would round to
+    1, which the draws refuse. Numbers of 1 and more stay there."""
+    t = v if hasattr(v, "dtype") else torch.as_tensor(v, dtype=torch.float64)
+    t = torch.as_tensor(t)
+    f = t.to(torch.float32)
+    return f if t.dtype != torch.float64 else torch.where((t < 1) & (f >= 1), 1 - 2.0 ** -24, f)
+
+
 class DraftPass:
     def __init__(self, wo_codes, wo_scales, w2_codes, w2_scales, head, head_fmt, head_scales,
                  k_ring, v_ring, window, steps, eps=1e-6, rope_base=10000.0, adapters=None,
@@ -101,12 +110,14 @@ class DraftPass:
                       min_p=None, p_dist=None):
         """Copy a sampled pass's random numbers (u_draft [steps][S], u_accept [S][steps], u_next
         [S]), settings [S] and the target's distributions p_dist [S][steps + 1][vocab]."""
-        given = dict(u_draft=u_draft, u_accept=u_accept, u_next=u_next, temperature=temperature,
-                     top_k=top_k, top_p=top_p, min_p=min_p, p_dist=p_dist)
+        given = dict(temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p, p_dist=p_dist)
         for name, v in given.items():
             if v is not None:
                 buf = getattr(self, name)
                 buf.copy_(torch.as_tensor(v).to(buf.dtype), non_blocking=True)
+        for name, v in dict(u_draft=u_draft, u_accept=u_accept, u_next=u_next).items():
+            if v is not None:
+                getattr(self, name).copy_(unit_f32(v), non_blocking=True)
 
     def load_adapter_ids(self, ids):
         """Copy each stream's adapter (-1: none)."""
