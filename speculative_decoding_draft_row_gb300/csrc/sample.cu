@@ -679,11 +679,13 @@ struct Sampler {
     b.khi = ~0ull;
     b.n_above = sh.f_above_n;
     b.m_above = sh.f_above_m;
-    // min_p's cut clearly above this bin: it alone decides. Clearly below: it has no say.
+    // min_p's cut clearly above this bin: it alone decides. Clearly below: it has no say. In between
+    // the weights decide, column by column. __log2f is within 2^-21.4 (3.6e-7) absolute near 1, which
+    // is many bins where the row spans little (logits 20 apart at a temperature of 1e6: 2.9e-5 in all).
     if (minw) {
-      const float at = -log2_minp * binscale;
-      if (at < (float)b.bin - 1.0f) return -1;
-      if (at > (float)b.bin + 2.0f && b.bin < kBins - 1) minw = 0;
+      const float at = -log2_minp * binscale, unsure = 1.0f + 4e-7f * binscale;
+      if (at < (float)b.bin - unsure) return -1;
+      if (at > (float)b.bin + 1.0f + unsure && b.bin < kBins - 1) minw = 0;
     }
     // this block's mass above: from its histogram, or column by column where min_p has a say
     uint64_t sum = 0;
