@@ -163,13 +163,10 @@ __global__ void __launch_bounds__(kT, kBlocks<RT, NT>) lora_kernel(const Args a)
       float v = 0.0f;
       if (row < TM)
         for (int c = 0; c < C; ++c) v += cl.map_shared_rank(mine, c)[o];
-      v *= scale;
-      const __nv_bfloat16 h0 = __float2bfloat16_rn(v);
-      const float r1 = v - __bfloat162float(h0);
-      const __nv_bfloat16 h1 = __float2bfloat16_rn(r1);
-      hs[row * HP + i % R] = h0;
-      hs[(HT + row) * HP + i % R] = h1;
-      if (a.f32) hs[(2 * HT + row) * HP + i % R] = __float2bfloat16_rn(r1 - __bfloat162float(h1));
+      v = i % R < a.rank ? v * scale : 0.0f;  // past the adapter's ranks 0 x inf would be NaN
+      hs[row * HP + i % R] = take_part(v);
+      hs[(HT + row) * HP + i % R] = take_part(v);
+      if (a.f32) hs[(2 * HT + row) * HP + i % R] = take_part(v);
     }
     cl.barrier_arrive();  // this block has read the others' sums
     __syncthreads();

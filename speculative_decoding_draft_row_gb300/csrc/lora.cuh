@@ -28,6 +28,17 @@ struct Args {
   bool f32, vec;
 };
 
+// Takes the leading bf16 part off v, in which it stays within bf16's range: parts taken one after the
+// other add up to a finite v (24 bits in three). An infinity or NaN goes whole into its first part,
+// with zeros behind it: as a difference, inf - inf, the rest would make NaN of an infinite product.
+__device__ __forceinline__ __nv_bfloat16 take_part(float& v) {
+  const float most = __uint_as_float(0x7F7F0000u);  // bf16's largest
+  const bool finite = fabsf(v) < INFINITY;
+  const __nv_bfloat16 x = __float2bfloat16_rn(finite ? fminf(fmaxf(v, -most), most) : v);
+  v = finite ? v - __bfloat162float(x) : 0.0f;
+  return x;
+}
+
 // Which adapter (n_adapters = none) and which rows tile `t` has; 0 rows when there is no such tile.
 template <int TM, int T = kT>
 __device__ int find_tile(const Args& a, int t, int32_t* rows_out, int32_t* cnt, int& key) {

@@ -358,8 +358,9 @@ __global__ void __launch_bounds__(kNT, 2) lora_tc_kernel(const Args a) {
       v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
       v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
     }
+    const bool in = i % pieces8 * 8 < a.rank;  // past the adapter's ranks 0 x inf would be NaN
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= scale;
+    for (int e = 0; e < 8; ++e) v[e] = in ? v[e] * scale : 0.0f;
   };
   auto put_h = [&](int i, float (&v)[8]) {
     const int row = i / pieces8, c = i % pieces8 * 8;
@@ -367,10 +368,8 @@ __global__ void __launch_bounds__(kNT, 2) lora_tc_kernel(const Args a) {
       uint32_t w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const __nv_bfloat16 x = __float2bfloat16_rn(v[2 * e]), y = __float2bfloat16_rn(v[2 * e + 1]);
+        const __nv_bfloat16 x = take_part(v[2 * e]), y = take_part(v[2 * e + 1]);
         w[e] = (uint32_t)__bfloat16_as_ushort(x) | ((uint32_t)__bfloat16_as_ushort(y) << 16);
-        v[2 * e] -= __bfloat162float(x);
-        v[2 * e + 1] -= __bfloat162float(y);
       }
       unsigned char* at = smem + l.h + (part * l.atoms + c / 64) * kXBytes + row * 128 +
                           (((c % 64 / 8) ^ (row & 7)) << 4);

@@ -1,0 +1,68 @@
+"""tfd_lora where a low-rank sum is infinite or out of bf16's range, in the form for few rows and in the
+one for prompts (more than 256 rows, 16-byte aligned), at ranks that fill a tile and that do not."""
+import numpy as np
+import pytest
+import torch
+
+from helpers import need_gpu, np32
+from oracle.lora import lora as oracle_lora
+from speculative_decoding_draft_row_gb300 import tfd
+
+pytestmark = pytest.mark.gpu
+
+RANKS = [8, 16, 24, 40, 64, 72, 128]
+
+
+def positive(R, k, n, rank, seed):
+    """Positive activations and adapters, so that an infinite activation makes every low-rank sum +inf;
+    the outputs of odd number have negative rows of B."""
+    g = torch.Generator().manual_seed(seed)
+    x = (0.5 + torch.rand((R, k), generator=g)).bfloat16().cuda()
+    a = ((0.5 + torch.rand((1, rank, k), generator=g)) / k).bfloat16().cuda()
+    b = (0.5 + torch.rand((1, n, rank), generator=g)).bfloat16()
+    b[:, 1::2] *= -1
+    return x, a, b.cuda(), torch.zeros(R, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("rank", RANKS)
+@pytest.mark.parametrize("R", [3, 40, 300])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_an_infinite_activation_gives_the_formulas_infinities(R, rank, dtype):
+    need_gpu()
+    k, n = 264, 136
+    x, a, b, ids = positive(R, k, n, rank, 7)
+    base = torch.ones((R, n), dtype=dtype, device="cuda")
+    ref = tfd.tfd_lora(x, a, b, ids, base=base)
+    x2 = x.clone()
+    x2[1, 5], x2[2, k - 1] = float("inf"), -float("inf")
+    y = tfd.tfd_lora(x2, a, b, ids, base=base)
+    torch.cuda.synchronize()
+    ex, _, _ = oracle_lora(np32(x2), np32(a), np32(b), ids.cpu().numpy(), np32(base))
+    assert np.isinf(ex[1:3]).all()
+    assert np.array_equal(np32(y)[1:3], ex[1:3].astype(np.float32))
+    rest = [r for r in range(R) if r not in (1, 2)]
+    assert torch.equal(y[rest], ref[rest]) and torch.isfinite(y[rest]).all()
+
+
+@pytest.mark.parametrize("rank", RANKS)
+@pytest.mark.parametrize("R", [3, 300])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_low_rank_sum_beyond_bf16s_range(R, rank, dtype):
+    """h = 2^127 (1.9921875 + 0.0078) is finite in fp32 and rounds to infinity in bf16; B brings it back.
+    h and its products are exact; the fp32 sum of a row adds 3 rank rounded products of one sign: at
+    most 3 rank 2^-24 relative, h's two parts 2^-16 where y is bf16, then y's own rounding."""
+    need_gpu()
+    k, n = 64, 72
+    x = torch.zeros((R, k), dtype=torch.bfloat16, device="cuda")
+    x[:, 0], x[:, 1] = 2.0 ** 127 * 1.9921875, 2.0 ** 120 * 0.99609375
+    a = torch.zeros((1, rank, k), dtype=torch.bfloat16, device="cuda")
+    a[:, :, :2] = 1
+    b = torch.full((1, n, rank), 2.0 ** -120, dtype=torch.bfloat16, device="cuda")
+    ids = torch.zeros(R, dtype=torch.int32, device="cuda")
+    mode = tfd.OUT_F32 if dtype == torch.float32 else tfd.OUT_BF16
+    y = tfd.tfd_lora(x, a, b, ids, out_mode=mode)
+    torch.cuda.synchronize()
+    want = rank * (2.0 ** 7 * 1.9921875 + 0.99609375)
+    rel = 3 * rank * 2.0 ** -24 + (0 if dtype == torch.float32 else 2.0 ** -16 + 2.0 ** -8)
+    got = np32(y).astype(np.float64)
+    assert (np.abs(got - want) <= rel * want).all(), (got.min(), got.max(), want)
