@@ -101,6 +101,7 @@ __device__ __forceinline__ uint2 ldg_stream8(const void* p, uint64_t pol) {
 // A build with -DTFD_TEST_STALL_EXCHANGE=1 has the second block of every two-block cluster split
 // drop its partial sums instead of sending them, so the leader's bounded waits run out and report
 // TFD_ERR_TIMEOUT in the device status (tests of the failure path); the default build sends them.
+// The adapters' tensor-memory form then does not announce that its first products are complete.
 #ifndef TFD_TEST_STALL_EXCHANGE
 #define TFD_TEST_STALL_EXCHANGE 0
 #endif

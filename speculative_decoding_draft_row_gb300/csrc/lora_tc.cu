@@ -208,9 +208,10 @@ __global__ void __launch_bounds__(kNT, 2) lora_tc_kernel(const Args a) {
   auto empty = [&](int s) { return bars + 8u * s; };              // stage s has been read
   const uint32_t shrunk = bars + 8u * kStages;                    // D1 is complete
   auto done = [&](int b) { return bars + 8u * (kStages + 1 + b); };  // D2 buffer b is complete
+  const uint32_t drained = bars + 8u * (kStages + 3);  // every product is, after a wait ran out
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + l.bars + 64);
   if (tid == 0) {
-    for (int s = 0; s < kStages + 3; ++s) bar_init(bars + 8u * s);
+    for (int s = 0; s < kStages + 4; ++s) bar_init(bars + 8u * s);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) {
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(kNT, 2) lora_tc_kernel(const Args a) {
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_slot;
-  bool ok = true;
+  bool ok = true;  // none of this thread's waits has run out; thread 0 issues products only so long
 
   // ---- shrink -----------------------------------------------------------------------------------
   const int kblocks = (a.k + kKB - 1) / kKB;
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(kNT, 2) lora_tc_kernel(const Args a) {
     copy_wait<kStages - 2>();
     fence_async();
     __syncthreads();
-    if (tid == 0) {
+    if (tid == 0 && ok) {
       fence_after();
       const uint32_t st = s_ring + (uint32_t)(i % kStages) * l.stage;
       const uint64_t da = sdesc(st), db = sdesc(st + kXBytes);
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kNT, 2) lora_tc_kernel(const Args a) {
     load_stage(i + kStages - 1);
   }
   if (nk > 0) {
-    if (tid == 0) mma_commit(shrunk);
+    if (tid == 0 && !TFD_TEST_STALL_EXCHANGE) mma_commit(shrunk);
     if (ok) ok = bar_wait(shrunk, 0);
   }
   copy_wait<0>();
@@ -417,13 +418,13 @@ __global__ void __launch_bounds__(kNT, 2) lora_tc_kernel(const Args a) {
   copy_wait<kBufs - 2>();
   fence_async();
   __syncthreads();
-  if (tid == 0 && j0 < j1) multiply(0);
+  if (tid == 0 && ok && j0 < j1) multiply(0);
   for (int j = j0; j < j1; ++j) {
     const int i = j - j0, buf = i % kBufs, d = i & 1;
     copy_wait<kBufs - 3>();
     fence_async();
     __syncthreads();  // the next chunk is here; the last one's rows have been written from its buffer
-    if (tid == 0 && j + 1 < j1) multiply(i + 1);
+    if (tid == 0 && ok && j + 1 < j1) multiply(i + 1);
     load_chunk(j + kBufs - 1);  // into the buffer of the chunk before this one
     if (ok) ok = bar_wait(done(d), (uint32_t)(i >> 1) & 1u);
     fence_after();
@@ -486,8 +487,16 @@ __global__ void __launch_bounds__(kNT, 2) lora_tc_kernel(const Args a) {
     }
   }
   copy_wait<0>();
+  if (!ok) {
+    set_dev_status(a.dev_status, TFD_ERR_TIMEOUT);
+    // no product may still read or write when this block's memory is given back (where no wait of
+    // thread 0 ran out, it has waited for the last of them)
+    if (tid == 0) {
+      mma_commit(drained);
+      bar_wait(drained, 0);
+    }
+  }
   __syncthreads();
-  if (!ok) set_dev_status(a.dev_status, TFD_ERR_TIMEOUT);
   if (warp == 0) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols)
                  : "memory");
