@@ -49,7 +49,7 @@ constexpr int kOffX = 0;
 constexpr int kOffStage = kOffX + kXBytes;
 constexpr int kOffInbox = kOffStage + kStages * kStageBytes;
 constexpr int kOffBar = kOffInbox + kInboxBytes;  // mbarriers (8 bytes each)
-constexpr int kNumBars = 2 * kStages + 1 + 2 + 2 + 2;
+constexpr int kNumBars = 2 * kStages + 1 + 2 + 2 + 2 + 1;
 constexpr int kOffBest = kOffBar + kNumBars * 8 + 8;  // (+ the tensor-memory address)
 constexpr int kOffJoin = kOffBest + 4 * kN * 8;
 constexpr int kOffPmax = kOffJoin + kN * 8;
@@ -213,6 +213,7 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
   auto tempty = [&](int b) { return b0 + 8u * (2 * kStages + 3 + b); };
   const uint32_t ifull = b0 + 8u * (2 * kStages + 5);   // leader: the second block's partials
   const uint32_t iempty = b0 + 8u * (2 * kStages + 6);  // second block: the leader has read them
+  const uint32_t drained = b0 + 8u * (2 * kStages + 7);  // every MMA is complete, after a timeout
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffBar + kNumBars * 8);
   uint64_t* sbest = reinterpret_cast<uint64_t*>(smem + kOffBest);
   uint64_t* sjoin = reinterpret_cast<uint64_t*>(smem + kOffJoin);
@@ -231,6 +232,7 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
     }
     bar_init(ifull, 1);
     bar_init(iempty, 4);
+    bar_init(drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -248,6 +250,7 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
   fence_after();
   const uint32_t tmem = *tmem_slot;
   bool timed_out = false;
+  int loads = 0;  // weight boxes that this thread has issued
 
   if (warp == 0) {
     if (lane == 0 && ng > 0) {
@@ -255,12 +258,14 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
       bar_expect_tx(xfull, (uint32_t)(nkb * kXBlockBytes));
       for (int kb = 0; kb < nkb; ++kb)
         tma_2d(s_x + (uint32_t)(kb * kXBlockBytes), &tx, (kb0 + kb) * kKB, 0, xfull);
-      int it = 0;
-      for (int64_t g = g_begin; g < g_end; ++g)
+      int& it = loads;
+      for (int64_t g = g_begin; g < g_end && !timed_out; ++g)
         for (int kb = 0; kb < nkb; ++kb, ++it) {
           const int s = it % kStages;
-          if (it >= kStages && !timed_out && !bar_wait(empty(s), (uint32_t)((it / kStages) - 1) & 1u))
-            timed_out = true;
+          if (it >= kStages && !bar_wait(empty(s), (uint32_t)((it / kStages) - 1) & 1u)) {
+            timed_out = true;  // nothing is issued after a wait that ran out
+            break;
+          }
           bar_expect_tx(full(s), kStageBytes);
           tma_2d(s_stage + (uint32_t)(s * kStageBytes), &tw, (kb0 + kb) * kKB, (int)(g * kM), full(s));
         }
@@ -270,14 +275,17 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
       if (!bar_wait(xfull, 0)) timed_out = true;  // (the first wait of this thread)
       fence_after();
       int it = 0;
-      for (int j = 0; j < ng; ++j) {
+      for (int j = 0; j < ng && !timed_out; ++j) {
         const int buf = j & 1;
-        if (j >= 2 && !timed_out && !bar_wait(tempty(buf), (uint32_t)((j >> 1) - 1) & 1u)) timed_out = true;
+        if (j >= 2 && !bar_wait(tempty(buf), (uint32_t)((j >> 1) - 1) & 1u)) timed_out = true;
         fence_after();
         const uint32_t d = tmem + (uint32_t)(buf * kN);
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
+        for (int kb = 0; kb < nkb && !timed_out; ++kb, ++it) {
           const int s = it % kStages;
-          if (!timed_out && !bar_wait(full(s), (uint32_t)(it / kStages) & 1u)) timed_out = true;
+          if (!bar_wait(full(s), (uint32_t)(it / kStages) & 1u)) {
+            timed_out = true;
+            break;
+          }
           fence_after();
           const uint64_t da = sdesc(s_stage + (uint32_t)(s * kStageBytes));
           const uint64_t db = sdesc(s_x + (uint32_t)(kb * kXBlockBytes));
@@ -286,7 +294,7 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
             mma(d, da + 2u * kk, db + 2u * kk, (kb | kk) != 0);
           mma_commit(empty(s));  // the stage is free once these MMAs have read it
         }
-        mma_commit(tfull(buf));  // the group's accumulator is complete
+        if (!timed_out) mma_commit(tfull(buf));  // the group's accumulator is complete
       }
     }
   } else {
@@ -322,7 +330,7 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
           if (!TFD_TEST_STALL_EXCHANGE) st_async4(dst + 4u * c, v[c], v[c + 1], v[c + 2], v[c + 3], rb);
         continue;
       }
-      if (warp == 2 && lane == 0) bar_expect_tx(ifull, kInboxBytes);
+      if (warp == 2 && lane == 0 && !timed_out) bar_expect_tx(ifull, kInboxBytes);
       if (!timed_out && !bar_wait(ifull, (uint32_t)j & 1u)) timed_out = true;
       float u[kN];
 #pragma unroll
@@ -388,6 +396,18 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
     }
   }
   if (timed_out) set_dev_status(a.status, TFD_ERR_TIMEOUT);
+  if (__syncthreads_or(timed_out) && lane == 0 && ng > 0) {
+    // a thread that timed out waited for nothing more: the loads and MMAs in flight end (bounded)
+    // before the block gives its memory back
+    if (warp == 0) {
+      bool landed = bar_wait(xfull, 0);
+      for (int it = max(loads - kStages, 0); it < loads && landed; ++it)
+        landed = bar_wait(full(it % kStages), (uint32_t)(it / kStages) & 1u);
+    } else if (warp == 1) {
+      mma_commit(drained);
+      bar_wait(drained, 0);
+    }
+  }
   __syncthreads();
   // the pair's last remote operations are done before either block leaves
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
