@@ -412,6 +412,8 @@ def tfd_accept_sampled(p, q, drafts, n_asked, u, u_next, q_map=None, n_kept=None
     qs, qw, nq = q.shape
     p0, ldp, p2 = p.stride()
     q0, ldq, q2 = q.stride()
+    if win == 1 and streams > 1:                         # one row a stream: theirs is the row stride
+        ldq = q0
     if p.dtype is not f32 or p.get_device() != dev or ps != streams or pw != win + 1 or \
             (p2 != 1 and n > 1) or (p0 != pw * ldp and streams > 1):
         raise ValueError(f"p: float32 [{streams}][{win + 1}][columns] with evenly spaced rows on the "
