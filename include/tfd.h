@@ -344,11 +344,13 @@ tfd_status tfd_absorb(const void* k_rows, const void* v_rows, const void* k_gamm
  *   logits   device bf16 or float (lfmt TFD_X_BF16, TFD_X_F32) [rows][ld], ld >= n; any
  *            element-aligned base and stride; rows >= 1, 1 <= n <= TFD_MAX_DRAW_COLS.
  *   temperature, top_p, min_p device float [rows], top_k device int32 [rows]; each may be NULL
- *            (1, 1, 0 and 0). u device float [rows].
- *   id_map   device int32 [n] or NULL: the id reported (and compared on ties) for column i.
+ *            (1, 1, 0 and 0). u device float [rows]; mind that a double from 1 - 2^-25 on is 1 as a
+ *            float.
+ *   id_map   device int32 [n] or NULL: the id reported (and compared on ties) for column i. Ids
+ *            differ: of columns with the same logit and the same id, top_k and top_p keep all or none.
  *   ids      device int32, row r at ids[r * ldt] (ldt 0 = 1), so that the tokens of one step can
  *            land in a column of a [streams][steps] array; prob device float or NULL, the same
- *            stride: the token's probability in the filtered distribution.
+ *            stride: the token's probability in the filtered distribution, to 2^-20 relative.
  *   probs    device float [rows][ldp] or NULL, ldp >= n: the filtered, normalised distribution by
  *            column (written in full, zeros where nothing is kept).
  *   The outputs' ranges (strides included) overlap no input: TFD_ERR_INVALID.
@@ -399,8 +401,11 @@ tfd_status tfd_accept_sampled(const float* p, int64_t ldp, const float* q, int64
 /*
  * tfd_lora - low-rank adapters of many requests at once, beside a projection they share.
  *   y[r] = base[r] + scales[a] * B[a] (A[a] x[r]) with a = adapter_ids[r]: the base is the shared
- *   projection's result (tfd_head_gemv's y), in place or not. Sums in fp32, A[a] x[r] kept in fp32,
- *   y rounded once. Rows may name adapters in any order and share them; -1 is no adapter
+ *   projection's result (tfd_head_gemv's y), in place or not. Sums in fp32; h = scales[a] * A[a] x[r]
+ *   in fp32 enters its product with B[a] with all its 24 bits where y is float, and to within 2^-17
+ *   of its value where y is bf16 (that shows only where base nearly cancels the adapter's term);
+ *   y is rounded once. An infinite activation or h gives what the formula gives; the adapters
+ *   themselves are finite (else y is infinite or NaN in the outputs they reach). Rows may name adapters in any order and share them; -1 is no adapter
  *   (y[r] = base[r]). One row up to whole prompts. The pages run one set of weights for all
  *   streams; this call has no counterpart there.
  * Args:

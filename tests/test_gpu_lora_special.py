@@ -1,5 +1,6 @@
-"""tfd_lora where a low-rank sum is infinite or out of bf16's range, in the form for few rows and in the
-one for prompts (more than 256 rows, 16-byte aligned), at ranks that fill a tile and that do not."""
+"""tfd_lora where a low-rank sum is infinite or out of bf16's range, or the base cancels it: in the form
+for few rows and in the one for prompts (more than 256 rows, 16-byte aligned), at ranks that fill a
+tile and that do not."""
 import numpy as np
 import pytest
 import torch
@@ -66,3 +67,34 @@ def test_a_low_rank_sum_beyond_bf16s_range(R, rank, dtype):
     rel = 3 * rank * 2.0 ** -24 + (0 if dtype == torch.float32 else 2.0 ** -16 + 2.0 ** -8)
     got = np32(y).astype(np.float64)
     assert (np.abs(got - want) <= rel * want).all(), (got.min(), got.max(), want)
+
+
+@pytest.mark.parametrize("rank", RANKS)
+@pytest.mark.parametrize("R", [3, 40, 300])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_base_that_cancels_the_adapters_term(R, rank, dtype):
+    """What is left shows how exactly h enters its product. One activation a rank, so h = s (a x) has
+    two roundings at most and only the scale's counts (a x is exact in fp32): 2^-24 relative. The
+    products with B add 3 rank + 1 fp32 sums of |B||h| at most, 2^-24 each; h's parts 2^-17 where y is
+    bf16; then y's own rounding."""
+    need_gpu()
+    k, n = 256, 72
+    g = torch.Generator().manual_seed(rank + R)
+    x = (1 + torch.rand((R, k), generator=g)).bfloat16().cuda()
+    a = torch.zeros((1, rank, k))
+    a[0, torch.arange(rank), torch.arange(rank)] = 1 + torch.rand(rank, generator=g)
+    a = a.bfloat16().cuda()
+    b = torch.randn((1, n, rank), generator=g).bfloat16().cuda()
+    s = torch.tensor([1.2345678], device="cuda")
+    ids = torch.zeros(R, dtype=torch.int32, device="cuda")
+    h = np32(s).astype(np.float64) * (np32(x).astype(np.float64) @ np32(a)[0].T.astype(np.float64))
+    b64 = np32(b)[0].astype(np.float64)
+    term, mag = h @ b64.T, np.abs(h) @ np.abs(b64).T
+    base = torch.from_numpy(-term).to(dtype).cuda()
+    y = tfd.tfd_lora(x, a, b, ids, base=base, scales=s)
+    torch.cuda.synchronize()
+    left = term + base.double().cpu().numpy()
+    tol = mag * ((3 * rank + 3) * 2.0 ** -24 + (2.0 ** -17 if dtype == torch.bfloat16 else 0))
+    half = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -24
+    err = np.abs(np32(y).astype(np.float64) - left)
+    assert (err <= tol + half * (np.abs(left) + tol)).all(), (err / mag).max()
