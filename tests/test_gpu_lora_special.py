@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from helpers import need_gpu, np32
+from helpers import assert_fp32_close, need_gpu, np32
 from oracle.lora import lora as oracle_lora
 from speculative_decoding_draft_row_gb300 import tfd
 
@@ -98,3 +98,26 @@ def test_a_base_that_cancels_the_adapters_term(R, rank, dtype):
     half = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -24
     err = np.abs(np32(y).astype(np.float64) - left)
     assert (err <= tol + half * (np.abs(left) + tol)).all(), (err / mag).max()
+
+
+@pytest.mark.parametrize("na,named", [(64, 1), (300, 6), (4096, 3)])
+@pytest.mark.parametrize("R", [40, 1100])
+def test_a_large_table_of_which_few_are_named(na, named, R):
+    need_gpu()
+    k, n, rank = 72, 136, 16
+    g = torch.Generator().manual_seed(na + R)
+    x = torch.randn((R, k), generator=g).bfloat16().cuda()
+    a = (torch.randn((na, rank, k), generator=g) / k ** 0.5).bfloat16().cuda()
+    b = (0.3 * torch.randn((na, n, rank), generator=g)).bfloat16().cuda()
+    s = (0.5 + torch.rand(na, generator=g)).cuda()
+    base = torch.randn((R, n), generator=g).cuda()
+    which = torch.randperm(na, generator=g)[:named]
+    which[0] = na - 1
+    ids = which[torch.randint(0, named, (R,), generator=g)].int()
+    ids[::7] = -1
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = tfd.tfd_lora(x, a, b, ids.cuda(), base=base, scales=s, dev_status=st)
+    torch.cuda.synchronize()
+    ex, mag, _ = oracle_lora(np32(x), np32(a), np32(b), ids.numpy(), np32(base), np32(s))
+    assert_fp32_close(np32(y), ex, mag)
+    assert st.item() == 0 and torch.equal(y[::7], base[::7])
