@@ -476,8 +476,8 @@ struct Sampler {
   }
   // Counts a column of the list in its bin. Equal logits share a bin, and adds to one address go one
   // by one: where the warp has a single bin, one lane adds the sums.
-  __device__ __forceinline__ void list_count(int b, uint64_t w) {
-    const unsigned on = __activemask();
+  // `on`: the warp's lanes that have one.
+  __device__ __forceinline__ void list_count(unsigned on, int b, uint64_t w) {
     int same;
     __match_all_sync(on, b, &same);
     if (!same) {
@@ -527,6 +527,7 @@ struct Sampler {
       for (int q = 0; q < kList / kT; ++q) {
         const int j = tid + q * kT;
         entry[q] = bin[q] = -1;
+        const unsigned on = __ballot_sync(0xffffffffu, j < mem);
         if (j < mem) {
           const int i = split ? sh.lmem[j] : j;
           entry[q] = i;
@@ -536,7 +537,7 @@ struct Sampler {
             const float l = __uint_as_float((uint32_t)(sh.lent[i] >> 32));
             bin[q] = max(0, min(kBins - 1, (int)((place(lead(l)) - t0) * mul)));
           }
-          list_count(bin[q], sh.lw[i]);
+          list_count(on, bin[q], sh.lw[i]);
         }
       }
       __syncthreads();
