@@ -22,9 +22,9 @@
 // itself; the lists and, behind way C, the shares of that block's masses cost a barrier more each.
 //
 // Bound by the barriers and the block's work between them where rows are few (1 x 4096 with all
-// filters 10.9 us, 4 x 163840 with top-p and distributions 30.0, 16 x 163840 bf16 with mixed filters
-// 37.1), by the weights' instructions where they are many (33 x 50021 without filters 14.3 us, 96 x
-// 163840 with mixed filters and distributions 132, of 19 for the bytes).
+// filters 10.9 us, 4 x 163840 with top-p and distributions 30.2, 16 x 163840 bf16 with mixed filters
+// 37.4), by the weights' instructions where they are many (33 x 50021 without filters 14.3 us, 96 x
+// 163840 with mixed filters and distributions 133, of 19 for the bytes).
 #include <cooperative_groups.h>
 
 #include "launch.cuh"
