@@ -13,9 +13,7 @@
 // x 256 B each, and the partial softmax states are combined in distributed shared memory.
 #include <cooperative_groups.h>
 
-#include <cmath>
-
-#include "common.cuh"
+#include "rope.cuh"
 
 namespace {
 
@@ -40,61 +38,6 @@ __device__ __forceinline__ float block_reduce(float v, float* sred, bool is_max)
   return r;
 }
 
-// Each pair's frequency base^(-2i/dim) in turns (1 turn = 2 pi), as a 64-bit binary fraction:
-// t_i = frac(base^(-2i/dim) / (2 pi)) * 2^64. For an integer position p, p * t_i mod 2^64 is the
-// angle p * base^(-2i/dim) reduced to one turn, exact up to the rounding of t_i (2^-53 relative),
-// so the reduction needs no floating-point arithmetic on the device.
-struct RopeTurns {
-  uint64_t t[kDim / 2];
-};
-
-// Lane l of a warp holds elements 4l..4l+3 of a 128-vector: RMSNorm with gamma, then RoPE with
-// the angle reduced to [-pi, pi) before the fp32 sine and cosine.
-// The sines and cosines of this lane's four pairs at position p (lane l holds pairs
-// 4 (l mod 16) .. + 3), shared by every head at that position.
-__device__ __forceinline__ void rope_sincos(int p, const RopeTurns& turns, float (&sn)[4],
-                                            float (&cs)[4]) {
-  const int lane = threadIdx.x & 31;
-  const float turn_unit = 1.4629180792671596e-9f;  // 2 pi / 2^32
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int i = 4 * (lane & 15) + j;  // pair index 0..63
-    const uint64_t ph = (uint64_t)(uint32_t)p * turns.t[i];  // mod 2^64: the reduced angle
-    const float red = (float)(int32_t)(ph >> 32) * turn_unit;
-    sincosf(red, &sn[j], &cs[j]);
-  }
-}
-
-// RMSNorm with gamma, then the rotation by the given sines and cosines.
-__device__ __forceinline__ void norm_rope_sc(float (&x)[4], const uint16_t* gamma, float eps,
-                                             const float (&sn)[4], const float (&cs)[4]) {
-  const int lane = threadIdx.x & 31;
-  float ss = x[0] * x[0] + x[1] * x[1] + x[2] * x[2] + x[3] * x[3];
-  ss = warp_sum(ss);
-  const float inv = 1.0f / sqrtf(ss / (float)kDim + eps);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float gm = gamma ? bf16_bits_to_f32(gamma[4 * lane + j]) : 1.0f;
-    x[j] = x[j] * inv * gm;
-  }
-  float other[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) other[j] = __shfl_xor_sync(0xffffffffu, x[j], 16);
-  const bool first_half = lane < 16;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    // first half holds a = x[i] (partner b = x[i+64]); second half holds b (partner a).
-    x[j] = first_half ? (x[j] * cs[j] - other[j] * sn[j]) : (other[j] * sn[j] + x[j] * cs[j]);
-  }
-}
-
-__device__ __forceinline__ void norm_rope(float (&x)[4], const uint16_t* gamma, float eps, int p,
-                                          const RopeTurns& turns) {
-  float sn[4], cs[4];
-  rope_sincos(p, turns, sn, cs);
-  norm_rope_sc(x, gamma, eps, sn, cs);
-}
-
 struct AttnPartial {
   float m, l;          // block max score and sum of exp(score - m)
   float acc[kDim];     // sum of exp(score - m) * v
@@ -108,7 +51,7 @@ struct AttnPartial {
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
 window_attn_kernel(const uint16_t* __restrict__ q, const uint16_t* __restrict__ k_new,
                    const uint16_t* __restrict__ v_new, const uint16_t* __restrict__ q_gamma,
-                   const uint16_t* __restrict__ k_gamma, float eps, const RopeTurns turns,
+                   const uint16_t* __restrict__ k_gamma, float eps, const RopeTurns<kDim> turns,
                    const int32_t* __restrict__ pos, uint16_t* k_ring, uint16_t* v_ring, int ring,
                    int window, int heads, uint16_t* __restrict__ out, int32_t* dev_status) {
   __shared__ float qn[kDim];
@@ -157,7 +100,7 @@ window_attn_kernel(const uint16_t* __restrict__ q, const uint16_t* __restrict__ 
     const uint16_t* src = (warp == 0 ? q : k_new) + head_off + 4 * lane;
     uint2 raw = *reinterpret_cast<const uint2*>(src);
     float x[4] = {bf16_lo(raw.x), bf16_hi(raw.x), bf16_lo(raw.y), bf16_hi(raw.y)};
-    norm_rope(x, warp == 0 ? q_gamma : k_gamma, eps, pp, turns);
+    norm_rope<kDim>(x, warp == 0 ? q_gamma : k_gamma, eps, pp, turns);
     if (warp == 0) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) qn[4 * lane + j] = x[j];
@@ -274,7 +217,7 @@ constexpr int kAbsorbHeads = 4;
 
 __global__ void __launch_bounds__(256)
 absorb_kernel(const uint16_t* __restrict__ k_rows, const uint16_t* __restrict__ v_rows,
-              const uint16_t* __restrict__ k_gamma, float eps, const RopeTurns turns,
+              const uint16_t* __restrict__ k_gamma, float eps, const RopeTurns<kDim> turns,
               const int32_t* __restrict__ p0, int n, uint16_t* k_ring, uint16_t* v_ring, int ring,
               int streams, int heads, int32_t* dev_status) {
   const int lane = threadIdx.x & 31;
@@ -302,36 +245,18 @@ absorb_kernel(const uint16_t* __restrict__ k_rows, const uint16_t* __restrict__ 
     }
   }
   float sn[4], cs[4];
-  rope_sincos(p, turns, sn, cs);  // one position: the same rotation for every head
+  rope_sincos<kDim>(p, turns, sn, cs);  // one position: the same rotation for every head
 #pragma unroll
   for (int j = 0; j < kAbsorbHeads; ++j) {
     if (h0 + j >= heads) break;  // warp-uniform
     float x[4] = {bf16_lo(kraw[j].x), bf16_hi(kraw[j].x), bf16_lo(kraw[j].y), bf16_hi(kraw[j].y)};
-    norm_rope_sc(x, k_gamma, eps, sn, cs);
+    norm_rope_sc<kDim>(x, k_gamma, eps, sn, cs);
     uint2 o;
     o.x = (uint32_t)f32_to_bf16_bits(x[0]) | ((uint32_t)f32_to_bf16_bits(x[1]) << 16);
     o.y = (uint32_t)f32_to_bf16_bits(x[2]) | ((uint32_t)f32_to_bf16_bits(x[3]) << 16);
     *reinterpret_cast<uint2*>(k_ring + dst + j * kDim) = o;
     *reinterpret_cast<uint2*>(v_ring + dst + j * kDim) = vraw[j];
   }
-}
-
-// The turn table of a RoPE base, computed in double on the host (kept for the last base used by
-// this thread).
-const RopeTurns& rope_turns(float base) {
-  thread_local float cached_base = -1.0f;
-  thread_local RopeTurns cached;
-  if (cached_base != base) {
-    const double two_pi = 6.283185307179586476925286766559;
-    for (int i = 0; i < kDim / 2; ++i) {
-      const double f = std::pow((double)base, -2.0 * i / kDim);
-      double turns = f / two_pi;
-      turns -= std::floor(turns);
-      cached.t[i] = (uint64_t)std::ldexp(turns, 64);
-    }
-    cached_base = base;
-  }
-  return cached;
 }
 
 }  // namespace
@@ -356,7 +281,7 @@ extern "C" tfd_status tfd_window_attn(const void* q, const void* k_new, const vo
   window_attn_kernel<<<grid, kThreads, 0, tfd_host::as_stream(stream)>>>(
       reinterpret_cast<const uint16_t*>(q), reinterpret_cast<const uint16_t*>(k_new),
       reinterpret_cast<const uint16_t*>(v_new), reinterpret_cast<const uint16_t*>(q_gamma),
-      reinterpret_cast<const uint16_t*>(k_gamma), eps, rope_turns(rope_base), pos,
+      reinterpret_cast<const uint16_t*>(k_gamma), eps, tfd_host::rope_turns<kDim>(rope_base), pos,
       reinterpret_cast<uint16_t*>(k_ring), reinterpret_cast<uint16_t*>(v_ring), ring, window,
       heads, reinterpret_cast<uint16_t*>(out), dev_status);
   return tfd_host::launch_status();
@@ -379,7 +304,7 @@ extern "C" tfd_status tfd_absorb(const void* k_rows, const void* v_rows, const v
   if ((warps + 7) / 8 > 2147483647) return TFD_ERR_INVALID;
   absorb_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, tfd_host::as_stream(stream)>>>(
       reinterpret_cast<const uint16_t*>(k_rows), reinterpret_cast<const uint16_t*>(v_rows),
-      reinterpret_cast<const uint16_t*>(k_gamma), eps, rope_turns(rope_base), p0, n,
+      reinterpret_cast<const uint16_t*>(k_gamma), eps, tfd_host::rope_turns<kDim>(rope_base), p0, n,
       reinterpret_cast<uint16_t*>(k_ring), reinterpret_cast<uint16_t*>(v_ring), ring, streams,
       heads, dev_status);
   return tfd_host::launch_status();
