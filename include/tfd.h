@@ -5,8 +5,9 @@
  * server: a few-row (1..16 token rows) vocabulary-head GEMV in bf16 or FP8 fused with a
  * split-vocabulary top-1 / top-k, the two-stage head (low-rank top-cand_k then exact rescore), the
  * qk_norm + RoPE ring-window attention, the accept-prefix count, and the FP8 quantisation of the
- * weights these calls read; and, for requests that sample, drawing tokens from logits and the
- * rejection accept of such drafts.
+ * weights these calls read; for requests that sample, drawing tokens from logits and the
+ * rejection accept of such drafts; and, for contexts longer than a ring, a paged key-value cache: its
+ * page tables, the append of new rows, and the attention of one or a few rows a request over it.
  *
  * Conventions shared by every call:
  *  - Pointers named as device buffers are caller-owned device memory on the current CUDA device.
@@ -88,6 +89,8 @@ typedef enum { TFD_OUT_NONE = 0, TFD_OUT_F32 = 1, TFD_OUT_BF16 = 2, TFD_OUT_ADD_
 #define TFD_MAX_RANK 128     /* rank of a low-rank adapter */
 #define TFD_MAX_LORA_ROWS 262144  /* rows of one tfd_lora call (every tile's search reads all ids) */
 #define TFD_MAX_DRAW_COLS 1048576 /* columns of a row that a token is drawn from (exact sums) */
+#define TFD_MAX_REQUESTS 8192     /* requests of one paged call */
+#define TFD_MAX_PAGE 1024         /* tokens of a page */
 
 /* A static string naming a status. Never NULL. */
 const char* tfd_status_string(int status);
@@ -427,6 +430,127 @@ tfd_status tfd_lora(const void* x, int rows, int64_t k, int64_t ldx, const void*
                     const int32_t* adapter_ids, const float* scales, int out_mode,
                     const void* base, int64_t ldb, void* y, int64_t ldy, int32_t* dev_status,
                     void* stream);
+
+/*
+ * A paged key-value cache: tokens stand in pages of page_size, and a request's tokens 0, 1, 2, ... in
+ * the pages that its row of a page table names, in order. The pages' rings have one run of slots a
+ * stream (tfd_window_attn, tfd_absorb); a paged cache has no counterpart there.
+ *   k, v      device [pages][page_size][heads][dim], the same strides (in elements) for both; bf16, or
+ *             E4M3 codes. Elements of a vector adjoin; the strides are multiples of 16 bytes, in any
+ *             order ([page][head][token] as well), k and v 16-byte aligned.
+ *   k_scales, v_scales device float [pages][heads][page_size] (E4M3 only, else NULL): a vector is its
+ *             codes times its scale. No row sees a NaN code (0x7F, 0xFF).
+ * A slot is page * page_size + the token's place in the page; pages * page_size < 2^31. page_size
+ * 1..TFD_MAX_PAGE; heads 1..1024; dim 64 or 128 (others: TFD_ERR_UNSUPPORTED).
+ */
+typedef enum { TFD_KV_BF16 = 0, TFD_KV_E4M3 = 1 } tfd_kvfmt;
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scales;
+  float* v_scales;
+  int64_t page_stride, token_stride, head_stride;
+  int32_t pages, page_size, heads, dim, fmt;
+} tfd_kv_pages;
+
+/* What a call does to query and key vectors: RMSNorm of each head, then RoPE (see tfd_window_attn). */
+#define TFD_QK_NORM 1
+#define TFD_QK_ROPE 2
+
+/*
+ * tfd_page_plan - page tables and slot maps of a round, from the requests' lengths.
+ *   Request r has lens[r] tokens cached and gets n_new[r] rows this round: it is given pages, or gives
+ *   pages back, so that it holds ceil((lens[r] + n_new[r]) / page_size) of them. So the call that
+ *   plans a round also returns what the last round's turned-down drafts took, and lens = n_new = 0
+ *   returns all of a request. The free pages are a stack free_ids[0 .. *n_free): pages given back go
+ *   on it, then missing ones come from its top, both in the order of requests and of their pages; of
+ *   the pages given back the first ends on top, so that pages taken by one call and given back by the next
+ *   leave the stack as it was. Lengths can stay on the GPU from round to round.
+ *   row_start[r] = n_new[0] + .. + n_new[r - 1] (requests + 1 values); for row i = row_start[r] + j:
+ *   pos[i] = lens[r] + j, slots[i] = the slot of that token. Rows from row_start[requests] to
+ *   `rows` get slot and position -1.
+ * Args:
+ *   lens, n_new device int32 [requests]; requests 1..TFD_MAX_REQUESTS; page_size 1..TFD_MAX_PAGE.
+ *   table    device int32 [requests][ldt], ldt >= max_pages >= 1, requests * max_pages < 2^31:
+ *            entries up to held[r] are the request's pages; entries behind what it then holds are left as they were.
+ *   held     device int32 [requests], in and out. free_ids device int32 [pages], n_free device int32,
+ *            in and out; pages >= 1 is the number of the cache's pages.
+ *   row_start device int32 [requests + 1]; slots, pos device int32 [rows], or both NULL (rows 0).
+ *   No array overlaps another.
+ *   TFD_ERR_DEVICE_DATA: a negative length or count, a held count outside [0, max_pages] or a
+ *   request that needs more than max_pages (it keeps its pages, its rows get slot and position -1; a
+ *   negative count counts as 0); pages that run out (a request whose missing pages, counted with those of
+ *   the requests before it, exceed the free ones gets none: it keeps what it holds, the table entries of the
+ *   missing pages and its rows' slots and positions become -1); an n_free outside [0, pages], or more pages given
+ *   back than the stack has room for (no page moves); a page id outside [0, pages) (slot -1); more
+ *   rows than `rows` (those are not written).
+ */
+tfd_status tfd_page_plan(const int32_t* lens, const int32_t* n_new, int requests, int page_size,
+                         int32_t* table, int64_t ldt, int max_pages, int32_t* held,
+                         int32_t* free_ids, int pages, int32_t* n_free, int32_t* row_start,
+                         int32_t* slots, int32_t* pos, int64_t rows, int32_t* dev_status,
+                         void* stream);
+
+/*
+ * tfd_paged_append - write rows of keys and values into their slots of a paged cache.
+ *   Beside tfd_absorb, which writes a span into each stream's ring. For row i and head h:
+ *     k' = rope(rmsnorm(k_rows[i][h]) * k_gamma, pos[i]), each step as `qk` names it;
+ *     bf16: the cache takes bf16(k') and v_rows[i][h]; E4M3: s = fl32(amax / 448) and
+ *     e4m3_rne_sat(fl32(x / s)) of k' (not rounded to bf16 before) and of v_rows[i][h] (amax 0 keeps its zeros).
+ *   The normalisation and rotation are those of tfd_window_attn.
+ * Args:
+ *   k_rows, v_rows device bf16 [rows][heads][dim], row strides ldk, ldv >= heads * dim, multiples
+ *            of 8, 16-byte aligned; rows >= 1, rows * heads < 2^31.
+ *   slots    device int32 [rows]: -1 leaves the row out; the others differ. Any other slot outside the cache, or a
+ *            negative position (with TFD_QK_ROPE), sets TFD_ERR_DEVICE_DATA and the row is left out.
+ *   pos      device int32 [rows] (may be NULL without TFD_QK_ROPE); k_gamma device bf16 [dim] or NULL
+ *            (ones). E4M3 wants finite rows. The cache overlaps no input.
+ */
+tfd_status tfd_paged_append(const void* k_rows, int64_t ldk, const void* v_rows, int64_t ldv,
+                            const int32_t* slots, const int32_t* pos, int rows, int qk,
+                            const void* k_gamma, float eps, float rope_base,
+                            const tfd_kv_pages* cache, int32_t* dev_status, void* stream);
+
+/*
+ * tfd_paged_attn - attention of each request's new rows (1 for a decode step, up to 32 for a verify
+ *   window) over its tokens in a paged cache, the new rows' own among them (append them first).
+ *   Request r has rows row_start[r] .. row_start[r + 1] - 1 of q, and lens[r] tokens before them; the
+ *   token of its row j is lens[r] + j. Query head h reads key head h / (q_heads / heads):
+ *     q' = rope(rmsnorm(q) * q_gamma, p), each step as `qk` names it;
+ *     out = softmax(scale * q' . k) . v over the tokens that the row sees; lse = ln sum exp(scale *
+ *     q' . k) over them.
+ *   A row sees the tokens before the new ones, and of the new ones those up to itself; with `tree`
+ *   those whose bit its word has set instead (bit j: row j; bits past the rows say nothing). With
+ *   window >= 0 only tokens at depth >= its own - window: a cached token's depth is its number, a new
+ *   row's lens[r] + j, or with `tree` lens[r] + (bits set in its word) - 1. A row that sees nothing
+ *   gets zeros and an lse of -inf. What a row does not see (pages not in use, tokens behind the last, masked rows) may
+ *   hold anything, NaN too.
+ *   Sums and softmax statistics in fp32. q' enters its products as two bf16 parts (E4M3: two f16
+ *   parts of q' over a power of two), within 2^-16 of it; probabilities as two bf16 parts, within 2^-16.
+ * Args:
+ *   q        device bf16 [rows][q_heads][dim], row stride ldq >= q_heads * dim, a multiple of 8,
+ *            16-byte aligned; q_heads a multiple of the cache's heads, at most 64 times as many.
+ *   table    device int32 [requests][ldt], ldt >= max_pages; lens device int32 [requests]; row_start
+ *            device int32 [requests + 1], from 0 to at most rows; max_new: no request has more rows,
+ *            1..TFD_MAX_ROWS.
+ *   pos      device int32 [rows] or NULL (the rows' depths): positions for TFD_QK_ROPE.
+ *   tree     device int32 [rows] (32 bits) or NULL. window -1 or >= 0. scale > 0, or 0 for 1 / sqrt(dim).
+ *   q_gamma  device bf16 [dim] or NULL (ones).
+ *   out      device bf16 [rows][ldo], ldo >= q_heads * dim, a multiple of 8, 16-byte aligned; lse device float
+ *            [rows][q_heads] or NULL. Rows of no request are left as they were. Outputs overlap no input.
+ *   ws       device workspace of tfd_paged_attn_workspace() bytes.
+ *   TFD_ERR_DEVICE_DATA: a request whose length is negative, whose tokens exceed max_pages or 2^31 - 1025,
+ *   or whose rows are not 0..max_new rows within `rows` (its rows are left as they were); a page id outside [0, pages) where a
+ *   token is needed (those tokens are not seen); a negative position (counts as 0).
+ */
+size_t tfd_paged_attn_workspace(int max_new, int q_heads, int heads, int dim);
+tfd_status tfd_paged_attn(const void* q, int64_t ldq, int rows, int q_heads,
+                          const tfd_kv_pages* cache, const int32_t* table, int64_t ldt,
+                          int max_pages, const int32_t* lens, const int32_t* row_start,
+                          int requests, int max_new, const int32_t* pos, const int32_t* tree,
+                          int window, int qk, const void* q_gamma, float eps, float rope_base,
+                          float scale, void* out, int64_t ldo, float* lse, void* ws,
+                          size_t ws_bytes, int32_t* dev_status, void* stream);
 
 #ifdef __cplusplus
 }

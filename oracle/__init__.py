@@ -18,6 +18,7 @@ Modules (each function cites the passage it follows):
 * ``accept``    - accept-prefix count with per-position asked/kept histograms.
 * ``sample``    - tokens drawn from filtered logits, and the rejection accept of such drafts.
 * ``lora``      - low-rank adapters of many requests beside a shared projection.
+* ``paged``     - a paged key-value cache: page tables, append, attention over the pages.
 * ``draft_pass``- the chained multi-step draft pass (composition of the above).
 
 Every function here is pinned by ``tests/test_oracle_*.py`` against closed forms, brute force,

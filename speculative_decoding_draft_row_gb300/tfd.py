@@ -17,9 +17,23 @@ W_BF16, W_FP8_ROW, W_FP8_BLOCK32, W_FP8_BLOCK32_IL = 0, 1, 2, 3
 X_BF16, X_F32, X_BF16_E4M3 = 0, 1, 2
 OUT_NONE, OUT_F32, OUT_BF16, OUT_ADD_BF16 = 0, 1, 2, 3
 MAX_ROWS, MAX_TOPK, MAX_WINDOW = 32, 512, 511
+MAX_REQUESTS, MAX_PAGE = 8192, 1024
+KV_BF16, KV_E4M3 = 0, 1
+QK_NORM, QK_ROPE = 1, 2
 
 _c = ctypes
 _vp, _i64, _i32, _sz, _f32 = _c.c_void_p, _c.c_int64, _c.c_int, _c.c_size_t, _c.c_float
+
+
+class _KvPages(_c.Structure):
+    """tfd_kv_pages"""
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scales", _vp), ("v_scales", _vp),
+                ("page_stride", _i64), ("token_stride", _i64), ("head_stride", _i64),
+                ("pages", _c.c_int32), ("page_size", _c.c_int32), ("heads", _c.c_int32),
+                ("dim", _c.c_int32), ("fmt", _c.c_int32)]
+
+
+_kv = _c.POINTER(_KvPages)
 
 SIGNATURES = {
     "tfd_status_string": (_c.c_char_p, [_i32]),
@@ -48,6 +62,14 @@ SIGNATURES = {
                                   _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "tfd_lora": (_i32, [_vp, _i32, _i64, _i64, _vp, _vp, _i32, _i32, _i64, _vp, _vp, _i32, _vp, _i64,
                         _vp, _i64, _vp, _vp]),
+    "tfd_page_plan": (_i32, [_vp, _vp, _i32, _i32, _vp, _i64, _i32, _vp, _vp, _i32, _vp, _vp, _vp,
+                             _vp, _i64, _vp, _vp]),
+    "tfd_paged_append": (_i32, [_vp, _i64, _vp, _i64, _vp, _vp, _i32, _i32, _vp, _f32, _f32, _kv,
+                                _vp, _vp]),
+    "tfd_paged_attn_workspace": (_sz, [_i32, _i32, _i32, _i32]),
+    "tfd_paged_attn": (_i32, [_vp, _i64, _i32, _i32, _kv, _vp, _i64, _i32, _vp, _vp, _i32, _i32,
+                              _vp, _vp, _i32, _i32, _vp, _f32, _f32, _f32, _vp, _i64, _vp, _vp,
+                              _sz, _vp, _vp]),
     "tfd_absorb": (_i32, [_vp, _vp, _vp, _f32, _f32, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32,
                           _vp, _vp]),
 }
@@ -473,3 +495,143 @@ def tfd_lora(x, a, b, adapter_ids, base=None, y=None, scales=None, out_mode=OUT_
     if st:
         _check("tfd_lora", st)
     return y
+
+
+class KvPages:
+    """A paged key-value cache: k and v [pages][page_size][heads][dim], bf16 or E4M3 codes (uint8 or
+    float8_e4m3fn, with float32 scales [pages][heads][page_size]). The elements of a vector adjoin; k
+    and v have one shape and the same strides, in any order (a cache laid out [pages][heads][page_size]
+    [dim] is passed as its .transpose(1, 2)). The object holds the tensors; their memory is the
+    caller's, and calls read and write it in place."""
+
+    def __init__(self, k, v, k_scales=None, v_scales=None):
+        bf = k.dtype is torch.bfloat16
+        if not bf and k.dtype not in (torch.uint8, torch.float8_e4m3fn):
+            raise ValueError("k: bfloat16, uint8 or float8_e4m3fn is wanted")
+        if k.dim() != 4 or v.shape != k.shape or v.dtype is not k.dtype or v.device != k.device:
+            raise ValueError("k and v: [pages][page_size][heads][dim] of one type on one device")
+        pages, page_size, heads, dim = k.shape
+        # a stride of something that is there once says nothing: a valid one takes its place
+        strides = [[s if n > 1 else dim for s, n in zip(t.stride()[:3], t.shape)] for t in (k, v)]
+        if strides[0] != strides[1] or k.stride(3) != 1 or v.stride(3) != 1:
+            raise ValueError("k and v: the same strides and contiguous vectors are wanted")
+        if bf != (k_scales is None) or bf != (v_scales is None):
+            raise ValueError("k_scales and v_scales: wanted for E4M3 codes, and only for them")
+        for t in (k_scales, v_scales):
+            if t is not None and (t.dtype is not torch.float32 or t.device != k.device or
+                                  t.shape != (pages, heads, page_size) or not t.is_contiguous()):
+                raise ValueError("scales: contiguous float32 [pages][heads][page_size] is wanted")
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self.pages, self.page_size, self.heads, self.dim = pages, page_size, heads, dim
+        self.device_index = k.get_device()
+        self.c = _KvPages(k.data_ptr(), v.data_ptr(), _p(k_scales), _p(v_scales), *strides[0], pages,
+                          page_size, heads, dim, KV_BF16 if bf else KV_E4M3)
+        self.ref = _c.byref(self.c)
+
+
+def _qk(norm, rope):
+    return (QK_NORM if norm else 0) | (QK_ROPE if rope else 0)
+
+
+def _vectors_of(t, rows, heads, dim, dev, name):
+    """Row stride of bf16 rows [rows][heads][dim] whose heads adjoin."""
+    s0, s1, s2 = t.stride()
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev or t.shape != (rows, heads, dim) or \
+            s2 != 1 or (s1 != dim and heads > 1):
+        raise ValueError(f"{name}: bfloat16 [{rows}][{heads}][{dim}] with contiguous rows on the "
+                         "current CUDA device is wanted")
+    return s0 if rows > 1 else max(s0, heads * dim)
+
+
+def _cache_here(cache, dev):
+    if cache.device_index != dev:
+        raise ValueError("the cache is not on the current CUDA device")
+
+
+def tfd_page_plan(lens, n_new, page_size, table, held, free_ids, n_free, row_start=None, slots=None,
+                  pos=None, rows=None, dev_status=None, stream=None):
+    """Pages for lens + n_new tokens a request [requests] (int32): updates table [requests][max pages],
+    held [requests] and the free stack (free_ids [pages], n_free [1]) in place; the row starts
+    [requests + 1], and the slots and positions of the new rows ([rows] each, -1 behind the last row; made
+    when ``rows`` is given). Returns (row_start, slots, pos)."""
+    i32, dev, vec = torch.int32, _current_device(), _vec
+    requests, = lens.shape
+    max_pages = table.shape[1]
+    ldt = _rows_of(table, requests, max_pages, i32, dev, "table")
+    if row_start is None:
+        row_start = torch.empty(requests + 1, dtype=i32, device=lens.device)
+    if rows is not None and slots is None:
+        slots = torch.empty(rows, dtype=i32, device=lens.device)
+    if slots is not None and pos is None:
+        pos = torch.empty_like(slots)
+    rows = 0 if slots is None else slots.numel()
+    st = (_lib or library()).tfd_page_plan(
+        vec(lens, i32, requests, dev, "lens"), vec(n_new, i32, requests, dev, "n_new"), requests,
+        page_size, table.data_ptr(), ldt, max_pages, vec(held, i32, requests, dev, "held"),
+        vec(free_ids, i32, free_ids.numel(), dev, "free_ids"), free_ids.numel(),
+        vec(n_free, i32, 1, dev, "n_free"), vec(row_start, i32, requests + 1, dev, "row_start"),
+        vec(slots, i32, rows, dev, "slots"), vec(pos, i32, rows, dev, "pos"), rows,
+        vec(dev_status, i32, 1, dev, "dev_status"), _stream(stream, dev))
+    if st:
+        _check("tfd_page_plan", st)
+    return row_start, slots, pos
+
+
+def tfd_paged_append(k_rows, v_rows, slots, pos, cache, k_gamma=None, norm=True, rope=True, eps=1e-6,
+                     rope_base=10000.0, dev_status=None, stream=None):
+    """Write k_rows and v_rows [rows][heads][dim] (bf16, any row stride) into the cache's slots [rows]
+    (-1: left out), the keys normalised (k_gamma [dim]) and turned to their positions pos [rows]."""
+    i32, dev, vec = torch.int32, _current_device(), _vec
+    _cache_here(cache, dev)
+    rows = k_rows.shape[0]
+    ldk = _vectors_of(k_rows, rows, cache.heads, cache.dim, dev, "k_rows")
+    ldv = _vectors_of(v_rows, rows, cache.heads, cache.dim, dev, "v_rows")
+    st = (_lib or library()).tfd_paged_append(
+        k_rows.data_ptr(), ldk, v_rows.data_ptr(), ldv, vec(slots, i32, rows, dev, "slots"),
+        vec(pos, i32, rows, dev, "pos"), rows, _qk(norm, rope),
+        vec(k_gamma, torch.bfloat16, cache.dim, dev, "k_gamma"), eps, rope_base, cache.ref,
+        vec(dev_status, i32, 1, dev, "dev_status"), _stream(stream, dev))
+    if st:
+        _check("tfd_paged_append", st)
+
+
+def tfd_paged_attn_workspace(max_new, q_heads, heads, dim):
+    return library().tfd_paged_attn_workspace(max_new, q_heads, heads, dim)
+
+
+def tfd_paged_attn(q, cache, table, lens, row_start, max_new, pos=None, tree=None, window=-1,
+                   q_gamma=None, norm=True, rope=True, eps=1e-6, rope_base=10000.0, scale=0.0,
+                   out=None, lse=None, want_lse=False, ws=None, dev_status=None, stream=None):
+    """Attention of the rows of q [rows][q_heads][dim] (request r: rows row_start[r] .. row_start[r + 1]
+    - 1, at most max_new) over the lens[r] cached tokens and the new ones. tree [rows]: int32 words whose
+    bit j shows row j of the request (None: causal). window -1: all tokens. scale 0: 1 / sqrt(dim).
+    Returns (out [rows][q_heads * dim] bf16, lse [rows][q_heads] float32 or None)."""
+    i32, f32, dev, vec = torch.int32, torch.float32, _current_device(), _vec
+    _cache_here(cache, dev)
+    rows, q_heads, dim = q.shape
+    requests, = lens.shape
+    if dim != cache.dim:
+        raise ValueError("q and the cache have heads of different sizes")
+    ldq = _vectors_of(q, rows, q_heads, dim, dev, "q")
+    max_pages = table.shape[1]
+    ldt = _rows_of(table, requests, max_pages, i32, dev, "table")
+    if out is None:
+        out = torch.empty((rows, q_heads * dim), dtype=torch.bfloat16, device=q.device)
+    ldo = _rows_of(out, rows, q_heads * dim, torch.bfloat16, dev, "out")
+    if lse is None and want_lse:
+        lse = torch.empty((rows, q_heads), dtype=f32, device=q.device)
+    if ws is None:
+        ws = zeroed_workspace(tfd_paged_attn_workspace(max_new, q_heads, cache.heads, dim), q.device)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws: a contiguous tensor on the current CUDA device is wanted")
+    st = (_lib or library()).tfd_paged_attn(
+        q.data_ptr(), ldq, rows, q_heads, cache.ref, table.data_ptr(), ldt, max_pages,
+        vec(lens, i32, requests, dev, "lens"), vec(row_start, i32, requests + 1, dev, "row_start"),
+        requests, max_new, vec(pos, i32, rows, dev, "pos"), vec(tree, i32, rows, dev, "tree"),
+        window, _qk(norm, rope), vec(q_gamma, torch.bfloat16, dim, dev, "q_gamma"), eps, rope_base,
+        scale, out.data_ptr(), ldo, vec(lse, f32, rows * q_heads, dev, "lse"), ws.data_ptr(),
+        ws.numel() * ws.element_size(), vec(dev_status, i32, 1, dev, "dev_status"),
+        _stream(stream, dev))
+    if st:
+        _check("tfd_paged_attn", st)
+    return out, lse
