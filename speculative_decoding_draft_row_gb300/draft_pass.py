@@ -8,8 +8,8 @@ linears" (wo and w2 in e4m3 with a row scale; a pass's steps captured once as a 
 replayed). The steps' inputs (q, k, v, the w2 input, positions) are staged in fixed buffers so the
 whole pass can be captured. Every computation is a libtfd call; this module only marshals buffers.
 
-Two options, both off by default, serve requests of their own kind (the pages' pass is greedy, with
-one set of weights):
+Three options, all off by default, serve requests of their own kind (the pages' pass is greedy, with
+one set of weights and contexts of a ring):
 
 * ``adapters`` gives wo, w2 and/or the head low-rank adapters; each stream names its own
   (``adapter_ids``, -1 for none), and its term is added to the projection's result.
@@ -17,6 +17,9 @@ one set of weights):
   top-k, top-p, min-p and the random numbers are fixed buffers per stream) and keeps the
   distributions; the accept is then the rejection accept against the target's distributions ``p``,
   which also draws the round's next token.
+* ``paged`` keeps keys and values in pages that all streams share instead of rings, so that contexts
+  can be of any length: each step plans its row's page from the positions (a pass that starts before the
+  last one's end gives the pages of drafts that were turned down back), appends it and attends.
 """
 import torch
 
@@ -35,12 +38,24 @@ def unit_f32(v):
 class DraftPass:
     def __init__(self, wo_codes, wo_scales, w2_codes, w2_scales, head, head_fmt, head_scales,
                  k_ring, v_ring, window, steps, eps=1e-6, rope_base=10000.0, adapters=None,
-                 adapter_scales=None, sampled=False):
+                 adapter_scales=None, sampled=False, paged=None):
         """``adapters``: {"wo" | "w2" | "head": (a [adapters][rank][in], b [adapters][out][rank])},
-        all with the same number of adapters; ``adapter_scales`` float32 [adapters] or None."""
+        all with the same number of adapters; ``adapter_scales`` float32 [adapters] or None.
+        ``paged``: dict(cache=KvPages, table [streams][max pages], held [streams], free_ids [pages],
+        n_free [1]), all updated in place; k_ring and v_ring are then None, window -1 (all tokens) or
+        any, and the cache may have fewer heads than the queries."""
         dev = head.device
         self.steps = steps
-        self.S, self.ring, self.H, self.D = k_ring.shape
+        self.paged = dict(paged) if paged is not None else None
+        if paged is None:
+            self.S, self.ring, self.H, self.D = k_ring.shape
+            kv_heads = self.H
+        else:
+            if k_ring is not None or v_ring is not None:
+                raise ValueError("paged: the rings are not used (None)")
+            cache = paged["cache"]
+            self.S, self.ring, self.D, kv_heads = paged["table"].shape[0], None, cache.dim, cache.heads
+            self.H = wo_codes.shape[1] // self.D
         self.hidden = wo_codes.shape[0]
         self.inner = w2_codes.shape[1]
         self.window, self.eps, self.rope_base = window, eps, rope_base
@@ -50,8 +65,8 @@ class DraftPass:
         S, H, D = self.S, self.H, self.D
         bf = torch.bfloat16
         self.q = torch.zeros((steps, S, H, D), dtype=bf, device=dev)
-        self.k = torch.zeros_like(self.q)
-        self.v = torch.zeros_like(self.q)
+        self.k = torch.zeros((steps, S, kv_heads, D), dtype=bf, device=dev)
+        self.v = torch.zeros_like(self.k)
         self.u = torch.zeros((steps, S, self.inner), dtype=bf, device=dev)
         self.pos = torch.zeros((steps, S), dtype=torch.int32, device=dev)
         self.resid = torch.zeros((S, self.hidden), dtype=bf, device=dev)
@@ -65,6 +80,13 @@ class DraftPass:
         self.kept_hist = torch.zeros(steps, dtype=torch.int64, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         self.ws = tfd.zeroed_workspace(tfd.tfd_head_gemv_workspace(S, head.shape[0], 1), dev)
+        if self.paged is not None:
+            i32 = dict(dtype=torch.int32, device=dev)
+            self.one_row = torch.ones(S, **i32)
+            self.row_start = torch.zeros(S + 1, **i32)
+            self.slots, self.slot_pos = torch.zeros(S, **i32), torch.zeros(S, **i32)
+            self.attn_ws = tfd.zeroed_workspace(
+                tfd.tfd_paged_attn_workspace(1, H, kv_heads, D), dev)
         self.graph = None
         self.adapters = dict(adapters or {})
         if set(self.adapters) - {"wo", "w2", "head"}:
@@ -130,6 +152,17 @@ class DraftPass:
                          dev_status=self.status)
 
     def step_attn(self, t):
+        if self.paged is not None:
+            p, cache = self.paged, self.paged["cache"]
+            tfd.tfd_page_plan(self.pos[t], self.one_row, cache.page_size, p["table"], p["held"],
+                              p["free_ids"], p["n_free"], row_start=self.row_start,
+                              slots=self.slots, pos=self.slot_pos, dev_status=self.status)
+            tfd.tfd_paged_append(self.k[t], self.v[t], self.slots, self.slot_pos, cache,
+                                 eps=self.eps, rope_base=self.rope_base, dev_status=self.status)
+            tfd.tfd_paged_attn(self.q[t], cache, p["table"], self.pos[t], self.row_start, 1,
+                               window=self.window, eps=self.eps, rope_base=self.rope_base,
+                               out=self.attn, ws=self.attn_ws, dev_status=self.status)
+            return
         tfd.tfd_window_attn(self.q[t], self.k[t], self.v[t], self.pos[t], self.k_ring, self.v_ring,
                             self.window, eps=self.eps, rope_base=self.rope_base, out=self.attn,
                             dev_status=self.status)
@@ -189,8 +222,10 @@ class DraftPass:
 
     def launches(self):
         """Kernels of this library one pass launches: per step attention, wo, w2 and head, one more
-        for each adapted projection, and one for a draft taken from written logits; the accept."""
-        per = 4 + len(self.adapters) + (1 if self.logits is not None else 0)
+        for each adapted projection, one for a draft taken from written logits, two for pages; the
+        accept."""
+        per = 4 + (2 if self.paged is not None else 0) + len(self.adapters) + \
+            (1 if self.logits is not None else 0)
         return per * self.steps + 1
 
     def capture(self):
