@@ -439,7 +439,7 @@ tfd_status tfd_lora(const void* x, int rows, int64_t k, int64_t ldx, const void*
  *             E4M3 codes. Elements of a vector adjoin; the strides are multiples of 16 bytes, in any
  *             order ([page][head][token] as well), k and v 16-byte aligned.
  *   k_scales, v_scales device float [pages][heads][page_size] (E4M3 only, else NULL): a vector is its
- *             codes times its scale. No row sees a NaN code (0x7F, 0xFF).
+ *             codes times its scale (not negative). No row sees a NaN code (0x7F, 0xFF).
  * A slot is page * page_size + the token's place in the page; pages * page_size < 2^31. page_size
  * 1..TFD_MAX_PAGE; heads 1..1024; dim 64 or 128 (others: TFD_ERR_UNSUPPORTED).
  */
@@ -525,8 +525,8 @@ tfd_status tfd_paged_append(const void* k_rows, int64_t ldk, const void* v_rows,
  *   row's lens[r] + j, or with `tree` lens[r] + (bits set in its word) - 1. A row that sees nothing
  *   gets zeros and an lse of -inf. What a row does not see (pages not in use, tokens behind the last, masked rows) may
  *   hold anything, NaN too.
- *   Sums and softmax statistics in fp32. q' enters its products as two bf16 parts (E4M3: two f16
- *   parts of q' over a power of two), within 2^-16 of it; probabilities as two bf16 parts, within 2^-16.
+ *   Sums and softmax statistics in fp32. q' enters its products as two bf16 parts (E4M3: four 8-bit parts),
+ *   within 2^-16 of it; probabilities as two bf16 parts, within 2^-16 (E4M3: as f16, 2^-11).
  * Args:
  *   q        device bf16 [rows][q_heads][dim], row stride ldq >= q_heads * dim, a multiple of 8,
  *            16-byte aligned; q_heads a multiple of the cache's heads, at most 64 times as many.

@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kT) paged_append_kernel(const Args<D> a) {
   float gm[8], sn[8], cs[8];
   if (a.qk & TFD_QK_ROPE) {
 #pragma unroll
-    for (int i = lane; i < D / 2; i += 32) rope_pair<D>(p, a.turns, i, turn[warp][i].y, turn[warp][i].x);
+    for (int i = lane; i < D / 2; i += 32) rope_pair_pi<D>(p, a.turns, i, turn[warp][i].y, turn[warp][i].x);
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {

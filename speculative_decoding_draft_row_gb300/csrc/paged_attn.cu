@@ -1,24 +1,18 @@
-// paged_attn.cu - attention of a request's new rows over its tokens in a paged key-value cache, one
-// pass with a running maximum and sum, split over the cache's length and joined.
+// paged_attn_tc.cu - attention of a request's new rows over its tokens in a paged key-value cache, on the
+// tensor cores with accumulators in tensor memory: one pass with a running maximum and sum, split over
+// the cache's length and joined.
 //
-// Work. A unit is one request, one key head, and up to 16 MT of its (row, query head) pairs, which share
-// every key and value read. The units' tokens, cut into tiles, form one line over all requests; each
+// Work. A unit is one request, one key head, and up to N of its (row, query head) pairs, which share
+// every key and value read. The units' tokens, cut into tiles of 128, form one line over all requests; each
 // block takes an equal stretch of it, found by a prefix sum over the requests that every block forms
 // for itself, so lengths can stay on the GPU and long requests spread over all SMs. A stretch that
 // covers a unit writes its rows; the others leave (maximum, sum, weighted values) in the workspace, and
 // the block that arrives last adds the unit's pieces in their order along the line (a counter for each block
-// in which a unit begins; nobody waits, and the sums' order does not depend on who is last).
+// in which a unit begins; nobody waits for another block, and the sums' order does not depend on who is last).
 //
-// A warp takes a slice of 16 or 32 tokens of each tile through a ring of its own in shared memory
-// (cp.async, 16 bytes a lane, 128-byte rows swizzled for ldmatrix), so no barrier stands in the loop. Scores and
-// values are warp-level MMAs with fp32 accumulators: at 16 rows a unit they need a third of the tensor
-// rate that the bytes leave, so q' and the probabilities go in as two bf16 parts each (2^-17 of their value)
-// instead of being rounded. E4M3 keys are widened to f16 (exact) against q' over a power of two in two
-// f16 parts; E4M3 values to bf16 (exact), their scales in the probabilities, which keep fp32's range.
-//
-// What a row does not see gets a score of -inf and a weight of zero; tokens past the last and on bad
-// pages are zero-filled. In slices with hidden tokens whose values hold an infinity or NaN (0 times
-// which would be NaN) the weights are multiplied by hand, only where the row sees the token.
+// A tile: S^T = K q'^T (128 tokens x N) and O^T += V^T P^T (dim x N). With the tokens and the dims as the 128 rows of
+// the products no part of them is padding, whatever N is, and keys and values are read from shared
+// memory as they come: keys as rows of dims, values as columns (MN-major).
 #include <cuda_fp16.h>
 
 #include "paged.cuh"
@@ -27,12 +21,24 @@ namespace {
 
 using namespace tfd;
 
-constexpr int kT = 128;
-constexpr int kW = kT / 32;
-constexpr int kStages = 3;
-constexpr int kPerSm = 2;
+constexpr int kTile = 128;                   // tokens of a tile
+constexpr int kCols = 16;                    // rows of a unit that one softmax group takes
+constexpr int kGroup = 128;                  // its threads, one a token; then one a dim
+constexpr int kAhead = 3;                    // pieces found ahead
+constexpr int kKeep = 4;                     // tiles that a unit's end keeps
+constexpr float kUnset = -3.0e38f;           // a reference that no score has set
+// Warps: the softmax groups, the one that issues products, those that fetch, the one that finds pieces.
+template <int N>
+struct Roles {
+  static constexpr int kGroups = N / kCols, kSoft = kGroups * kGroup;
+  static constexpr int kFetch = N == 16 ? 128 : 64;  // threads that fetch (more where registers allow)
+  static constexpr int kMmaWarp = kSoft / 32, kWalkWarp = kMmaWarp + 1 + kFetch / 32;
+  static constexpr int kT = 32 * (kWalkWarp + 1);
+  static constexpr int kReaders = kSoft / 32 + 1 + kFetch / 32;  // warps that read a piece
+};
 constexpr int kMostTokens = 0x7fffffff - 1024;  // of a request: a tile behind them is still an int
-constexpr int kMaxBlocks = 304;  // blocks of a launch at most: 2 an SM of 152
+constexpr int kMaxBlocks = 152;              // blocks of a launch at most, one an SM
+constexpr float kHead = 8.0f;                // powers of two that a weight may pass its reference by
 
 template <int D>
 struct Args {
@@ -48,68 +54,156 @@ struct Args {
   uint16_t* out;
   int64_t ldo;
   float* lse;
-  int32_t* count;   // [kMaxBlocks], zero between calls
+  int32_t* count;   // [kMaxBlocks][N / 16], zero between calls
   float2* ml;       // [2 kMaxBlocks][rows of a unit]: maximum and sum (base 2)
   float* acc;       // [2 kMaxBlocks][rows of a unit][D]
   int32_t* dev_status;
   tfd_kv_pages c;
   int rows, q_heads, group, max_pages, requests, max_new, window, qk;
   float eps, scale;  // scale: times log2 e
+  uint32_t page_mul, page_shift;  // token / page_size = token * page_mul >> page_shift
   RopeTurns<D> turns;
 };
 
-// Tokens of a slice and of a tile; bytes of a vector; stage of a warp: keys, values, scales, which tokens are there.
-template <int D, bool kF8>
-struct Shape {
-  static constexpr int kRow = D * (kF8 ? 1 : 2);
-  static constexpr int kKeys = kRow == 256 ? 16 : 32;
-  static constexpr int kTile = kW * kKeys;
-  static constexpr int kPlane = kKeys * kRow;
-  static constexpr int kScales = 2 * kPlane;               // offset: kKeys floats of k, then of v
-  static constexpr int kMask = kScales + (kF8 ? 8 * kKeys : 0);
-  static constexpr int kStage = kMask + 16;
-  static constexpr int kRing = (kW * kStages * kStage + 127) / 128 * 128;
-};
-
+// ---- PTX -----------------------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t sa(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(in ? 16 : 0)
                : "memory");
 }
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool in) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0)
-               : "memory");
+// The barrier gets this thread's arrival when all copies that it has issued are there.
+__device__ __forceinline__ void copy_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void fence_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(at));
+__device__ __forceinline__ void fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t at) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(at));
+__device__ __forceinline__ void fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
-template <bool kHalf>
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if (kHalf)
+__device__ __forceinline__ void bar_init(uint32_t bar, int count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t par) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(par)
+      : "memory");
+  return ok;
+}
+__device__ __forceinline__ bool bar_test_now(uint32_t bar, uint32_t par) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(par)
+      : "memory");
+  return ok;
+}
+__device__ __forceinline__ uint64_t now() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+// Bounded wait for the phase of parity `par` (about a second of global time); false on timeout.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t par) {
+  if (bar_test(bar, par)) return true;
+  uint64_t t0 = 0;
+  for (int it = 1;; ++it) {
+    if (bar_test(bar, par)) return true;
+    if (it % 64 == 0) {
+      const uint64_t t = now();
+      if (t0 == 0) t0 = t;
+      else if (t - t0 > 1000000000ull) return false;
+    }
+  }
+}
+// A softmax group's own barrier, and the OR of a predicate over it.
+__device__ __forceinline__ void group_sync(int id) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kGroup) : "memory");
+}
+__device__ __forceinline__ bool group_any(int id, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x), "r"(id), "n"(kGroup)
+      : "memory");
+  return r;
+}
+// Shared-memory matrix descriptors: strides in bytes between a tile's pieces. 128-byte swizzle (2) or
+// none (0).
+__device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lead, uint32_t stride, int swizzle) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(lead >> 4) << 16 |
+         (uint64_t)(stride >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)swizzle << 61;
+}
+// Instruction descriptor: fp32 accumulator, operands of types ta and tb (kind::f16: bf16 1; kind::f8f6f4:
+// E4M3 0, E5M2 1), 128 x n; which are MN-major.
+__device__ __forceinline__ uint32_t idesc(int n, uint32_t ta, uint32_t tb, bool mn_a, bool mn_b) {
+  return (1u << 4) | (ta << 7) | (tb << 10) | ((uint32_t)mn_a << 15) | ((uint32_t)mn_b << 16) |
+         ((uint32_t)(n >> 3) << 17) | (8u << 24);
+}
+template <bool kF8>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool acc) {
+  if (kF8)
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(desc), "r"((uint32_t)acc)
+        : "memory");
   else
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(desc), "r"((uint32_t)acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {  // not waited for
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+// Waits for the loads; no use of the values moves before it.
+template <int C>
+__device__ __forceinline__ void tmem_ld_wait(float (&v)[C]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < C; ++i) asm volatile("" : "+f"(v[i]));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15};" ::"f"(v[0]),
+      "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]),
+      "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "r"(taddr)
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 // 2^x (2^-22 relative); 0 for -inf.
 __device__ __forceinline__ float exp2_(float x) {
@@ -122,34 +216,47 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// Two floats as E4M3 codes (nearest, saturating), and back.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 e4m3_floats(uint32_t codes) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)codes));
+  return __half22float2(*reinterpret_cast<__half2*>(&r));
+}
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// Two E4M3 codes (the low half of w) as f16.
-__device__ __forceinline__ uint32_t e4m3_f16x2(uint16_t w) {
+__device__ __forceinline__ uint32_t sub16x2(uint32_t x, uint32_t y) {
   uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(w));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
   return r;
 }
-// Two E4M3 codes, each in the high byte of a half word, as bf16: the code's 7 bits placed 4 lower read
-// as its value times 2^-120 (exact, as are all E4M3 values; a NaN code reads as 480).
-__device__ __forceinline__ uint32_t e4m3_bf16x2(uint32_t w) {
-  const uint32_t x = (w & 0x80008000u) | ((w >> 4) & 0x07F007F0u);
+__device__ __forceinline__ uint32_t mul16x2(uint32_t x, uint32_t y) {
   uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x7B807B80u));  // 2^120
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+// The largest of a warp's values (NaN passed over), in all lanes.
+__device__ __forceinline__ float warp_most(float x) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
   return r;
 }
 __device__ __forceinline__ bool finite_(float x) { return fabsf(x) < INFINITY; }
 
-// Where 16-byte piece c of row r of a plane stands.
-template <int kRow>
-__device__ __forceinline__ uint32_t piece(int r, int c) {
-  if (kRow == 64) return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
-  return (uint32_t)(r * kRow + ((c ^ (r & 7)) << 4));
+// A token's place in its request's table.
+template <int D>
+__device__ __forceinline__ int page_of(const Args<D>& a, int64_t token) {
+  return (int)((uint64_t)(uint32_t)token * a.page_mul >> a.page_shift);
 }
 
+// ---- the line ------------------------------------------------------------------------------------
 struct Request {
   int r, row0, n, len;   // its rows and the tokens before them
   int64_t base;          // first tile of its first unit on the line
@@ -158,9 +265,8 @@ struct Request {
 };
 
 // Request r's part of the line.
-template <int D, bool kF8, int MT>
+template <int D, int N>
 __device__ __forceinline__ Request request(const Args<D>& a, int r) {
-  using S = Shape<D, kF8>;
   Request q;
   q.r = r;
   q.row0 = a.row_start[r];
@@ -171,47 +277,157 @@ __device__ __forceinline__ Request request(const Args<D>& a, int r) {
           (n > 0 && (q.len + n > (int64_t)a.max_pages * a.c.page_size || q.len + n > kMostTokens));
   q.n = q.bad ? 0 : (int)n;
   const int64_t lo = a.window >= 0 ? (int64_t)q.len - a.window - (a.tree ? 1 : 0) : 0;
-  q.tile0 = q.n > 0 && lo > 0 ? (int)(lo / S::kTile) : 0;
-  q.tiles = q.n > 0 ? (q.len + q.n - 1) / S::kTile + 1 - q.tile0 : 0;
-  q.mt = (q.n * a.group + 16 * MT - 1) / (16 * MT);
+  q.tile0 = q.n > 0 && lo > 0 ? (int)(lo / kTile) : 0;
+  q.tiles = q.n > 0 ? (q.len + q.n - 1) / kTile + 1 - q.tile0 : 0;
+  q.mt = (q.n * a.group + N - 1) / N;
   return q;
 }
 
-template <int D, bool kF8, int MT>
-struct Smem {
-  using S = Shape<D, kF8>;
-  static constexpr int kM = 16 * MT;                  // rows of a unit
-  static constexpr int kQ = S::kRing;                 // two parts of q', [kM] rows of 2 D bytes each
-  static constexpr int kRows = kQ + 2 * kM * 2 * D;   // per row: first cached token seen, new ones seen, factor
-  static constexpr int kStat = kQ;                    // [kW][kM] maximum and sum, when q' is done with
-  static constexpr int kBytes = kRows + kM * 12;
-  static_assert(kW * kM * 8 <= kRows - kQ, "the warps' statistics fit the place of q'");
-  static constexpr int kPitch = D + 8;                // floats of a row of the warps' sums, in the ring
-  static_assert(kW * kM * kPitch * 4 <= S::kRing, "the warps' sums fit the ring");
-  static_assert(kMaxBlocks * kM * 4 <= S::kRing, "the pieces' weights fit the ring");
+// A unit's part in a block's stretch of the line: what everyone needs to know of it.
+struct Piece {
+  int64_t line0;          // the unit's first tile on the line
+  int r, row0, n, len;    // request; its rows and the tokens before them
+  int tile0, tiles;       // the unit's first tile of tokens, its tiles
+  int first, cnt;         // of these the piece's: from, number (0: no more pieces)
+  int h, m0, valid;       // head; first of the unit's (row, query head) pairs, pairs there are
+  int j0, h0;             // that pair's row and query head within the group
 };
 
-template <int D, bool kF8, int MT>
-__global__ void __launch_bounds__(kT, kPerSm) paged_attn_kernel(const __grid_constant__ Args<D> a) {
-  using S = Shape<D, kF8>;
-  using M = Smem<D, kF8, MT>;
-  constexpr int kM = M::kM, kRow = S::kRow, kKeys = S::kKeys, NT = kKeys / 8, E = D / 32;
-  extern __shared__ __align__(128) unsigned char sm[];
-  __shared__ int64_t scan[kW];
-  __shared__ int64_t s_base;
-  __shared__ int s_r, s_last;
-  tfd_host::after_previous();
+// A block's odds and ends.
+struct Misc {
+  Request first;  // the request in which the block's cut falls
+  int64_t ends[2];
+  Piece piece[kAhead];
+  int last[4], odd[4];
+  uint32_t tmem;
+};
+
+// Cuts of the line. A cut falls every `share` tiles, but not within `keep` tiles of a unit's ends (there
+// it moves to that end), nor in a unit of fewer than 2 keep: a piece that small costs more, being joined,
+// than it takes off its neighbour. Where a unit of `tiles` that begins at `line0` is cut from, and its pieces:
+struct Cuts {
+  int64_t share;
+  int keep;
+  // the block that has the unit's first tile
+  __device__ __forceinline__ int64_t owner(int64_t line0, int tiles) const {
+    return (line0 + min(tiles, keep + (tiles < 2 * keep ? tiles : 0)) - 1) / share;
+  }
+  __device__ __forceinline__ int64_t pieces(int64_t line0, int tiles) const {
+    if (tiles < 2 * keep) return 1;
+    return (line0 + tiles - keep) / share - owner(line0, tiles) + 1;
+  }
+  // where the cut at `t`, which lies in the unit, moves to
+  __device__ __forceinline__ int64_t moved(int64_t t, int64_t line0, int tiles) const {
+    if (tiles < 2 * keep || t - line0 < keep) return line0;
+    return t - line0 > tiles - keep ? line0 + tiles : t;
+  }
+};
+
+// Parts that a value of q' or a weight enters its products in, side by side as columns: two bf16 ones
+// against bf16 keys and values; four of 8 bits against E4M3 (q' in E4M3, weights in E5M2), of which the last two
+// stand for 2^-8 of what they are.
+template <int D, int N, bool kF8>
+struct Smem {
+  static constexpr int kParts = kF8 ? 4 : 2;
+  static constexpr int kSlot = kF8 ? kTile * 128 : kTile * D * 2;  // E4M3: rows of 128 bytes, whatever D is
+  static constexpr int kSlots = kF8 ? 12 : D == 64 ? 9 : N == 64 ? 5 : 6;  // keys and values of a tile in turn
+  static constexpr int kQ = kSlots * kSlot;                  // q': [row bytes / 128][parts N] rows of 128 bytes
+  static constexpr int kP = kQ + (kF8 ? 512 * N : 4 * N * D);  // weights: [parts N / (16 bytes)][128] x 16 bytes
+  static constexpr int kRows = kP + 4 * N * kTile;           // two of: a row's first cached token seen, new ones seen
+  static constexpr int kRef = kRows + 2 * N * 8;             // reference of each row
+  static constexpr int kFac = kRef + N * 4;
+  static constexpr int kRed = kFac + N * 4;                  // [N / 16][4][16]
+  static constexpr int kPow = kRed + N * 16;                 // E4M3: two of: the power of two of q' of each row
+  static constexpr int kBars = kPow + (kF8 ? 2 * N * 4 : 0);
+  static constexpr int kMisc = (kBars + 8 * (2 * kSlots + 10 + 2 * kAhead) + 15) / 16 * 16;
+  static constexpr int kBytes = kMisc + (int)sizeof(Misc);
+  static_assert(kBytes <= 227 * 1024, "shared memory of a block");
+  static constexpr uint32_t kWide = kParts * N;              // columns of a product
+  static constexpr uint32_t kTmem = kWide <= 32 ? 128 : kWide <= 64 ? 256 : 512;
+  static constexpr uint32_t kO = 2 * kWide;                  // scores twice, then the weighted values
+};
+
+// Sums of 16 columns over a warp: lanes 2 i and 2 i + 1 end with column i's in v[0].
+__device__ __forceinline__ void column_sums(float (&v)[kCols]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int n = 8, mask = 16; n > 0; n >>= 1, mask >>= 1) {
+    const bool up = lane & mask;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) {
+        const float keep = up ? v[i + n] : v[i], send = up ? v[i] : v[i + n];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, send, mask);
+      }
+  }
+  v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+}
+
+template <int D, int N, bool kF8>
+__global__ void __launch_bounds__(Roles<N>::kT, 1)
+paged_attn_kernel(const __grid_constant__ Args<D> a) {
+  using M = Smem<D, N, kF8>;
+  using R = Roles<N>;
+  constexpr int kFetch = R::kFetch, kT = R::kT, kMmaWarp = R::kMmaWarp, kWalkWarp = R::kWalkWarp;
+  extern __shared__ __align__(1024) unsigned char sm[];  // all of the block's: it begins on a swizzle's period
+  Misc& ms = *reinterpret_cast<Misc*>(sm + M::kMisc);
+  int64_t* scan = reinterpret_cast<int64_t*>(sm + M::kP);  // before there are weights
+  if (sa(sm) & 1023u) {
+    if (threadIdx.x == 0) set_dev_status(a.dev_status, TFD_ERR_CUDA);
+    return;
+  }
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t bars = sa(sm + M::kBars);
+  auto full = [&](int s) { return bars + 8u * s; };
+  auto empty = [&](int s) { return bars + 8u * (M::kSlots + s); };
+  const uint32_t more = bars + 16u * M::kSlots;
+  auto s_full = [&](int b) { return more + 8u * b; };
+  auto s_empty = [&](int b) { return more + 16u + 8u * b; };
+  const uint32_t p_full = more + 32u, p_empty = more + 40u, q_full = more + 48u, o_full = more + 56u,
+                 o_empty = more + 64u, drained = more + 72u;
+  auto w_full = [&](int e) { return more + 80u + 8u * e; };
+  auto w_empty = [&](int e) { return more + 80u + 8u * (kAhead + e); };
+  if (tid == 0) {
+    for (int s = 0; s < M::kSlots; ++s) {
+      bar_init(full(s), kFetch);
+      bar_init(empty(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      bar_init(s_full(b), 1);
+      bar_init(s_empty(b), R::kSoft);
+    }
+    bar_init(p_full, R::kSoft);
+    bar_init(p_empty, 1);
+    bar_init(q_full, R::kSoft);
+    bar_init(o_full, 1);
+    bar_init(o_empty, R::kSoft);
+    bar_init(drained, 1);
+    for (int e = 0; e < kAhead; ++e) {
+      bar_init(w_full(e), 1);
+      bar_init(w_empty(e), R::kReaders);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    for (int i = 0; i < 4; ++i) ms.odd[i] = 0;
+  }
+  constexpr uint32_t kTmem = M::kTmem, kO = M::kO, kWide = M::kWide;
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sa(&ms.tmem)),
+                 "r"(kTmem)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tfd_host::after_previous();
   const int H = a.c.heads, ps = a.c.page_size;
 
   // ---- this block's stretch of the line -----------------------------------------------------------
-  int64_t total;
+  int64_t total = 0;
+  Cuts cuts;
   {
     const int per = (a.requests + kT - 1) / kT;
     const int r0 = min(a.requests, tid * per), r1 = min(a.requests, r0 + per);
     int64_t mine = 0;
     for (int r = r0; r < r1; ++r) {
-      const Request q = request<D, kF8, MT>(a, r);
+      const Request q = request<D, N>(a, r);
       if (q.bad && blockIdx.x == 0) set_dev_status(a.dev_status, TFD_ERR_DEVICE_DATA);
       mine += (int64_t)q.tiles * q.mt * H;
     }
@@ -223,626 +439,865 @@ __global__ void __launch_bounds__(kT, kPerSm) paged_attn_kernel(const __grid_con
       if (lane >= d) x += (int64_t)((uint64_t)hi << 32 | lo);
     }
     if (lane == 31) scan[warp] = x;
+    fence_before();
     __syncthreads();
-    total = 0;
+    fence_after();
     int64_t before = x - mine;
-    for (int w = 0; w < kW; ++w) {
+    for (int w = 0; w < kT / 32; ++w) {
       if (w < warp) before += scan[w];
       total += scan[w];
     }
-    const int64_t share = (total + gridDim.x - 1) / gridDim.x, t0 = blockIdx.x * share;
-    if (t0 >= total) return;  // block-uniform
-    if (before <= t0 && t0 < before + mine) {  // one thread
-      int r = r0;
-      for (; r < r1 - 1; ++r) {
-        const Request q = request<D, kF8, MT>(a, r);
-        const int64_t u = (int64_t)q.tiles * q.mt * H;
-        if (t0 < before + u) break;
-        before += u;
+    cuts.share = (total + gridDim.x - 1) / gridDim.x;
+    cuts.keep = (int)min(cuts.share, (int64_t)kKeep);
+    // the block's stretch: from its cut to the next one's
+    if (tid < 2) ms.ends[tid] = total;
+    __syncthreads();
+    int64_t at = before;
+    for (int r = r0; r < r1; ++r) {  // for the threads in whose requests a cut falls
+      const int64_t lo = blockIdx.x * cuts.share, hi = lo + cuts.share;
+      if (!((before <= lo && lo < before + mine) || (before <= hi && hi < before + mine))) break;
+      Request q = request<D, N>(a, r);
+      const int64_t u = (int64_t)q.tiles * q.mt * H;
+      q.base = at;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int64_t t = e ? hi : lo;
+        if (at <= t && t < at + u) {
+          ms.ends[e] = cuts.moved(t, at + (t - at) / q.tiles * q.tiles, q.tiles);
+          if (e == 0) ms.first = q;
+        }
       }
-      s_r = r;
-      s_base = before;
+      at += u;
     }
     __syncthreads();
   }
-  const int64_t share = (total + gridDim.x - 1) / gridDim.x;
-  int64_t t = blockIdx.x * share;
-  const int64_t t_end = t + share < total ? t + share : total;
-  Request rq = request<D, kF8, MT>(a, s_r);
-  rq.base = s_base;
+  const uint32_t tmem = ms.tmem;
+  const int64_t t0 = ms.ends[0], t_end = ms.ends[1];
+  const int64_t steps = t_end - t0;  // tiles of the stretch
+  bool ok = true;                   // none of this thread's waits has run out
 
-  unsigned char* ring = sm + warp * kStages * S::kStage;
-  const uint32_t s_ring = sa(ring), s_q = sa(sm + M::kQ);
-  int* s_lo = reinterpret_cast<int*>(sm + M::kRows);
-  uint32_t* s_new = reinterpret_cast<uint32_t*>(s_lo + kM);
-  float* s_fac = reinterpret_cast<float*>(s_new + kM);
-  float2* s_stat = reinterpret_cast<float2*>(sm + M::kStat);
-  const int qr = lane >> 2, qc = lane & 3;  // this lane's row (and row + 8) and columns of an accumulator
+  // Piece k of the stretch, from the warp that finds them: a copy. All lanes of a warp call it.
+  auto get_piece = [&](int k, bool one_lane) {
+    const int e = k % kAhead;
+    if (ok) ok = bar_wait(w_full(e), (uint32_t)(k / kAhead) & 1u);
+    if (!one_lane) ok = __all_sync(0xffffffffu, ok);
+    Piece p = ms.piece[e];
+    if (!ok) p.cnt = 0;
+    if (!one_lane) __syncwarp();
+    if (one_lane || lane == 0) bar_arrive(w_empty(e));
+    return p;
+  };
 
-  while (t < t_end) {
-    while (t >= rq.base + (int64_t)rq.tiles * rq.mt * H) {
-      const int64_t next = rq.base + (int64_t)rq.tiles * rq.mt * H;
-      if (rq.r + 1 >= a.requests) return;  // the line ends before: lengths that changed meanwhile
-      rq = request<D, kF8, MT>(a, rq.r + 1);
-      rq.base = next;
+  if (steps > 0 && tid == 32 * kWalkWarp) {
+    // ---- the pieces, one after the other -------------------------------------------------------------
+    Request rq = ms.first;
+    int64_t t = t0;
+    for (int k = 0;; ++k) {
+      Piece p;
+      p.cnt = 0;
+      while (t < t_end && t >= rq.base + (int64_t)rq.tiles * rq.mt * H) {
+        const int64_t next = rq.base + (int64_t)rq.tiles * rq.mt * H;
+        if (rq.r + 1 >= a.requests) t = t_end;  // lengths that changed meanwhile
+        else rq = request<D, N>(a, rq.r + 1);
+        rq.base = next;
+      }
+      if (t < t_end) {
+        const int64_t unit = (t - rq.base) / rq.tiles;
+        p.line0 = rq.base + unit * rq.tiles;
+        p.r = rq.r, p.row0 = rq.row0, p.n = rq.n, p.len = rq.len, p.tile0 = rq.tile0, p.tiles = rq.tiles;
+        p.first = (int)(t - p.line0);
+        p.h = (int)(unit / rq.mt);
+        p.m0 = (int)(unit - (int64_t)p.h * rq.mt) * N;
+        p.cnt = (int)min((int64_t)(rq.tiles - p.first), t_end - t);
+        p.valid = min(N, rq.n * a.group - p.m0);
+        p.j0 = p.m0 / a.group;
+        p.h0 = p.m0 - p.j0 * a.group;
+        t += p.cnt;
+      }
+      const int e = k % kAhead;
+      if (k >= kAhead) ok = bar_wait(w_empty(e), (uint32_t)(k / kAhead - 1) & 1u);
+      if (!ok) break;
+      ms.piece[e] = p;
+      bar_arrive(w_full(e));
+      if (p.cnt == 0) break;
     }
-    const int64_t unit = (t - rq.base) / rq.tiles;
-    const int first = (int)(t - rq.base - unit * rq.tiles);  // tile of the unit
-    const int h = (int)(unit / rq.mt), m0 = (int)(unit - (int64_t)h * rq.mt) * kM;
-    const int cnt = (int)min((int64_t)(rq.tiles - first), t_end - t);
-    const int valid = min(kM, rq.n * a.group - m0);
-    const int tokens = rq.len + rq.n;
-    const int32_t* table = a.table + rq.r * a.ldt;
-    const unsigned char* kbase = (const unsigned char*)a.c.k;
-    const unsigned char* vbase = (const unsigned char*)a.c.v;
-
-    // ---- a warp's slice of a tile on its way ------------------------------------------------------
-    int page = 0;  // of this lane's token of the slice that is fetched next
-    auto token_of = [&](int i) {
-      return (int64_t)(rq.tile0 + first + i) * S::kTile + warp * kKeys + (lane & (kKeys - 1));
-    };
-    auto look_up = [&](int i) {
-      const int64_t tok = token_of(i);
-      page = i < cnt && tok < tokens ? table[(uint32_t)tok / (uint32_t)ps] : -1;
-    };
-    auto fetch = [&](int i) {
-      if (i < cnt) {
-        const int64_t tok = token_of(i);
-        const uint32_t st = s_ring + (uint32_t)(i % kStages) * S::kStage;
-        const bool in = page >= 0 && page < a.c.pages;
-        if (tok < tokens && !in) set_dev_status(a.dev_status, TFD_ERR_DEVICE_DATA);
-        const int at = (int)((uint32_t)tok % (uint32_t)ps);
-        const int64_t off =
-            in ? (page * a.c.page_stride + at * a.c.token_stride + h * a.c.head_stride) * (kF8 ? 1 : 2)
-               : -1;
-        const uint32_t there = __ballot_sync(0xffffffffu, in);
-        if (lane == 0) *reinterpret_cast<uint32_t*>(ring + (i % kStages) * S::kStage + S::kMask) =
-              kKeys == 32 ? there : there & 0xffffu;
-        constexpr int L = kRow / 16, P = 32 / L;  // lanes of a vector, vectors a step
+  } else if (steps > 0 && warp > kMmaWarp && warp < kWalkWarp) {
+    // ---- fetch: a warp half of each tile, a lane the pages of two tokens ----------------------------
+    constexpr int kMine = kTile / (kFetch / 32), kPer = kMine / 32;  // tokens of a warp, of a lane
+    constexpr int es = kF8 ? 1 : 2, L = D * es / 16, P = 32 / L;  // lanes of a vector, vectors a step
+    const int mine0 = kMine * (warp - kMmaWarp - 1), c = lane % L;
+    const unsigned char* kbase = (const unsigned char*)a.c.k + 16 * c;
+    const unsigned char* vbase = (const unsigned char*)a.c.v + 16 * c;
+    // where this lane's pieces go: rows mine0 + lane / L + j P, whose swizzle repeats after 8 rows
+    uint32_t to[8 / P];
 #pragma unroll
-        for (int j = 0; j < kKeys / P; ++j) {
-          const int row = j * P + lane / L, c = lane % L;
-          const int64_t o = __shfl_sync(0xffffffffu, off, row);
-          const uint32_t d = st + piece<kRow>(row, c);
-          const int64_t from = o >= 0 ? o + 16 * c : 0;
-          copy16(d, kbase + from, o >= 0);
-          copy16(d + S::kPlane, vbase + from, o >= 0);
+    for (int u = 0; u < 8 / P; ++u) {
+      const int row = mine0 + u * P + lane / L;
+      to[u] = (uint32_t)((c >> 3) * (kTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+    }
+    int slot = 0;
+    uint32_t round = 0;  // of the slots
+    for (int k = 0;; ++k) {
+      const Piece w = get_piece(k, false);
+      if (w.cnt == 0) break;
+      const int tokens = w.len + w.n;
+      const int32_t* table = a.table + w.r * a.ldt;
+      const int64_t head = w.h * a.c.head_stride;
+      int64_t tok = (int64_t)(w.tile0 + w.first) * kTile + mine0 + lane;
+      int pg[kPer], page[kPer];
+      auto look_up = [&](bool on) {
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) {
+          pg[q] = page_of(a, tok + 32 * q);
+          page[q] = on && tok + 32 * q < tokens ? table[pg[q]] : -1;
         }
-        if (kF8) {
-          const int64_t sc = in ? ((int64_t)page * H + h) * ps + at : 0;
-          copy4(st + S::kScales + 4 * lane, a.c.k_scales + sc, in);
-          copy4(st + S::kScales + 4 * kKeys + 4 * lane, a.c.v_scales + sc, in);
+      };
+      look_up(true);
+#pragma unroll 1
+      for (int i = 0; i < w.cnt && ok; ++i) {
+        int64_t off[kPer];
+        uint32_t there[kPer];
+        bool whole = true;
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) {
+          const bool in = page[q] >= 0 && page[q] < a.c.pages;
+          if (tok + 32 * q < tokens && !in) set_dev_status(a.dev_status, TFD_ERR_DEVICE_DATA);
+          off[q] = in ? (page[q] * a.c.page_stride + ((int)tok + 32 * q - pg[q] * ps) * a.c.token_stride + head) * es
+                      : 0;
+          there[q] = __ballot_sync(0xffffffffu, in);
+          whole = whole && there[q] == 0xffffffffu;
+        }
+        tok += kTile;
+        look_up(i + 1 < w.cnt);
+        int64_t from[kMine / P];  // of the rows whose pieces this lane copies
+#pragma unroll
+        for (int j = 0; j < kMine / P; ++j)
+          from[j] = __shfl_sync(0xffffffffu, off[j * P / 32], (j * P & 31) + lane / L);
+#pragma unroll 1
+        for (int v = 0; v < 2; ++v) {
+          if (round > 0)
+            ok = __all_sync(0xffffffffu, bar_wait(empty(slot), (round - 1) & 1u));
+          if (!ok) break;
+          const uint32_t st = sa(sm) + (uint32_t)slot * M::kSlot;
+          const unsigned char* base = v ? vbase : kbase;
+          if (whole) {
+#pragma unroll
+            for (int j = 0; j < kMine / P; ++j)
+              copy16(st + to[j % (8 / P)] + j / (8 / P) * 1024, base + from[j], true);
+          } else {
+#pragma unroll
+            for (int j = 0; j < kMine / P; ++j)
+              copy16(st + to[j % (8 / P)] + j / (8 / P) * 1024, base + from[j],
+                     (there[j * P / 32] >> ((j * P & 31) + lane / L)) & 1u);
+          }
+          copy_arrive(full(slot));
+          if (++slot == M::kSlots) slot = 0, ++round;
         }
       }
-      copy_commit();
-      look_up(i + 1);
-    };
-    look_up(0);
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) fetch(i);
-
-    // ---- q' in two parts, and what each row sees ----------------------------------------------------
-    {
-      int at_row = -1;
-      float sn[E], cs[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e) sn[e] = cs[e] = 0.0f;
-      for (int i = warp; i < kM; i += kW) {  // a row a warp
-        uint32_t hi[E / 2], lo[E / 2];
-        float fac = 1.0f;
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) hi[e] = lo[e] = 0u;
-        if (i < valid) {
-          const int j = (m0 + i) / a.group, hq = h * a.group + (m0 + i) % a.group;
-          const int row = rq.row0 + j;
-          float x[E];
-          const uint16_t* src = a.q + row * a.ldq + (int64_t)hq * D + E * lane;
-#pragma unroll
-          for (int e = 0; e < E; e += 2) {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(src + e);
-            x[e] = bf16_lo(w);
-            x[e + 1] = bf16_hi(w);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (steps > 0 && tid == 32 * kMmaWarp) {
+    // ---- products: one thread ------------------------------------------------------------------------
+    const uint32_t ds = idesc(kWide, kF8 ? 0 : 1, kF8 ? 0 : 1, false, false);
+    const uint32_t dv = idesc(kWide, kF8 ? 0 : 1, 1, true, true);
+    constexpr int kStep = kF8 ? 32 : 16;  // k of a product: 32 bytes of a row of dims
+    const uint32_t ring = sa(sm), qa = sa(sm + M::kQ), pa = sa(sm + M::kP);
+    int64_t gq = 0, gp = 0;      // tiles whose scores, whose values have been issued
+    int left = 0, pieces = 0;    // tiles of the piece that are to be scored, pieces begun
+    int idle = 0;
+    uint32_t firsts = 0u, lasts = 0u;  // of the tiles in flight (bit: tile mod 32)
+    int begun = 0;               // pieces whose values have begun
+    uint64_t since = 0;
+    while (gp < steps) {
+      bool moved = false;
+      if (gq < steps && gq < gp + 2) {
+        if (left == 0) {
+          left = -get_piece(pieces, true).cnt;  // its q' is waited for
+          if (left == 0) {
+            ok = false;
+            break;
           }
-          const uint32_t rows_there = rq.n == 32 ? 0xffffffffu : (1u << rq.n) - 1u;
-          const uint32_t word = a.tree ? (uint32_t)a.tree[row] & rows_there : 0u;
-          const int depth = rq.len + (a.tree ? __popc(word) - 1 : j);
-          if (a.qk & TFD_QK_NORM) norm_rows<D>(x, a.gamma, a.eps);
-          if (a.qk & TFD_QK_ROPE) {
-            if (j != at_row) {
-              int p = a.pos ? a.pos[row] : depth;
-              if (p < 0) {
-                if (a.pos && lane == 0) set_dev_status(a.dev_status, TFD_ERR_DEVICE_DATA);
-                p = 0;
-              }
-              rope_sincos<D>(p, a.turns, sn, cs);
-              at_row = j;
-            }
-            rotate<D>(x, sn, cs);
-          }
-#pragma unroll
-          for (int e = 0; e < E; ++e) x[e] *= a.scale;
-          if (kF8) {  // into f16's range: the largest magnitude in [1, 2)
-            float top = 0.0f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(x[e]));
-            top = warp_max(top);
-            if (top > 0.0f && finite_(top)) {
-              int ex = (int)((__float_as_uint(top) >> 23) & 0xffu) - 127;
-              ex = max(-126, min(126, ex));
-              const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
-              fac = __uint_as_float((uint32_t)(127 + ex) << 23);
-#pragma unroll
-              for (int e = 0; e < E; ++e) x[e] *= inv;
-            }
-          }
-#pragma unroll
-          for (int e = 0; e < E; e += 2) {
-            float rest[2];
-            hi[e / 2] = kF8 ? f16x2(x[e], x[e + 1]) : bf16x2(x[e], x[e + 1]);
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              const uint32_t w = b ? hi[e / 2] >> 16 : hi[e / 2] & 0xffffu;
-              const float back = kF8 ? __half2float(__ushort_as_half((uint16_t)w))
-                                     : __uint_as_float(w << 16);
-              rest[b] = finite_(back) ? x[e + b] - back : 0.0f;
-            }
-            lo[e / 2] = kF8 ? f16x2(rest[0], rest[1]) : bf16x2(rest[0], rest[1]);
-          }
-          if (lane == 0) {
-            // the new tokens that the row sees, and its first cached one
-            uint32_t sees = 0u;
-            const int64_t from = a.window >= 0 ? (int64_t)depth - a.window : -1;
-            for (int jj = 0; jj < rq.n; ++jj) {
-              const int dj =
-                  rq.len + (a.tree ? __popc((uint32_t)a.tree[rq.row0 + jj] & rows_there) - 1 : jj);
-              const bool on = (a.tree ? (word >> jj) & 1u : jj <= j) && dj >= from;
-              sees |= (uint32_t)on << jj;
-            }
-            s_new[i] = sees;
-            s_lo[i] = from > 0 ? (int)min(from, (int64_t)rq.len) : 0;
-          }
-        } else if (lane == 0) {
-          s_new[i] = 0u;
-          s_lo[i] = rq.len;
+          ++pieces;
         }
-        if (lane == 0) s_fac[i] = fac;
-        // element d of a row stands at its place in the k order of the products: as it is for bf16; for
-        // E4M3, whose lanes hold 4 codes in a row, 4t + {0, 1} at 2t + {0, 1} and 4t + {2, 3} at 8 + 2t + {0, 1}
+        if (left < 0 && bar_test_now(q_full, (uint32_t)(pieces - 1) & 1u)) {
+          left = -left;
+          firsts |= 1u << (gq & 31);
+        }
+        const int b = (int)(gq & 1);
+        const int64_t x = 2 * gq;
+        const int s = (int)(x % M::kSlots);
+        if (left > 0 && (gq < 2 || bar_test_now(s_empty(b), (uint32_t)((gq >> 1) - 1) & 1u)) &&
+            bar_test_now(full(s), (uint32_t)(x / M::kSlots) & 1u)) {
+          fence_async();
+          fence_after();
+#pragma unroll
+          for (int k = 0; k < D / kStep; ++k)
+            mma<kF8>(tmem + b * kWide,
+                     sdesc(ring + s * M::kSlot + (k >> 2) * (kTile * 128) + (k & 3) * 32, 16, 1024, 2),
+                     sdesc(qa + (k >> 2) * (kWide * 128) + (k & 3) * 32, 16, 1024, 2), ds, k != 0);
+          if (!TFD_TEST_STALL_EXCHANGE) mma_commit(s_full(b));
+          mma_commit(empty(s));
+          if (--left == 0) lasts |= 1u << (gq & 31);
+          ++gq;
+          moved = true;
+        }
+      }
+      if (gp < gq) {
+        const int64_t x = 2 * gp + 1;
+        const int s = (int)(x % M::kSlots);
+        const uint32_t bit = 1u << (gp & 31);
+        if (bar_test_now(p_full, (uint32_t)gp & 1u) &&
+            bar_test_now(full(s), (uint32_t)(x / M::kSlots) & 1u) &&
+            (!(firsts & bit) || begun == 0 || bar_test_now(o_empty, (uint32_t)(begun - 1) & 1u))) {
+          fence_async();
+          fence_after();
+          // values: 64 dims (E4M3: 128) a row of 128 bytes; heads of 64 leave the other 64 rows to themselves
+#pragma unroll
+          for (int k = 0; k < kTile / kStep; ++k)
+            mma<kF8>(tmem + kO,
+                     sdesc(ring + s * M::kSlot + k * kStep * 128, D == 64 || kF8 ? 0 : kTile * 128, 1024, 2),
+                     sdesc(pa + k * kStep * 16, 128, kTile * 16, 0), dv, !(firsts & bit) || k != 0);
+          mma_commit(empty(s));
+          mma_commit(p_empty);
+          if (lasts & bit) mma_commit(o_full);
+          if (firsts & bit) ++begun;
+          firsts &= ~bit;
+          lasts &= ~bit;
+          ++gp;
+          moved = true;
+        }
+      }
+      idle = moved ? 0 : idle + 1;
+      if (idle == 0) since = 0;
+      else if (idle % 256 == 0) {
+        const uint64_t t = now();
+        if (since == 0) since = t;
+        else if (t - since > 1000000000ull) {
+          ok = false;
+          break;
+        }
+      }
+    }
+    if (!ok) {  // no product may still read or write when this block's memory is given back
+      mma_commit(drained);
+      bar_wait(drained, 0);
+    }
+  } else if (steps > 0 && warp < kMmaWarp) {
+    // ---- softmax of 16 rows: a thread a token; then their sums, a thread a dim -----------------------
+    const int grp = warp / 4, bid = 1 + grp, n0 = grp * kCols, gw = warp & 3, gt = tid & (kGroup - 1);
+    float* s_ref = reinterpret_cast<float*>(sm + M::kRef) + n0;
+    float* s_fac = reinterpret_cast<float*>(sm + M::kFac) + n0;
+    float* s_red = reinterpret_cast<float*>(sm + M::kRed) + 4 * n0;
+    // what the unit's rows of piece p see: the first cached token, the new ones
+    auto rows_of = [&](int p) { return reinterpret_cast<int2*>(sm + M::kRows) + (p & 1) * N; };
+    auto sees = [&](const int2& row, int key, int len) {
+      const int j = key - len;
+      return j < 0 ? key >= row.x : j < 32 && (((uint32_t)row.y >> (j & 31)) & 1u);
+    };
+    // from where all the unit's rows see the cached tokens, and the new ones that they all see
+    int2 every = make_int2(0, 0), every_next = every;
+    const uint32_t lanes = (uint32_t)(32 * gw) << 16;
+
+    // q' of a piece in two parts, and what each of its rows sees; the rows' q is loaded before. Four rows
+    // a warp at once, 8 lanes a row: a lane holds the first and second elements of D / 16 pairs.
+    constexpr int E = D / 16;
+    uint32_t raw[E], gam[E], raw_word = 0u;
+    int raw_pos = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      gam[e] = a.gamma && (a.qk & TFD_QK_NORM)
+                   ? (uint32_t)a.gamma[(2 * e / E) * (D / 2) + E * (lane & 7) + 2 * e % E] |
+                         (uint32_t)a.gamma[(2 * e / E) * (D / 2) + E * (lane & 7) + 2 * e % E + 1] << 16
+                   : 0x3F803F80u;
+    auto load_q = [&](const Piece& w) {
+      if (lane < w.n) {
+        if (a.tree) raw_word = (uint32_t)a.tree[w.row0 + lane];
+        if (a.pos && (a.qk & TFD_QK_ROPE)) raw_pos = a.pos[w.row0 + lane];
+      }
+      const int v = w.h0 + min(n0 + 4 * gw + lane / 8, w.valid - 1), j = v / a.group;
+      const uint16_t* src = a.q + (w.row0 + w.j0 + j) * a.ldq + (int64_t)(w.h * a.group + v - j * a.group) * D +
+                            E * (lane & 7);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (E == 8) {
+          const uint4 x = *reinterpret_cast<const uint4*>(src + half * (D / 2));
+          raw[half * (E / 2)] = x.x, raw[half * (E / 2) + 1] = x.y;
+          raw[half * (E / 2) + E / 2 - 2] = x.z, raw[half * (E / 2) + E / 2 - 1] = x.w;
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(src + half * (D / 2));
+          raw[half * (E / 2)] = x.x, raw[half * (E / 2) + 1] = x.y;
+        }
+      }
+    };
+    auto prepare = [&](const Piece& w, int p) {
+      int2* s_rows = rows_of(p) + n0;
+      // new row `lane`: its word, depth and position
+      const bool there = lane < w.n;
+      const uint32_t rows_there = w.n == 32 ? 0xffffffffu : (1u << w.n) - 1u;
+      uint32_t words = (2u << lane) - 1u;  // itself and those before
+      if (a.tree && there) words = raw_word;
+      words &= rows_there;
+      const int depths = w.len + (a.tree ? __popc(words) - 1 : lane);
+      int places = there && a.pos && (a.qk & TFD_QK_ROPE) ? raw_pos : depths;
+      if (places < 0) {
+        if (there && a.pos) set_dev_status(a.dev_status, TFD_ERR_DEVICE_DATA);
+        places = 0;
+      }
+      {
+        const bool in = lane >= w.j0 && lane <= w.j0 + (w.h0 + w.valid - 1) / a.group;  // the unit's
+        const int deepest = __reduce_max_sync(0xffffffffu, in ? depths : INT32_MIN);
+        const int64_t from = a.window >= 0 ? (int64_t)deepest - a.window : -1;
+        every_next.x = from > 0 ? (int)min(from, (int64_t)w.len) : 0;
+        every_next.y = (int)(__reduce_and_sync(0xffffffffu, in ? words : 0xffffffffu) &
+                             __ballot_sync(0xffffffffu, depths >= from));
+      }
+      const int i = 4 * gw + lane / 8, n = n0 + i, l = lane & 7;
+      const bool row = n < w.valid;
+      const int j = w.j0 + (w.h0 + min(n, w.valid - 1)) / a.group;
+      float x[2 * E];  // first elements of the pairs, then the second
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        x[2 * e] = row ? bf16_lo(raw[e]) : 0.0f;
+        x[2 * e + 1] = row ? bf16_hi(raw[e]) : 0.0f;
+      }
+      if (a.qk & TFD_QK_NORM) {
+        float ss = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 2 * E; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+        for (int m = 4; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+        const float inv = row ? 1.0f / sqrtf(ss / (float)D + a.eps) : 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          x[2 * e] = x[2 * e] * inv * bf16_lo(gam[e]);
+          x[2 * e + 1] = x[2 * e + 1] * inv * bf16_hi(gam[e]);
+        }
+      }
+      if (a.qk & TFD_QK_ROPE) {
+        const int at = __shfl_sync(0xffffffffu, places, j);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          float sn, cs;
+          rope_pair_fast<D>(at, a.turns, E * l + e, sn, cs);
+          const float first = x[e], second = x[E + e];
+          x[e] = first * cs - second * sn;
+          x[E + e] = first * sn + second * cs;
+        }
+      }
+      // the new tokens that the row sees, and its first cached one
+      const uint32_t word = __shfl_sync(0xffffffffu, words, j);
+      const int64_t from = a.window >= 0 ? (int64_t)__shfl_sync(0xffffffffu, depths, j) - a.window : -1;
+      uint32_t sees = word;
+      if (a.window >= 0) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint32_t deep = __ballot_sync(0xffffffffu, depths >= __shfl_sync(0xffffffffu, from, 8 * r));
+          if (lane / 8 == r) sees &= deep;
+        }
+      }
+      // past the last row: it hides nothing
+      if (l == 0) s_rows[i] = row ? make_int2(from > 0 ? (int)min(from, (int64_t)w.len) : 0, (int)sees) : make_int2(0, -1);
+      if (kF8) {
+        // into E4M3's range, the row's largest magnitude in [128, 256); then part by part what is left
+        float top = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 2 * E; ++e) {
+          x[e] *= a.scale;
+          top = fmaxf(top, fabsf(x[e]));
+        }
+#pragma unroll
+        for (int m = 4; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+        int ex = (int)((__float_as_uint(top) >> 23) & 0xffu) - 127 - 7;
+        ex = finite_(top) ? max(-126, min(120, ex)) : 0;
+        const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+        if (l == 0)
+          reinterpret_cast<float*>(sm + M::kPow)[(p & 1) * N + n] =
+              finite_(top) ? __uint_as_float((uint32_t)(127 + ex) << 23) : NAN;  // infinite: NaN, as the formula gives
+#pragma unroll
+        for (int e = 0; e < 2 * E; ++e) x[e] *= down;
+#pragma unroll
+        for (int part = 0; part < 4; ++part)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t w[E / 4];
+#pragma unroll
+            for (int e = 0; e < E; e += 4) {
+              float* y = x + half * E + e;
+              const uint32_t lo = e4m3x2(y[0], y[1]), hi = e4m3x2(y[2], y[3]);
+              w[e / 4] = lo | hi << 16;
+              const float2 b0 = e4m3_floats(lo), b1 = e4m3_floats(hi);
+              const float up = part == 1 ? 256.0f : 1.0f;
+              y[0] = (y[0] - b0.x) * up, y[1] = (y[1] - b0.y) * up;
+              y[2] = (y[2] - b1.x) * up, y[3] = (y[3] - b1.y) * up;
+            }
+            const int d = half * (D / 2) + E * l, r = part * N + n;
+            unsigned char* to = sm + M::kQ + r * 128 + (((d >> 4) ^ (r & 7)) << 4) + (d & 15);
+            if (E == 8) *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[E / 4 - 1]);
+            else *reinterpret_cast<uint32_t*>(to) = w[0];
+          }
+      } else {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t hi[E / 2], lo[E / 2];
 #pragma unroll
         for (int e = 0; e < E; e += 2) {
-          const int d = E * lane + e, in = d & 15;
-          const int to = kF8 ? (d & ~15) + (in >> 2) * 2 + ((in & 2) ? 8 : 0) : d;
-          const uint32_t at = (uint32_t)M::kQ + piece<2 * D>(i, to >> 3) + (to & 7) * 2;
-          *reinterpret_cast<uint32_t*>(sm + at) = hi[e / 2];
-          *reinterpret_cast<uint32_t*>(sm + at + kM * 2 * D) = lo[e / 2];
+          const float y0 = x[half * E + e] * a.scale, y1 = x[half * E + e + 1] * a.scale;
+          hi[e / 2] = bf16x2(y0, y1);
+          const float b0 = bf16_lo(hi[e / 2]), b1 = bf16_hi(hi[e / 2]);
+          lo[e / 2] = bf16x2(finite_(b0) ? y0 - b0 : 0.0f, finite_(b1) ? y1 - b1 : 0.0f);
+        }
+        const int d = half * (D / 2) + E * l;
+        unsigned char* to = sm + M::kQ + (d >> 6) * (kWide * 128) + n * 128 + ((((d >> 3) & 7) ^ (n & 7)) << 4) +
+                            (d & 7) * 2;
+        if (E == 8) {
+          *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[E / 2 - 2], hi[E / 2 - 1]);
+          *reinterpret_cast<uint4*>(to + N * 128) = make_uint4(lo[0], lo[1], lo[E / 2 - 2], lo[E / 2 - 1]);
+        } else {
+          *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(to + N * 128) = make_uint2(lo[0], lo[1]);
         }
       }
-    }
-    __syncthreads();
-    uint32_t aq[MT == 1 ? D / 16 : 1][2][4];
-    const int a_row = lane & 15, a_piece = lane >> 4;  // ldmatrix: rows and halves of an A tile
-    if (MT == 1) {
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-        for (int part = 0; part < 2; ++part)
-          ldsm4(aq[MT == 1 ? k : 0][part],
-                s_q + part * kM * 2 * D + piece<2 * D>(a_row, 2 * k + a_piece));
-    }
-    float o[MT][D / 8][4], mx[MT][2], sum[MT][2], fac[MT][2];
-    int lo[MT][2];
-    uint32_t fresh[MT][2];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[m][n][e] = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        mx[m][e] = -INFINITY;
-        sum[m][e] = 0.0f;
-        lo[m][e] = s_lo[16 * m + qr + 8 * e];
-        fresh[m][e] = s_new[16 * m + qr + 8 * e];
-        fac[m][e] = kF8 ? s_fac[16 * m + qr + 8 * e] : 1.0f;
       }
-    }
-    int lo_most = 0;  // from here to the last cached token every row sees all
-    for (int i = 0; i < valid; ++i) lo_most = max(lo_most, s_lo[i]);
-
-    // ---- the warp's slices --------------------------------------------------------------------------
-    for (int i = 0; i < cnt; ++i) {
-      copy_wait<kStages - 2>();
-      __syncwarp();  // slice i is here for all lanes, and all are done with slice i - 1
-      fetch(i + kStages - 1);
-      const int key0 = (int)((int64_t)(rq.tile0 + first + i) * S::kTile) + warp * kKeys;
-      if (key0 >= tokens) continue;  // warp-uniform
-      const uint32_t st = s_ring + (uint32_t)(i % kStages) * S::kStage;
-      const unsigned char* stage = ring + (i % kStages) * S::kStage;
-      const uint32_t there = *reinterpret_cast<const uint32_t*>(stage + S::kMask);
-      constexpr uint32_t kAll = kKeys == 32 ? 0xffffffffu : 0xffffu;
-
-      float s[MT][NT][4];
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[m][n][e] = 0.0f;
-      if (kF8) {
-#pragma unroll
-        for (int k = 0; k < D / 16; k += 2) {
-          uint32_t af[2][MT][2][4];
-#pragma unroll
-          for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-              for (int part = 0; part < 2; ++part) {
-                if (MT == 1) {
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) af[kk][m][part][e] = aq[MT == 1 ? k + kk : 0][part][e];
-                } else {
-                  ldsm4(af[kk][m][part], s_q + part * kM * 2 * D +
-                                             piece<2 * D>(16 * m + a_row, 2 * (k + kk) + a_piece));
-                }
-              }
-#pragma unroll
-          for (int n = 0; n < NT; n += 2) {
-            uint32_t b[4];  // keys 8n.. at pieces k, k + 1; keys 8n + 8.. at both
-            ldsm4(b, st + piece<kRow>(8 * n + (lane & 7) + ((lane >> 4) << 3), k + ((lane >> 3) & 1)));
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t b0 = e4m3_f16x2((uint16_t)b[q]), b1 = e4m3_f16x2((uint16_t)(b[q] >> 16));
-#pragma unroll
-              for (int m = 0; m < MT; ++m) {
-                mma<true>(s[m][n + (q >> 1)], af[q & 1][m][0], b0, b1);
-                mma<true>(s[m][n + (q >> 1)], af[q & 1][m][1], b0, b1);
-              }
-            }
-          }
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          uint32_t af[MT][2][4];
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int part = 0; part < 2; ++part) {
-              if (MT == 1) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) af[m][part][e] = aq[MT == 1 ? k : 0][part][e];
-              } else {
-                ldsm4(af[m][part],
-                      s_q + part * kM * 2 * D + piece<2 * D>(16 * m + a_row, 2 * k + a_piece));
-              }
-            }
-#pragma unroll
-          for (int n = 0; n < NT; n += 2) {
-            uint32_t b[4];
-            ldsm4(b, st + piece<kRow>(8 * n + (lane & 7) + ((lane >> 4) << 3),
-                                      2 * k + ((lane >> 3) & 1)));
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-              for (int part = 0; part < 2; ++part) {
-                mma<false>(s[m][n], af[m][part], b[0], b[1]);
-                mma<false>(s[m][n + 1], af[m][part], b[2], b[3]);
-              }
-          }
-        }
-      }
-      const float* ks = reinterpret_cast<const float*>(stage + S::kScales);
-      if (kF8) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const float2 f = *reinterpret_cast<const float2*>(ks + 8 * n + 2 * qc);
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            s[m][n][0] *= fac[m][0] * f.x;
-            s[m][n][1] *= fac[m][0] * f.y;
-            s[m][n][2] *= fac[m][1] * f.x;
-            s[m][n][3] *= fac[m][1] * f.y;
-          }
-        }
-      }
-      // hidden tokens
-      const bool hidden = there != kAll || key0 + kKeys > rq.len || key0 < lo_most;  // warp-uniform
-      if (hidden) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int c = 8 * n + 2 * qc + (e & 1), key = key0 + c, j = key - rq.len;
-            const bool is = (there >> c) & 1u;
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              const bool on = is && (j < 0 ? key >= lo[m][e >> 1]
-                                           : j < 32 && ((fresh[m][e >> 1] >> (j & 31)) & 1u));
-              if (!on) s[m][n][e] = -INFINITY;
-            }
-          }
-      }
-      // running maximum
-      float base[MT][2];
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float x = fmaxf(s[m][0][2 * e], s[m][0][2 * e + 1]);
-#pragma unroll
-          for (int n = 1; n < NT; ++n) x = fmaxf(x, fmaxf(s[m][n][2 * e], s[m][n][2 * e + 1]));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-          const float was = mx[m][e];
-          x = fmaxf(x, was);
-          mx[m][e] = x;
-          base[m][e] = x == -INFINITY ? 0.0f : x;
-          if (__any_sync(0xffffffffu, x > was)) {
-            const float f = exp2_(was - base[m][e]);
-            sum[m][e] *= f;
-#pragma unroll
-            for (int n = 0; n < D / 8; ++n) {
-              o[m][n][2 * e] *= f;
-              o[m][n][2 * e + 1] *= f;
-            }
-          }
-        }
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s[m][n][e] = exp2_(s[m][n][e] - base[m][e >> 1]);
-            sum[m][e >> 1] += s[m][n][e];
-          }
-      if (kF8) {  // the values' scales go into the weights; a weight of zero stays zero
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const float2 f = *reinterpret_cast<const float2*>(ks + kKeys + 8 * n + 2 * qc);
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              s[m][n][e] = hidden && s[m][n][e] == 0.0f ? 0.0f : s[m][n][e] * (e & 1 ? f.y : f.x);
-        }
-      }
-      bool odd = false;  // values that are not finite, where a row does not see them all
-      if (!kF8 && hidden) {
-#pragma unroll 4
-        for (int j = lane; j < S::kPlane / 16; j += 32) {
-          const uint4 v = *reinterpret_cast<const uint4*>(stage + S::kPlane + 16 * j);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            odd |= (w[e] & 0x7F80u) == 0x7F80u || (w[e] & 0x7F800000u) == 0x7F800000u;
-        }
-        odd = __any_sync(0xffffffffu, odd);
-      }
-      const uint32_t sv = st + S::kPlane;
-      if (kF8 || !odd) {
-#pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k) {
-          uint32_t p[MT][2][4];
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const float x = s[m][2 * k + b][2 * e], y = s[m][2 * k + b][2 * e + 1];
-                const uint32_t w = bf16x2(x, y);
-                p[m][0][2 * b + e] = w;
-                p[m][1][2 * b + e] = bf16x2(x - bf16_lo(w), y - bf16_hi(w));
-              }
-          if (kF8) {
-#pragma unroll
-            for (int n = 0; n < D / 32; ++n) {
-              uint32_t v[4];  // codes of dims 32 n + 2 g, + 1 (then 16 more) of tokens 2t, 2t + 1 (then 8 more)
-              ldsm4t(v, sv + piece<kRow>(16 * k + (lane & 7) + (((lane >> 3) & 1) << 3),
-                                         2 * n + (lane >> 4)));
-#pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                const uint32_t even0 = e4m3_bf16x2(__byte_perm(v[2 * q], 0, 0x2404));
-                const uint32_t even1 = e4m3_bf16x2(__byte_perm(v[2 * q + 1], 0, 0x2404));
-                const uint32_t odd0 = e4m3_bf16x2(__byte_perm(v[2 * q], 0, 0x3414));
-                const uint32_t odd1 = e4m3_bf16x2(__byte_perm(v[2 * q + 1], 0, 0x3414));
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                  for (int part = 0; part < 2; ++part) {
-                    mma<false>(o[m][4 * n + 2 * q], p[m][part], even0, even1);
-                    mma<false>(o[m][4 * n + 2 * q + 1], p[m][part], odd0, odd1);
-                  }
-              }
-            }
-          } else {
-#pragma unroll
-            for (int n = 0; n < D / 16; ++n) {
-              uint32_t v[4];
-              ldsm4t(v, sv + piece<kRow>(16 * k + (lane & 7) + (((lane >> 3) & 1) << 3),
-                                         2 * n + (lane >> 4)));
-#pragma unroll
-              for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int part = 0; part < 2; ++part) {
-                  mma<false>(o[m][2 * n], p[m][part], v[0], v[1]);
-                  mma<false>(o[m][2 * n + 1], p[m][part], v[2], v[3]);
-                }
-            }
-          }
-        }
-      } else {
-        for (int c = 0; c < kKeys; ++c) {
-          const int src = (lane & ~3) | ((c & 7) >> 1);
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            float w[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float x = 0.0f;
-#pragma unroll
-              for (int n = 0; n < NT; ++n)
-                if (n == c >> 3) x = c & 1 ? s[m][n][2 * e + 1] : s[m][n][2 * e];
-              w[e] = __shfl_sync(0xffffffffu, x, src);
-            }
-#pragma unroll
-            for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int byte = 2 * (8 * n + 2 * qc + e);
-                const float v = bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(
-                    stage + S::kPlane + piece<kRow>(c, byte >> 4) + (byte & 15)));
-                if (w[0] != 0.0f) o[m][n][e] = fmaf(w[0], v, o[m][n][e]);
-                if (w[1] != 0.0f) o[m][n][2 + e] = fmaf(w[1], v, o[m][n][2 + e]);
-              }
-          }
-        }
-      }
-    }
-
-    // ---- the warps' sums added up -------------------------------------------------------------------
-    copy_wait<0>();
-    __syncthreads();  // the ring is free
-    float* sums = reinterpret_cast<float*>(sm);
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float x = sum[m][e];
-        x += __shfl_xor_sync(0xffffffffu, x, 1);
-        x += __shfl_xor_sync(0xffffffffu, x, 2);
-        const int row = 16 * m + qr + 8 * e;
-        if (qc == 0) s_stat[warp * kM + row] = make_float2(mx[m][e], x);
-        float* to = sums + (warp * kM + row) * M::kPitch;
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-          if (kF8) {
-            const int d = 16 * (n >> 1) + 4 * qc + (n & 1);
-            to[d] = o[m][n][2 * e];
-            to[d + 2] = o[m][n][2 * e + 1];
-          } else {
-            *reinterpret_cast<float2*>(to + 8 * n + 2 * qc) =
-                make_float2(o[m][n][2 * e], o[m][n][2 * e + 1]);
-          }
-        }
-      }
-    __syncthreads();
-    const bool whole = cnt == rq.tiles;
-    const int64_t line0 = rq.base + unit * rq.tiles;     // the unit's first tile on the line
-    const int b0 = (int)(line0 / share), pieces = (int)((line0 + rq.tiles - 1) / share) - b0 + 1;
-    const int slot = 2 * blockIdx.x + (first == 0 ? 1 : 0);
-    auto put_row = [&](int i, int d, const float4& v, float mxi, float l) {
-      const int row = rq.row0 + (m0 + i) / a.group, hq = h * a.group + (m0 + i) % a.group;
-      const float inv = l > 0.0f ? 1.0f / l : l == l ? 0.0f : l;
-      uint2 w;
-      w.x = bf16x2(v.x * inv, v.y * inv);
-      w.y = bf16x2(v.z * inv, v.w * inv);
-      if (l == 0.0f) w = make_uint2(0u, 0u);
-      *reinterpret_cast<uint2*>(a.out + row * a.ldo + (int64_t)hq * D + d) = w;
-      if (a.lse && d == 0)
-        a.lse[(int64_t)row * a.q_heads + hq] =
-            l == 0.0f ? -INFINITY : (mxi + log2f(l)) * 0.6931471805599453f;
+      fence_async();
+      bar_arrive(q_full);
     };
-    for (int i = tid / (D / 4); i < valid; i += kT / (D / 4)) {
-      const int d = tid % (D / 4) * 4;
-      float top = -INFINITY, l = 0.0f;
-      float2 st[kW];
+
+    int64_t g = 0;  // tiles done
+    Piece next = get_piece(0, false);
+    bool have = !group_any(bid, next.cnt == 0);
+    if (have) {
+      load_q(next);
+      prepare(next, 0);
+    }
+    for (int p = 0; have; ++p) {
+      const Piece cur = next;
+      const int tokens = cur.len + cur.n;
+      group_sync(bid);  // the last piece's sums are done with
+      if (gt < kCols) s_ref[gt] = kUnset;
+      group_sync(bid);  // what each row sees, and its reference
+      const int2* s_rows = rows_of(p) + n0;
+      if (tid == 0) ms.odd[(p + 2) & 3] = 0;
+      every = every_next;
+      float sum[kCols];
 #pragma unroll
-      for (int w = 0; w < kW; ++w) {
-        st[w] = s_stat[w * kM + i];
-        top = fmaxf(top, st[w].x);
-      }
-      const float b = top == -INFINITY ? 0.0f : top;
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int n = 0; n < kCols; ++n) sum[n] = 0.0f;
+      int part_tile[4], part_tiles = 0;  // tiles that some rows see in part
+      const int32_t* table = a.table + cur.r * a.ldt;
+      int64_t tok = (int64_t)(cur.tile0 + cur.first) * kTile + gt;
+      int page = tok < tokens ? table[page_of(a, tok)] : -1;  // of this thread's token; -1: none
+      float ks = 0.0f, vs = 1.0f, ks_next = 0.0f, vs_next = 1.0f;  // E4M3: its scales
+      auto load_scales = [&](int64_t tok, int page, float& ks, float& vs) {
+        ks = 0.0f, vs = 1.0f;
+        if (page >= 0 && page < a.c.pages) {
+          const int64_t at = ((int64_t)page * H + cur.h) * ps + ((int)tok - page_of(a, tok) * ps);
+          ks = a.c.k_scales[at];
+          vs = a.c.v_scales[at];
+        }
+      };
+      int page_next = cur.cnt > 1 && tok + kTile < tokens ? table[page_of(a, tok + kTile)] : -1;
+      if (kF8) load_scales(tok, page, ks_next, vs_next);
+      next = get_piece(p + 1, false);
+      if (next.cnt > 0) load_q(next);
+
+#pragma unroll 1
+      for (int i = 0; i < cur.cnt; ++i, ++g) {
+        const int b = (int)(g & 1);
+        const int key0 = (cur.tile0 + cur.first + i) * kTile, key = key0 + gt;
+        const bool there = page >= 0 && page < a.c.pages;
+        tok += kTile;
+        page = page_next;
+        page_next = i + 2 < cur.cnt && tok + kTile < tokens ? table[page_of(a, tok + kTile)] : -1;
+        if (kF8) {
+          ks = ks_next, vs = vs_next;
+          load_scales(tok, page, ks_next, vs_next);
+        }
+        if (ok) ok = bar_wait(s_full(b), (uint32_t)(g >> 1) & 1u);
+        fence_after();
+        const bool partly = key0 < every.x || key0 + kTile > cur.len;  // the same for all groups
+        float s[kCols];
+        {
+          float rest[kCols], more[kF8 ? 2 * kCols : 1];
+          tmem_ld16(tmem + lanes + b * kWide + n0, s);
+          tmem_ld16(tmem + lanes + b * kWide + N + n0, rest);
+          if (kF8) {
+            tmem_ld16(tmem + lanes + b * kWide + 2 * N + n0, more);
+            tmem_ld16(tmem + lanes + b * kWide + 3 * N + n0, more + (kF8 ? kCols : 0));
+          }
+          tmem_ld_wait(s);
+          tmem_ld_wait(rest);
+          if (kF8) tmem_ld_wait(more);
+          fence_before();
+          bar_arrive(s_empty(b));
 #pragma unroll
-      for (int w = 0; w < kW; ++w) {
-        const float f = exp2_(st[w].x - b);
-        const float4 x = *reinterpret_cast<const float4*>(sums + (w * kM + i) * M::kPitch + d);
-        l += f * st[w].y;
-        v.x += f * x.x, v.y += f * x.y, v.z += f * x.z, v.w += f * x.w;
+          for (int n = 0; n < kCols; ++n) {
+            s[n] += rest[n];
+            if (kF8) s[n] = fmaf(more[kF8 ? n : 0] + more[kF8 ? kCols + n : 0], 0.00390625f, s[n]);
+          }
+        }
+        // E4M3: the value's scale is part of its weight, as the score's summand: the weights stay below 2^15,
+        // whatever the scales are (scales below 2^-60 are made up for behind)
+        float lv = 0.0f, lv_fin = 0.0f, small = 1.0f;
+        if (kF8) {
+          lv = log2f(vs);
+          if (vs < 8.673617379884035e-19f) {
+            small = vs * 1.152921504606847e18f;
+            lv = -60.0f;
+          }
+          lv_fin = finite_(lv) ? lv : 0.0f;
+          const float* pow = reinterpret_cast<const float*>(sm + M::kPow) + (p & 1) * N + n0;
+#pragma unroll
+          for (int n = 0; n < kCols; n += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(pow + n);
+            s[n] = fmaf(s[n] * f.x, ks, lv), s[n + 1] = fmaf(s[n + 1] * f.y, ks, lv);
+            s[n + 2] = fmaf(s[n + 2] * f.z, ks, lv), s[n + 3] = fmaf(s[n + 3] * f.w, ks, lv);
+          }
+        }
+        if (partly || !__all_sync(0xffffffffu, there)) {  // -inf where this token is not seen
+#pragma unroll
+          for (int n = 0; n < kCols; ++n)
+            if (!there || !sees(s_rows[n], key, cur.len)) s[n] = -INFINITY;
+        }
+        bool free = g == 0;  // the weights' place
+        auto wait_free = [&]() {
+          if (!free && ok) ok = bar_wait(p_empty, (uint32_t)(g - 1) & 1u);
+          free = true;
+        };
+        float over = -INFINITY;  // by how much a score passes its reference
+#pragma unroll
+        for (int n = 0; n < kCols; n += 4) {
+          const float4 r = *reinterpret_cast<const float4*>(s_ref + n);
+          over = fmaxf(over, fmaxf(fmaxf(s[n] - r.x, s[n + 1] - r.y), fmaxf(s[n + 2] - r.z, s[n + 3] - r.w)));
+        }
+        if (i == 0 || group_any(bid, over > kHead)) {  // every row's reference is its largest score so far
+          float most = 0.0f;
+#pragma unroll
+          for (int n = 0; n < kCols; ++n) {
+            const float x = warp_most(s[n]);
+            if (lane == n) most = x;
+          }
+          if (lane < kCols) s_red[gw * kCols + lane] = most;
+          group_sync(bid);
+          if (gt < kCols) {
+            const float was = s_ref[gt];
+            const float x = fmaxf(fmaxf(fmaxf(s_red[gt], s_red[16 + gt]), fmaxf(s_red[32 + gt], s_red[48 + gt])),
+                                  was);
+            s_fac[gt] = exp2_(was - x);
+            s_ref[gt] = x;
+          }
+          group_sync(bid);
+          if (i > 0) {
+            wait_free();  // all so far is added up
+            fence_after();
+#pragma unroll 1
+            for (int part = 0; part < M::kParts; ++part) {
+              float o[kCols];
+              tmem_ld16(tmem + lanes + kO + part * N + n0, o);
+              tmem_ld_wait(o);
+#pragma unroll
+              for (int n = 0; n < kCols; ++n) o[n] *= s_fac[n];
+              tmem_st16(tmem + lanes + kO + part * N + n0, o);
+            }
+            fence_before();
+#pragma unroll
+            for (int n = 0; n < kCols; ++n) sum[n] *= s_fac[n];
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < kCols; n += 4) {
+          const float4 r = *reinterpret_cast<const float4*>(s_ref + n);
+          s[n] -= r.x, s[n + 1] -= r.y, s[n + 2] -= r.z, s[n + 3] -= r.w;
+        }
+#pragma unroll
+        for (int n = 0; n < kCols; ++n) {
+          if (kF8) {
+            sum[n] += exp2_(s[n] - lv_fin);
+            s[n] = exp2_(s[n] + 7.0f) * small;
+          } else {
+            s[n] = exp2_(s[n]);
+            sum[n] += s[n];
+          }
+        }
+        wait_free();
+        if (kF8) {
+          // f16 weights (2^-11) by bits: an E5M2 number is the upper half of an f16 one, and 3 of its 11
+          // bits; what is left is exact, and four parts hold it all
+          uint32_t w[kCols / 2];
+#pragma unroll
+          for (int n = 0; n < kCols; n += 2) w[n / 2] = f16x2(s[n], s[n + 1]);
+#pragma unroll
+          for (int part = 0; part < 4; ++part) {
+            uint32_t c[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) c[n] = __byte_perm(w[2 * n], w[2 * n + 1], 0x7531);
+            *reinterpret_cast<uint4*>(sm + M::kP + ((part * N + n0) >> 4) * (kTile * 16) + gt * 16) =
+                make_uint4(c[0], c[1], c[2], c[3]);
+            if (part < 3) {
+#pragma unroll
+              for (int n = 0; n < kCols / 2; ++n) {
+                w[n] = sub16x2(w[n], w[n] & 0xFF00FF00u);
+                if (part == 1) w[n] = mul16x2(w[n], 0x5C005C00u);  // 256
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int n = 0; n < kCols; n += 8) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float x = s[n + 2 * e], y = s[n + 2 * e + 1];
+              hi[e] = bf16x2(x, y);
+              lo[e] = bf16x2(x - bf16_lo(hi[e]), y - bf16_hi(hi[e]));
+            }
+            unsigned char* to = sm + M::kP + ((n0 + n) >> 3) * (kTile * 16) + gt * 16;
+            *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(to + 2 * N * kTile) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+        }
+        if (!kF8 && partly) {
+          // a value that is not finite, of a token that not all rows see: 0 times it would be NaN. It
+          // leaves the product, and is added at the end to the rows that see it
+          if (part_tiles < 4) part_tile[part_tiles] = key0;
+          const int64_t x = 2 * g + 1;
+          const int slot = (int)(x % M::kSlots);
+          if (there && !sees(every, key, cur.len)) {
+            if (ok) ok = bar_wait(full(slot), (uint32_t)(x / M::kSlots) & 1u);
+            auto at = [&](int c) {
+              return reinterpret_cast<uint4*>(sm + slot * M::kSlot + (c >> 3) * (kTile * 128) + gt * 128 +
+                                              (((c & 7) ^ (gt & 7)) << 4));
+            };
+            bool odd = false;
+#pragma unroll 8
+            for (int c = 0; c < D / 8; ++c) {
+              const uint4 v = *at(c);
+              const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                odd |= (u[e] & 0x7F80u) == 0x7F80u || (u[e] & 0x7F800000u) == 0x7F800000u;
+            }
+#pragma unroll 1
+            for (int c = 0; odd && c < D / 8; ++c) {
+              uint4 v = *at(c);
+              uint32_t* u = &v.x;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if ((u[e] & 0x7F80u) == 0x7F80u) u[e] &= 0xFFFF0000u;
+                if ((u[e] & 0x7F800000u) == 0x7F800000u) u[e] &= 0xFFFFu;
+              }
+              *at(c) = v;
+            }
+            if (odd) atomicOr(&ms.odd[p & 3], 1 << min(part_tiles, 3));
+          }
+          ++part_tiles;
+        }
+        fence_async();
+        bar_arrive(p_full);
       }
+
+      // ---- the sums; the next piece's scores can begin meanwhile ---------------------------------------
+      const float ref = gt < kCols ? s_ref[gt] : 0.0f;  // of row gt, before the next piece's
+      column_sums(sum);
+      if (!(lane & 1)) s_red[gw * kCols + (lane >> 1)] = sum[0];
+      have = !group_any(bid, !ok || next.cnt == 0);
+      if (have) prepare(next, p + 1);
+      float l = 0.0f;
+      if (gt < kCols) {
+        l = (s_red[gt] + s_red[16 + gt]) + (s_red[32 + gt] + s_red[48 + gt]);
+        s_fac[gt] = l == 0.0f ? 0.0f : 1.0f / l;  // 0: a row that sees nothing
+      }
+      if (ok) ok = bar_wait(o_full, (uint32_t)p & 1u);
+      fence_after();
+      const bool mine = D == 128 || gw < 2;
+      const int d = gt;
+      float o[kCols];
+      {
+        float rest[kCols];
+        tmem_ld16(tmem + lanes + kO + n0, o);
+        tmem_ld16(tmem + lanes + kO + N + n0, rest);
+        tmem_ld_wait(o);
+        tmem_ld_wait(rest);
+#pragma unroll
+        for (int n = 0; n < kCols; ++n) o[n] += rest[n];
+        if (kF8) {
+          tmem_ld16(tmem + lanes + kO + 2 * N + n0, rest);
+          tmem_ld_wait(rest);
+#pragma unroll
+          for (int n = 0; n < kCols; ++n) o[n] = fmaf(rest[n], 0.00390625f, o[n]);
+          tmem_ld16(tmem + lanes + kO + 3 * N + n0, rest);
+          tmem_ld_wait(rest);
+#pragma unroll
+          for (int n = 0; n < kCols; ++n) o[n] = fmaf(rest[n], 0.00390625f, o[n]) * 0.0078125f;  // 2^-7
+        }
+      }
+      if (!kF8 && ms.odd[p & 3]) {
+#pragma unroll 1
+        for (int k = 0; k < min(part_tiles, 4) && mine; ++k) {
+          if (!((ms.odd[p & 3] >> k) & 1)) continue;
+          const int k0 = k == 0 ? part_tile[0] : k == 1 ? part_tile[1] : k == 2 ? part_tile[2] : part_tile[3];
+#pragma unroll 1
+          for (int key = k0; key < min(k0 + kTile, tokens); ++key) {
+            const int pg = page_of(a, key), page = table[pg];
+            if (page < 0 || page >= a.c.pages || sees(every, key, cur.len)) continue;
+            const float v = bf16_bits_to_f32(
+                ((const uint16_t*)a.c.v)[page * a.c.page_stride + (key - pg * ps) * a.c.token_stride +
+                                         cur.h * a.c.head_stride + d]);
+            if (finite_(v)) continue;
+#pragma unroll
+            for (int n = 0; n < kCols; ++n)
+              if (sees(rows_of(p)[n0 + n], key, cur.len)) o[n] += v;
+          }
+        }
+      }
+      fence_before();
+      bar_arrive(o_empty);
+      group_sync(bid);  // s_fac
+      const bool whole = cur.cnt == cur.tiles;
+      const int64_t slot = (int64_t)(2 * blockIdx.x + (cur.first == 0 ? 1 : 0)) * N;
+      auto put_lse = [&](int n, float ref, float l) {
+        const int v = cur.h0 + n, j = v / a.group;
+        if (a.lse)
+          a.lse[(int64_t)(cur.row0 + cur.j0 + j) * a.q_heads + cur.h * a.group + v - j * a.group] =
+              l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
+      };
       if (whole) {
-        put_row(i, d, v, top, l);
+        if (mine) {
+          int j = (cur.h0 + n0) / a.group, hq = cur.h0 + n0 - j * a.group;
+          uint16_t* to = a.out + (cur.row0 + cur.j0 + j) * a.ldo + (int64_t)(cur.h * a.group + hq) * D + d;
+#pragma unroll
+          for (int n = 0; n < kCols; ++n) {
+            if (n0 + n < cur.valid) {
+              const float inv = s_fac[n];
+              *to = f32_to_bf16_bits(inv == 0.0f ? 0.0f : o[n] * inv);
+              to += D;
+              if (++hq == a.group) hq = 0, to += a.ldo - (int64_t)a.group * D;
+            }
+          }
+        }
+        if (gt < kCols && n0 + gt < cur.valid) put_lse(n0 + gt, ref, l);
       } else {
-        __stcg(reinterpret_cast<float4*>(a.acc + ((int64_t)slot * kM + i) * D + d), v);
-        if (d == 0) __stcg(a.ml + (int64_t)slot * kM + i, make_float2(top, l));
+        const int b0 = (int)cuts.owner(cur.line0, cur.tiles), pieces = (int)cuts.pieces(cur.line0, cur.tiles);
+#pragma unroll
+        for (int n = 0; n < kCols; ++n)
+          if (n0 + n < cur.valid && mine) __stcg(a.acc + (slot + n0 + n) * D + d, o[n]);
+        if (gt < kCols && n0 + gt < cur.valid) __stcg(a.ml + slot + n0 + gt, make_float2(ref, l));
+        group_sync(bid);
+        if (gt == 0) {
+          __threadfence();
+          int32_t* count = a.count + b0 * R::kGroups + grp;
+          const int was = atomicAdd(count, 1);
+          ms.last[grp] = was == pieces - 1;
+          if (ms.last[grp]) *count = 0;
+        }
+        group_sync(bid);
+        if (ms.last[grp]) {  // all pieces are there: added in their order
+          __threadfence();
+          auto slot_of = [&](int k) { return (int64_t)(k == 0 ? 2 * b0 + 1 : 2 * (b0 + k)) * N + n0; };
+          const int mine_n = min(kCols, cur.valid - n0);
+          // each row's reference and sum: 8 threads a row, a piece in turn
+          const int jn = gt & 15;
+          auto stat = [&](int k) {
+            return k < pieces && jn < mine_n ? __ldcg(a.ml + slot_of(k) + jn) : make_float2(kUnset, 0.0f);
+          };
+          const float2 own = stat(gt / 16);
+          float top = own.x;
+#pragma unroll 1
+          for (int k = gt / 16 + 8; k < pieces; k += 8) top = fmaxf(top, stat(k).x);
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          if (lane < 16) s_red[gw * 16 + jn] = top;
+          group_sync(bid);
+          top = fmaxf(fmaxf(s_red[jn], s_red[16 + jn]), fmaxf(s_red[32 + jn], s_red[48 + jn]));
+          float sums = exp2_(own.x - top) * own.y;
+#pragma unroll 1
+          for (int k = gt / 16 + 8; k < pieces; k += 8) {
+            const float2 st = stat(k);
+            sums += exp2_(st.x - top) * st.y;
+          }
+          sums += __shfl_xor_sync(0xffffffffu, sums, 16);
+          group_sync(bid);
+          if (lane < 16) s_red[gw * 16 + jn] = sums;
+          group_sync(bid);
+          sums = (s_red[jn] + s_red[16 + jn]) + (s_red[32 + jn] + s_red[48 + jn]);
+          if (gt < kCols) {
+            s_ref[gt] = top;  // the next piece's is set after
+            s_fac[gt] = sums == 0.0f ? 0.0f : 1.0f / sums;
+            if (gt < mine_n) put_lse(n0 + gt, top, sums);
+          }
+          group_sync(bid);
+          // several rows a thread at once, 4 dims of each
+          constexpr int T = D / 4, kRowsAt = kGroup / T, kEach = kCols / kRowsAt;
+          const int d4 = gt % T * 4, r0 = gt / T;
+          float4 v[kEach];
+          float tops[kEach];
+#pragma unroll
+          for (int u = 0; u < kEach; ++u) {
+            v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            tops[u] = s_ref[r0 + u * kRowsAt];
+          }
+#pragma unroll 1
+          for (int k = 0; k < pieces; ++k)
+#pragma unroll
+            for (int u = 0; u < kEach; ++u) {
+              const int n = r0 + u * kRowsAt;
+              if (n < mine_n) {
+                const float f = exp2_(__ldcg(a.ml + slot_of(k) + n).x - tops[u]);
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(a.acc + (slot_of(k) + n) * D + d4));
+                v[u].x += f * x.x, v[u].y += f * x.y, v[u].z += f * x.z, v[u].w += f * x.w;
+              }
+            }
+#pragma unroll
+          for (int u = 0; u < kEach; ++u) {
+            const int n = r0 + u * kRowsAt;
+            if (n >= mine_n) continue;
+            const float inv = s_fac[n];
+            const int r = cur.h0 + n0 + n, j = r / a.group;
+            uint2 w = make_uint2(bf16x2(v[u].x * inv, v[u].y * inv), bf16x2(v[u].z * inv, v[u].w * inv));
+            if (inv == 0.0f) w = make_uint2(0u, 0u);
+            *reinterpret_cast<uint2*>(a.out + (cur.row0 + cur.j0 + j) * a.ldo +
+                                      (int64_t)(cur.h * a.group + r - j * a.group) * D + d4) = w;
+          }
+        }
       }
     }
-    if (!whole) {
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const int was = atomicAdd(a.count + b0, 1);
-        s_last = was == pieces - 1;
-        if (s_last) a.count[b0] = 0;
-      }
-      __syncthreads();
-      if (s_last) {  // all pieces are there: added in their order
-        __threadfence();
-        auto slot_of = [&](int p) { return (int64_t)(p == 0 ? 2 * b0 + 1 : 2 * (b0 + p)) * kM; };
-        float* weight = reinterpret_cast<float*>(sm);  // [valid][pieces]
-        for (int i = warp; i < valid; i += kW) {
-          float top = -INFINITY, l = 0.0f;
-          for (int p = lane; p < pieces; p += 32) top = fmaxf(top, __ldcg(a.ml + slot_of(p) + i).x);
-          top = warp_max(top);
-          const float b = top == -INFINITY ? 0.0f : top;
-          for (int p = lane; p < pieces; p += 32) {
-            const float2 st = __ldcg(a.ml + slot_of(p) + i);
-            const float f = exp2_(st.x - b);
-            weight[i * pieces + p] = f;
-            l += f * st.y;
-          }
-          l = warp_sum(l);
-          if (lane == 0) s_stat[i] = make_float2(top, l);
-        }
-        __syncthreads();
-        for (int i = tid / (D / 4); i < valid; i += kT / (D / 4)) {
-          const int d = tid % (D / 4) * 4;
-          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-          for (int p = 0; p < pieces; ++p) {
-            const float f = weight[i * pieces + p];
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(a.acc + (slot_of(p) + i) * D + d));
-            v.x += f * x.x, v.y += f * x.y, v.z += f * x.z, v.w += f * x.w;
-          }
-          const float2 st = s_stat[i];
-          put_row(i, d, v, st.x, st.y);
-        }
-      }
-    }
-    __syncthreads();  // shared memory is free for the next piece
-    t += cnt;
   }
+  if (!ok) set_dev_status(a.dev_status, TFD_ERR_TIMEOUT);
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem)
+                 : "memory");
 }
 
-// Rows of a unit: 16 where no request can have more, else 32.
-inline int unit_rows(int max_new, int group) { return max_new * group <= 16 ? 16 : 32; }
-
-inline size_t workspace(int max_new, int group, int dim) {
-  const size_t rows = (size_t)2 * kMaxBlocks * unit_rows(max_new, group);
-  return kMaxBlocks * 4 + rows * 8 + rows * dim * 4;
+// Rows of a unit: the least of 16, 32 and 64 that the rows of a request fit, or the most there is (E4M3's four parts a
+// row fill tensor memory at 32).
+inline int unit_rows(int max_new, int group, int fmt) {
+  const int rows = max_new * group, most = fmt == TFD_KV_E4M3 ? 32 : 64;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : most;
 }
 
-template <int D, bool kF8, int MT>
+inline size_t workspace(int rows_of_unit, int dim) {
+  const size_t rows = (size_t)2 * kMaxBlocks * rows_of_unit;
+  return kMaxBlocks * 16 + rows * 8 + rows * dim * 4;
+}
+
+template <int D, int N, bool kF8>
 tfd_status launch(const Args<D>& a, cudaStream_t stream) {
   int dev = 0;
   const int sms = tfd_host::device_sms(dev);
-  const int blocks = std::min(kMaxBlocks, std::max(1, sms * kPerSm));
-  constexpr int smem = Smem<D, kF8, MT>::kBytes;
-  return tfd_host::launch_clusters<paged_attn_kernel<D, kF8, MT>>(a, dev, blocks, 1, kT, smem, smem,
-                                                                  stream);
+  constexpr int smem = Smem<D, N, kF8>::kBytes;
+  return tfd_host::launch_clusters<paged_attn_kernel<D, N, kF8>>(
+      a, dev, std::min(kMaxBlocks, std::max(1, sms)), 1, Roles<N>::kT, smem, smem, stream);
 }
 
 template <int D>
 tfd_status launch_dim(Args<D>& a, float rope_base, cudaStream_t stream) {
   if (a.qk & TFD_QK_ROPE) a.turns = tfd_host::rope_turns<D>(rope_base);
-  const bool one = unit_rows(a.max_new, a.group) == 16;
+  const int n = unit_rows(a.max_new, a.group, a.c.fmt);
   if (a.c.fmt == TFD_KV_E4M3)
-    return one ? launch<D, true, 1>(a, stream) : launch<D, true, 2>(a, stream);
-  return one ? launch<D, false, 1>(a, stream) : launch<D, false, 2>(a, stream);
+    return n == 16 ? launch<D, 16, true>(a, stream) : launch<D, 32, true>(a, stream);
+  return n == 16   ? launch<D, 16, false>(a, stream)
+         : n == 32 ? launch<D, 32, false>(a, stream)
+                   : launch<D, 64, false>(a, stream);
 }
 
 }  // namespace
@@ -851,7 +1306,7 @@ extern "C" size_t tfd_paged_attn_workspace(int max_new, int q_heads, int heads, 
   if (max_new < 1 || max_new > TFD_MAX_ROWS || heads < 1 || heads > 1024 || q_heads < heads ||
       q_heads % heads || q_heads / heads > 64 || (dim != 64 && dim != 128))
     return 0;
-  return workspace(max_new, q_heads / heads, dim);
+  return workspace(unit_rows(max_new, q_heads / heads, TFD_KV_BF16), dim);
 }
 
 extern "C" tfd_status tfd_paged_attn(const void* q, int64_t ldq, int rows, int q_heads,
@@ -883,7 +1338,7 @@ extern "C" tfd_status tfd_paged_attn(const void* q, int64_t ldq, int rows, int q
       !aligned(lse, 4) || !aligned(dev_status, 4) || !aligned(ws, 16))
     return TFD_ERR_INVALID;
   const int group = q_heads / c.heads;
-  const size_t need = workspace(max_new, group, c.dim);
+  const size_t need = workspace(unit_rows(max_new, group, TFD_KV_BF16), c.dim);
   if (!ws || ws_bytes < need) return TFD_ERR_WORKSPACE;
   const struct {
     const void* p;
@@ -910,16 +1365,20 @@ extern "C" tfd_status tfd_paged_attn(const void* q, int64_t ldq, int rows, int q
   const float sc =
       (float)((scale > 0.0f ? (double)scale : 1.0 / std::sqrt((double)c.dim)) * 1.4426950408889634);
   char* w = (char*)ws;
-  const size_t slots = (size_t)2 * kMaxBlocks * unit_rows(max_new, group);
+  const size_t slots = (size_t)2 * kMaxBlocks * unit_rows(max_new, group, TFD_KV_BF16);
   int32_t* count = (int32_t*)w;
-  float2* ml = (float2*)(w + kMaxBlocks * 4);
-  float* acc = (float*)(w + kMaxBlocks * 4 + slots * 8);
+  float2* ml = (float2*)(w + kMaxBlocks * 16);
+  float* acc = (float*)(w + kMaxBlocks * 16 + slots * 8);
   cudaStream_t s = tfd_host::as_stream(stream);
+  // 2^(31 + b) / page_size rounded up, b the bits of page_size - 1: exact for tokens below 2^31
+  uint32_t shift = 31;
+  while ((1 << (shift - 31)) < c.page_size) ++shift;
+  const uint32_t mul = (uint32_t)((((uint64_t)1 << shift) + c.page_size - 1) / c.page_size);
 #define TFD_ATTN_DIM(D)                                                                          \
   if (c.dim == D) {                                                                              \
     Args<D> a = {(const uint16_t*)q, ldq, table, ldt, lens, row_start, pos, tree,                \
                  (const uint16_t*)q_gamma, (uint16_t*)out, ldo, lse, count, ml, acc, dev_status, \
-                 c, rows, q_heads, group, max_pages, requests, max_new, window, qk, eps, sc, {}}; \
+                 c, rows, q_heads, group, max_pages, requests, max_new, window, qk, eps, sc, mul, shift, {}}; \
     return launch_dim<D>(a, rope_base, s);                                                       \
   }
   TFD_ATTN_DIM(64)

@@ -26,6 +26,24 @@ __device__ __forceinline__ void rope_pair(int p, const RopeTurns<D>& turns, int 
   sincosf(red, &sn, &cs);
 }
 
+// The same by the sine and cosine of half turns, which need no reduction of their own (within 2^-22 of
+// the above).
+template <int D>
+__device__ __forceinline__ void rope_pair_pi(int p, const RopeTurns<D>& turns, int i, float& sn,
+                                             float& cs) {
+  const uint64_t ph = (uint64_t)(uint32_t)p * turns.t[i];
+  sincospif((float)(int32_t)(ph >> 32) * 4.6566128730773926e-10f, &sn, &cs);  // over 2^31
+}
+
+// The same by the hardware's sine and cosine: within 2^-20.5 on [-pi, pi].
+template <int D>
+__device__ __forceinline__ void rope_pair_fast(int p, const RopeTurns<D>& turns, int i, float& sn,
+                                               float& cs) {
+  const float turn_unit = 1.4629180792671596e-9f;  // 2 pi / 2^32
+  const uint64_t ph = (uint64_t)(uint32_t)p * turns.t[i];
+  __sincosf((float)(int32_t)(ph >> 32) * turn_unit, &sn, &cs);
+}
+
 // Lane l of a warp holds elements E l .. E l + E - 1 of a vector of D = 32 E elements.
 // The sines and cosines of this lane's pairs at position p (lane l holds pairs
 // E (l mod 16) .. + E - 1), shared by every head at that position.

@@ -5,9 +5,12 @@ Tolerances of an output, before its bf16 rounding: with each seen token's log-we
 eta_j the output is within sum_j p_j eta_j |v_j - out| (first order, times 1.01). eta_j has
 * (2^-16 + 2^-18) (A_j + max A): q' in two 16-bit parts (2^-8 each), and q', its products and the
   subtraction of the maximum in fp32, as in ``helpers``; A_j = scale sum_e m_e |k_je|;
-* for E4M3 keys 2^-23 A_most: the second f16 part of q' over its largest magnitude is a multiple of 2^-24;
+* for E4M3 keys 2^-23 A_most: q' over a power of two, its largest magnitude in [128, 256), enters as four
+  E4M3 parts, each within 2^-4 of what is left (2^-16 in all) or, where that is less than half a step of the
+  smallest numbers, within 2^-10; the last two stand for 2^-8 of what they are, so within 2^-18 / 2^7;
 * 2^-20: exponentials and their arguments.
-The weights in two bf16 parts add 2^-16 sum_j p_j |v_j|, and their sums, whose fp32 adds may each cut off
+The weights in two bf16 parts add 2^-16 sum_j p_j |v_j| (for E4M3, as f16, 2^-11: half a step is at most 2^-11
+of the value; what is below f16's smallest step counts for less than 2^-30 of the largest weight), and their sums, whose fp32 adds may each cut off
 2^-23, 2^-17 and 2^-23 a 8 tokens. A log-sum is within max_j eta_j, 2^-20, 2^-23 of itself and the
 sum's 2^-24 a token.
 """
@@ -131,7 +134,8 @@ class Case:
             part, f8 = 2.0 ** -16 + 2.0 ** -18, 2.0 ** -23 if self.fmt != "bf16" else 0.0
             tok = length + n
             err = 1.01 * (part * t["dev_a"] + (2.0 ** -20 + f8 * t["a_most"][..., None]) * t["dev"]) + \
-                (2.0 ** -16 + 2.0 ** -17 + 2.0 ** -23 * tok / 8) * t["abs_out"]
+                ((2.0 ** -16 if self.fmt == "bf16" else 2.0 ** -11) + 2.0 ** -17 + 2.0 ** -23 * tok / 8) * \
+                t["abs_out"]
             assert_bf16_rounding(out[a:b, :width].reshape(y.shape), y, err, f"{what} request {r}")
             fin = np.isfinite(ls)
             assert np.array_equal(lse[a:b][~fin], ls[~fin])
