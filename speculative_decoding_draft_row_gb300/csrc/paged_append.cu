@@ -11,7 +11,13 @@ namespace {
 using namespace tfd;
 
 constexpr int kT = 256;
-constexpr int kIter = 4;  // steps of a warp: 8 heads of 128, 16 of 64
+#ifndef KI
+#define KI 2
+#endif
+#ifndef KB
+#define KB 4
+#endif
+constexpr int kIter = KI;  // steps of a warp: 8 heads of 128, 16 of 64
 
 template <int D>
 struct Args {
@@ -56,7 +62,7 @@ __device__ __forceinline__ void put_codes(const float (&x)[8], uint8_t* to, floa
 }
 
 template <int D, bool kF8>
-__global__ void __launch_bounds__(kT) paged_append_kernel(const Args<D> a) {
+__global__ void __launch_bounds__(kT, KB) paged_append_kernel(const Args<D> a) {
   constexpr int L = D / 8, kPer = 32 / L;  // lanes of a vector, vectors of a step
   __shared__ __align__(16) float2 turn[kT / 32][D / 2];
   tfd_host::after_previous();

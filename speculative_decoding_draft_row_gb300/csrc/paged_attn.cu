@@ -25,19 +25,29 @@ constexpr int kTile = 128;                   // tokens of a tile
 constexpr int kCols = 16;                    // rows of a unit that one softmax group takes
 constexpr int kGroup = 128;                  // its threads, one a token; then one a dim
 constexpr int kAhead = 3;                    // pieces found ahead
-constexpr int kKeep = 4;                     // tiles that a unit's end keeps
+constexpr int kKeep = 3;                     // tiles that a unit's end keeps
+// Places on the line that beginning a unit takes, in tiles of its type: its query, its first and last tiles and its
+// sums cost a block about that. The blocks' times even out by it (96 requests: 557 us at 0, 531 at 1, 508 at 3,
+// 479 at 5, 490 at 12; the E4M3 batch 173, 165, 147, 134 and at 8 124).
+template <bool kF8>
+constexpr int kStartOf = kF8 ? 8 : 5;
 constexpr float kUnset = -3.0e38f;           // a reference that no score has set
-// Warps: the softmax groups, the one that issues products, those that fetch, the one that finds pieces.
-template <int N>
+// Warps: the softmax groups, the one that finds the pieces and issues the scores' products, the one that
+// issues the values', those that fetch.
+template <int D, int N, bool kF8>
 struct Roles {
-  static constexpr int kGroups = N / kCols, kSoft = kGroups * kGroup;
-  static constexpr int kFetch = N == 16 ? 128 : 64;  // threads that fetch (more where registers allow)
-  static constexpr int kMmaWarp = kSoft / 32, kWalkWarp = kMmaWarp + 1 + kFetch / 32;
-  static constexpr int kT = 32 * (kWalkWarp + 1);
+  static constexpr int kCtas = N == 16 && (kF8 || D == 64) ? 2 : 1;  // blocks of an SM
+  // At 16 rows two groups take tiles in turn, each with sums and references of its own, added at the end of
+  // a piece; else a group takes 16 of the rows.
+  static constexpr int kTurns = N == 16 && kCtas == 1 ? 2 : 1;
+  static constexpr int kGroups = N / kCols * kTurns, kSoft = kGroups * kGroup;
+  static constexpr int kFetch = 64;  // threads that fetch
+  static constexpr int kScoreWarp = kSoft / 32, kValueWarp = kScoreWarp + 1, kFetchWarp = kValueWarp + 1;
+  static constexpr int kT = 32 * kFetchWarp + kFetch;
   static constexpr int kReaders = kSoft / 32 + 1 + kFetch / 32;  // warps that read a piece
 };
 constexpr int kMostTokens = 0x7fffffff - 1024;  // of a request: a tile behind them is still an int
-constexpr int kMaxBlocks = 152;              // blocks of a launch at most, one an SM
+constexpr int kMaxBlocks = 304;              // blocks of a launch at most
 constexpr float kHead = 8.0f;                // powers of two that a weight may pass its reference by
 
 template <int D>
@@ -61,7 +71,8 @@ struct Args {
   tfd_kv_pages c;
   int rows, q_heads, group, max_pages, requests, max_new, window, qk;
   float eps, scale;  // scale: times log2 e
-  uint32_t page_mul, page_shift;  // token / page_size = token * page_mul >> page_shift
+  uint32_t page_mul, page_shift;  // token / page_size = 2 token * page_mul >> (32 + page_shift)
+  int page_stride, token_stride, head_stride;  // the cache's
   RopeTurns<D> turns;
 };
 
@@ -102,17 +113,6 @@ __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t par) {
       : "memory");
   return ok;
 }
-__device__ __forceinline__ bool bar_test_now(uint32_t bar, uint32_t par) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(par)
-      : "memory");
-  return ok;
-}
 __device__ __forceinline__ uint64_t now() {
   uint64_t t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
@@ -131,17 +131,23 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t par) {
     }
   }
 }
-// A softmax group's own barrier, and the OR of a predicate over it.
-__device__ __forceinline__ void group_sync(int id) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kGroup) : "memory");
+// A barrier of some warps, the OR of a predicate over it, and an arrival that does not wait.
+template <int kThreads>
+__device__ __forceinline__ void warps_sync(int id) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kThreads) : "memory");
 }
-__device__ __forceinline__ bool group_any(int id, bool x) {
+template <int kThreads>
+__device__ __forceinline__ void warps_arrive(int id) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(kThreads) : "memory");
+}
+template <int kThreads>
+__device__ __forceinline__ bool warps_any(int id, bool x) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
       "bar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)x), "r"(id), "n"(kGroup)
+      : "r"((uint32_t)x), "r"(id), "n"(kThreads)
       : "memory");
   return r;
 }
@@ -253,7 +259,7 @@ __device__ __forceinline__ bool finite_(float x) { return fabsf(x) < INFINITY; }
 // A token's place in its request's table.
 template <int D>
 __device__ __forceinline__ int page_of(const Args<D>& a, int64_t token) {
-  return (int)((uint64_t)(uint32_t)token * a.page_mul >> a.page_shift);
+  return (int)(__umulhi(2u * (uint32_t)token, a.page_mul) >> a.page_shift);
 }
 
 // ---- the line ------------------------------------------------------------------------------------
@@ -261,11 +267,12 @@ struct Request {
   int r, row0, n, len;   // its rows and the tokens before them
   int64_t base;          // first tile of its first unit on the line
   int tile0, tiles, mt;  // first tile of its tokens that a row can see, tiles from there, units a head
+  int places;            // of a unit on the line
   bool bad;
 };
 
 // Request r's part of the line.
-template <int D, int N>
+template <int D, int N, bool kF8>
 __device__ __forceinline__ Request request(const Args<D>& a, int r) {
   Request q;
   q.r = r;
@@ -280,6 +287,7 @@ __device__ __forceinline__ Request request(const Args<D>& a, int r) {
   q.tile0 = q.n > 0 && lo > 0 ? (int)(lo / kTile) : 0;
   q.tiles = q.n > 0 ? (q.len + q.n - 1) / kTile + 1 - q.tile0 : 0;
   q.mt = (q.n * a.group + N - 1) / N;
+  q.places = q.tiles + kStartOf<kF8>;
   return q;
 }
 
@@ -289,8 +297,8 @@ struct Piece {
   int r, row0, n, len;    // request; its rows and the tokens before them
   int tile0, tiles;       // the unit's first tile of tokens, its tiles
   int first, cnt;         // of these the piece's: from, number (0: no more pieces)
-  int h, m0, valid;       // head; first of the unit's (row, query head) pairs, pairs there are
-  int j0, h0;             // that pair's row and query head within the group
+  int h, valid;           // head; (row, query head) pairs there are
+  int j0, h0;             // the first pair's row and query head within the group
 };
 
 // A block's odds and ends.
@@ -302,24 +310,26 @@ struct Misc {
   uint32_t tmem;
 };
 
-// Cuts of the line. A cut falls every `share` tiles, but not within `keep` tiles of a unit's ends (there
-// it moves to that end), nor in a unit of fewer than 2 keep: a piece that small costs more, being joined,
-// than it takes off its neighbour. Where a unit of `tiles` that begins at `line0` is cut from, and its pieces:
+// Cuts of the line, on which a unit of `tiles` takes kStart places and one for each tile. A cut falls every
+// `share` places, but not within `keep` tiles of a unit's ends (there it moves to that end), nor in a unit of
+// fewer than 2 keep: a piece that small costs more, being joined, than it takes off its neighbour.
+template <int kStart>
 struct Cuts {
   int64_t share;
   int keep;
-  // the block that has the unit's first tile
+  // the block that has the first tile of the unit that begins at `line0`
   __device__ __forceinline__ int64_t owner(int64_t line0, int tiles) const {
-    return (line0 + min(tiles, keep + (tiles < 2 * keep ? tiles : 0)) - 1) / share;
+    return (line0 + kStart + (tiles < 2 * keep ? tiles : keep) - 1) / share;
   }
   __device__ __forceinline__ int64_t pieces(int64_t line0, int tiles) const {
     if (tiles < 2 * keep) return 1;
-    return (line0 + tiles - keep) / share - owner(line0, tiles) + 1;
+    return (line0 + kStart + tiles - keep) / share - owner(line0, tiles) + 1;
   }
   // where the cut at `t`, which lies in the unit, moves to
   __device__ __forceinline__ int64_t moved(int64_t t, int64_t line0, int tiles) const {
-    if (tiles < 2 * keep || t - line0 < keep) return line0;
-    return t - line0 > tiles - keep ? line0 + tiles : t;
+    const int64_t at = t - line0 - kStart;
+    if (tiles < 2 * keep || at < keep) return line0;
+    return at > tiles - keep ? line0 + kStart + tiles : t;
   }
 };
 
@@ -330,21 +340,26 @@ template <int D, int N, bool kF8>
 struct Smem {
   static constexpr int kParts = kF8 ? 4 : 2;
   static constexpr int kSlot = kF8 ? kTile * 128 : kTile * D * 2;  // E4M3: rows of 128 bytes, whatever D is
-  static constexpr int kSlots = kF8 ? 12 : D == 64 ? 9 : N == 64 ? 5 : 6;  // keys and values of a tile in turn
+  static constexpr int kSlots = Roles<D, N, kF8>::kCtas == 2 ? 5 : kF8 ? 11 : D == 64 ? 9 : N == 64 ? 5 : 6;  // keys, values in turn
   static constexpr int kQ = kSlots * kSlot;                  // q': [row bytes / 128][parts N] rows of 128 bytes
-  static constexpr int kP = kQ + (kF8 ? 512 * N : 4 * N * D);  // weights: [parts N / (16 bytes)][128] x 16 bytes
-  static constexpr int kRows = kP + 4 * N * kTile;           // two of: a row's first cached token seen, new ones seen
+  static constexpr int kQBytes = kF8 ? 512 * N : 4 * N * D;
+  static constexpr int kQs = Roles<D, N, kF8>::kCtas == 2 ? 2 : 1;                // of them: the next piece's is made ahead where it fits
+  static constexpr int kP = kQ + kQs * kQBytes;              // weights: [parts N / (16 bytes)][128] x 16 bytes
+  static constexpr int kTurns = Roles<D, N, kF8>::kTurns, kPlace = 4 * N * kTile;  // a place for weights a turn
+  static constexpr int kRows = kP + kTurns * kPlace;         // two of: a row's first cached token seen, new ones seen
   static constexpr int kRef = kRows + 2 * N * 8;             // reference of each row
-  static constexpr int kFac = kRef + N * 4;
-  static constexpr int kRed = kFac + N * 4;                  // [N / 16][4][16]
-  static constexpr int kPow = kRed + N * 16;                 // E4M3: two of: the power of two of q' of each row
+  static constexpr int kFac = kRef + kTurns * N * 4;
+  static constexpr int kRed = kFac + kTurns * N * 4;         // [groups][4][16]
+  static constexpr int kPow = kRed + kTurns * N * 16;                 // E4M3: two of: the power of two of q' of each row
   static constexpr int kBars = kPow + (kF8 ? 2 * N * 4 : 0);
-  static constexpr int kMisc = (kBars + 8 * (2 * kSlots + 10 + 2 * kAhead) + 15) / 16 * 16;
+  static constexpr int kMisc = (kBars + 8 * (2 * kSlots + 13 + 2 * kAhead) + 15) / 16 * 16;
   static constexpr int kBytes = kMisc + (int)sizeof(Misc);
-  static_assert(kBytes <= 227 * 1024, "shared memory of a block");
+  static_assert(kBytes <= (Roles<D, N, kF8>::kCtas == 2 ? 113 : 227) * 1024, "shared memory of a block");
   static constexpr uint32_t kWide = kParts * N;              // columns of a product
-  static constexpr uint32_t kTmem = kWide <= 32 ? 128 : kWide <= 64 ? 256 : 512;
-  static constexpr uint32_t kO = 2 * kWide;                  // scores twice, then the weighted values
+  static constexpr uint32_t kO = 2 * kWide;                  // scores twice, then the weighted values a turn
+  static constexpr uint32_t kUsed = kO + kTurns * kWide;
+  static constexpr uint32_t kTmem = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+  static_assert(kUsed <= 512, "tensor memory");
 };
 
 // Sums of 16 columns over a warp: lanes 2 i and 2 i + 1 end with column i's in v[0].
@@ -364,11 +379,11 @@ __device__ __forceinline__ void column_sums(float (&v)[kCols]) {
 }
 
 template <int D, int N, bool kF8>
-__global__ void __launch_bounds__(Roles<N>::kT, 1)
+__global__ void __launch_bounds__(Roles<D, N, kF8>::kT, Roles<D, N, kF8>::kCtas)
 paged_attn_kernel(const __grid_constant__ Args<D> a) {
   using M = Smem<D, N, kF8>;
-  using R = Roles<N>;
-  constexpr int kFetch = R::kFetch, kT = R::kT, kMmaWarp = R::kMmaWarp, kWalkWarp = R::kWalkWarp;
+  using R = Roles<D, N, kF8>;
+  constexpr int kFetch = R::kFetch, kT = R::kT, kScoreWarp = R::kScoreWarp;
   extern __shared__ __align__(1024) unsigned char sm[];  // all of the block's: it begins on a swizzle's period
   Misc& ms = *reinterpret_cast<Misc*>(sm + M::kMisc);
   int64_t* scan = reinterpret_cast<int64_t*>(sm + M::kP);  // before there are weights
@@ -383,10 +398,13 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
   const uint32_t more = bars + 16u * M::kSlots;
   auto s_full = [&](int b) { return more + 8u * b; };
   auto s_empty = [&](int b) { return more + 16u + 8u * b; };
-  const uint32_t p_full = more + 32u, p_empty = more + 40u, q_full = more + 48u, o_full = more + 56u,
-                 o_empty = more + 64u, drained = more + 72u;
-  auto w_full = [&](int e) { return more + 80u + 8u * e; };
-  auto w_empty = [&](int e) { return more + 80u + 8u * (kAhead + e); };
+  auto p_full = [&](int t) { return more + 32u + 8u * t; };
+  auto p_empty = [&](int t) { return more + 48u + 8u * t; };
+  const uint32_t q_full = more + 64u, o_full = more + 72u, o_empty = more + 80u, drained = more + 88u;
+  auto w_full = [&](int e) { return more + 104u + 8u * e; };
+  auto w_empty = [&](int e) { return more + 104u + 8u * (kAhead + e); };
+  constexpr int kTurns = R::kTurns;
+  auto round_of = [](int64_t g) { return (uint32_t)(g / kTurns); };  // tile g's, of its turn g mod kTurns
   if (tid == 0) {
     for (int s = 0; s < M::kSlots; ++s) {
       bar_init(full(s), kFetch);
@@ -394,14 +412,15 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
     }
     for (int b = 0; b < 2; ++b) {
       bar_init(s_full(b), 1);
-      bar_init(s_empty(b), R::kSoft);
+      bar_init(s_empty(b), R::kSoft / kTurns);
+      bar_init(p_full(b), R::kSoft / kTurns);
+      bar_init(p_empty(b), 1);
     }
-    bar_init(p_full, R::kSoft);
-    bar_init(p_empty, 1);
-    bar_init(q_full, R::kSoft);
+    bar_init(q_full, R::kSoft / kTurns);
     bar_init(o_full, 1);
     bar_init(o_empty, R::kSoft);
     bar_init(drained, 1);
+    bar_init(drained + 8u, 1);
     for (int e = 0; e < kAhead; ++e) {
       bar_init(w_full(e), 1);
       bar_init(w_empty(e), R::kReaders);
@@ -410,7 +429,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
     for (int i = 0; i < 4; ++i) ms.odd[i] = 0;
   }
   constexpr uint32_t kTmem = M::kTmem, kO = M::kO, kWide = M::kWide;
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sa(&ms.tmem)),
                  "r"(kTmem)
                  : "memory");
@@ -421,15 +440,16 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
 
   // ---- this block's stretch of the line -----------------------------------------------------------
   int64_t total = 0;
-  Cuts cuts;
+  constexpr int kStart = kStartOf<kF8>;
+  Cuts<kStart> cuts;
   {
     const int per = (a.requests + kT - 1) / kT;
     const int r0 = min(a.requests, tid * per), r1 = min(a.requests, r0 + per);
     int64_t mine = 0;
     for (int r = r0; r < r1; ++r) {
-      const Request q = request<D, N>(a, r);
+      const Request q = request<D, N, kF8>(a, r);
       if (q.bad && blockIdx.x == 0) set_dev_status(a.dev_status, TFD_ERR_DEVICE_DATA);
-      mine += (int64_t)q.tiles * q.mt * H;
+      mine += (int64_t)q.places * q.mt * H;
     }
     int64_t x = mine;
 #pragma unroll
@@ -456,14 +476,14 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
     for (int r = r0; r < r1; ++r) {  // for the threads in whose requests a cut falls
       const int64_t lo = blockIdx.x * cuts.share, hi = lo + cuts.share;
       if (!((before <= lo && lo < before + mine) || (before <= hi && hi < before + mine))) break;
-      Request q = request<D, N>(a, r);
-      const int64_t u = (int64_t)q.tiles * q.mt * H;
+      Request q = request<D, N, kF8>(a, r);
+      const int64_t u = (int64_t)q.places * q.mt * H;
       q.base = at;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int64_t t = e ? hi : lo;
         if (at <= t && t < at + u) {
-          ms.ends[e] = cuts.moved(t, at + (t - at) / q.tiles * q.tiles, q.tiles);
+          ms.ends[e] = cuts.moved(t, at + (t - at) / q.places * q.places, q.tiles);
           if (e == 0) ms.first = q;
         }
       }
@@ -473,7 +493,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
   }
   const uint32_t tmem = ms.tmem;
   const int64_t t0 = ms.ends[0], t_end = ms.ends[1];
-  const int64_t steps = t_end - t0;  // tiles of the stretch
+  const int64_t steps = t_end - t0;  // places of the stretch, some of them tiles
   bool ok = true;                   // none of this thread's waits has run out
 
   // Piece k of the stretch, from the warp that finds them: a copy. All lanes of a warp call it.
@@ -488,44 +508,11 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
     return p;
   };
 
-  if (steps > 0 && tid == 32 * kWalkWarp) {
-    // ---- the pieces, one after the other -------------------------------------------------------------
-    Request rq = ms.first;
-    int64_t t = t0;
-    for (int k = 0;; ++k) {
-      Piece p;
-      p.cnt = 0;
-      while (t < t_end && t >= rq.base + (int64_t)rq.tiles * rq.mt * H) {
-        const int64_t next = rq.base + (int64_t)rq.tiles * rq.mt * H;
-        if (rq.r + 1 >= a.requests) t = t_end;  // lengths that changed meanwhile
-        else rq = request<D, N>(a, rq.r + 1);
-        rq.base = next;
-      }
-      if (t < t_end) {
-        const int64_t unit = (t - rq.base) / rq.tiles;
-        p.line0 = rq.base + unit * rq.tiles;
-        p.r = rq.r, p.row0 = rq.row0, p.n = rq.n, p.len = rq.len, p.tile0 = rq.tile0, p.tiles = rq.tiles;
-        p.first = (int)(t - p.line0);
-        p.h = (int)(unit / rq.mt);
-        p.m0 = (int)(unit - (int64_t)p.h * rq.mt) * N;
-        p.cnt = (int)min((int64_t)(rq.tiles - p.first), t_end - t);
-        p.valid = min(N, rq.n * a.group - p.m0);
-        p.j0 = p.m0 / a.group;
-        p.h0 = p.m0 - p.j0 * a.group;
-        t += p.cnt;
-      }
-      const int e = k % kAhead;
-      if (k >= kAhead) ok = bar_wait(w_empty(e), (uint32_t)(k / kAhead - 1) & 1u);
-      if (!ok) break;
-      ms.piece[e] = p;
-      bar_arrive(w_full(e));
-      if (p.cnt == 0) break;
-    }
-  } else if (steps > 0 && warp > kMmaWarp && warp < kWalkWarp) {
+  if (steps > 0 && warp >= R::kFetchWarp) {
     // ---- fetch: a warp half of each tile, a lane the pages of two tokens ----------------------------
     constexpr int kMine = kTile / (kFetch / 32), kPer = kMine / 32;  // tokens of a warp, of a lane
     constexpr int es = kF8 ? 1 : 2, L = D * es / 16, P = 32 / L;  // lanes of a vector, vectors a step
-    const int mine0 = kMine * (warp - kMmaWarp - 1), c = lane % L;
+    const int mine0 = kMine * (warp - R::kFetchWarp), c = lane % L;
     const unsigned char* kbase = (const unsigned char*)a.c.k + 16 * c;
     const unsigned char* vbase = (const unsigned char*)a.c.v + 16 * c;
     // where this lane's pieces go: rows mine0 + lane / L + j P, whose swizzle repeats after 8 rows
@@ -542,7 +529,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
       if (w.cnt == 0) break;
       const int tokens = w.len + w.n;
       const int32_t* table = a.table + w.r * a.ldt;
-      const int64_t head = w.h * a.c.head_stride;
+      const int64_t head = (int64_t)w.h * a.head_stride;
       int64_t tok = (int64_t)(w.tile0 + w.first) * kTile + mine0 + lane;
       int pg[kPer], page[kPer];
       auto look_up = [&](bool on) {
@@ -562,7 +549,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
         for (int q = 0; q < kPer; ++q) {
           const bool in = page[q] >= 0 && page[q] < a.c.pages;
           if (tok + 32 * q < tokens && !in) set_dev_status(a.dev_status, TFD_ERR_DEVICE_DATA);
-          off[q] = in ? (page[q] * a.c.page_stride + ((int)tok + 32 * q - pg[q] * ps) * a.c.token_stride + head) * es
+          off[q] = in ? ((int64_t)page[q] * a.page_stride + (int64_t)((int)tok + 32 * q - pg[q] * ps) * a.token_stride + head) * es
                       : 0;
           there[q] = __ballot_sync(0xffffffffu, in);
           whole = whole && there[q] == 0xffffffffu;
@@ -596,98 +583,122 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (steps > 0 && tid == 32 * kMmaWarp) {
-    // ---- products: one thread ------------------------------------------------------------------------
-    const uint32_t ds = idesc(kWide, kF8 ? 0 : 1, kF8 ? 0 : 1, false, false);
-    const uint32_t dv = idesc(kWide, kF8 ? 0 : 1, 1, true, true);
+  } else if (steps > 0 && tid == 32 * kScoreWarp) {
+    // ---- the pieces, two ahead, and the scores' products: one thread --------------------------------
+    Request rq = ms.first;
+    int64_t t = t0;
+    int found = 0;
+    bool more_pieces = true;
+    auto find = [&]() {
+      Piece p;
+      p.cnt = 0;
+      while (t < t_end && t >= rq.base + (int64_t)rq.places * rq.mt * H) {
+        const int64_t next = rq.base + (int64_t)rq.places * rq.mt * H;
+        if (rq.r + 1 >= a.requests) t = t_end;  // lengths that changed meanwhile
+        else rq = request<D, N, kF8>(a, rq.r + 1);
+        rq.base = next;
+      }
+      if (t < t_end) {
+        const int64_t unit = (t - rq.base) / rq.places;
+        p.line0 = rq.base + unit * rq.places;
+        p.r = rq.r, p.row0 = rq.row0, p.n = rq.n, p.len = rq.len, p.tile0 = rq.tile0, p.tiles = rq.tiles;
+        const int64_t line1 = p.line0 + kStart;  // of its first tile
+        p.first = (int)max((int64_t)0, t - line1);
+        p.h = (int)(unit / rq.mt);
+        const int m0 = (int)(unit - (int64_t)p.h * rq.mt) * N;
+        p.cnt = (int)(min((int64_t)rq.tiles, t_end - line1) - p.first);
+        p.valid = min(N, rq.n * a.group - m0);
+        p.j0 = m0 / a.group;
+        p.h0 = m0 - p.j0 * a.group;
+        t = line1 + p.first + p.cnt;
+      }
+      const int e = found % kAhead;
+      if (found >= kAhead && ok) ok = bar_wait(w_empty(e), (uint32_t)(found / kAhead - 1) & 1u);
+      if (!ok) return;
+      ms.piece[e] = p;
+      bar_arrive(w_full(e));
+      ++found;
+      more_pieces = p.cnt > 0;
+    };
+    const uint32_t desc = idesc(kWide, kF8 ? 0 : 1, kF8 ? 0 : 1, false, false);
     constexpr int kStep = kF8 ? 32 : 16;  // k of a product: 32 bytes of a row of dims
-    const uint32_t ring = sa(sm), qa = sa(sm + M::kQ), pa = sa(sm + M::kP);
-    int64_t gq = 0, gp = 0;      // tiles whose scores, whose values have been issued
-    int left = 0, pieces = 0;    // tiles of the piece that are to be scored, pieces begun
-    int idle = 0;
-    uint32_t firsts = 0u, lasts = 0u;  // of the tiles in flight (bit: tile mod 32)
-    int begun = 0;               // pieces whose values have begun
-    uint64_t since = 0;
-    while (gp < steps) {
-      bool moved = false;
-      if (gq < steps && gq < gp + 2) {
-        if (left == 0) {
-          left = -get_piece(pieces, true).cnt;  // its q' is waited for
-          if (left == 0) {
-            ok = false;
-            break;
-          }
-          ++pieces;
-        }
-        if (left < 0 && bar_test_now(q_full, (uint32_t)(pieces - 1) & 1u)) {
-          left = -left;
-          firsts |= 1u << (gq & 31);
-        }
-        const int b = (int)(gq & 1);
-        const int64_t x = 2 * gq;
-        const int s = (int)(x % M::kSlots);
-        if (left > 0 && (gq < 2 || bar_test_now(s_empty(b), (uint32_t)((gq >> 1) - 1) & 1u)) &&
-            bar_test_now(full(s), (uint32_t)(x / M::kSlots) & 1u)) {
-          fence_async();
-          fence_after();
+    const uint64_t keys = sdesc(sa(sm), 16, 1024, 2), rows = sdesc(sa(sm + M::kQ), 16, 1024, 2);
+    for (int i = 0; i < kAhead && ok && more_pieces; ++i) find();
+    uint32_t slot = 0, round = 0, g = 0;
+    for (int p = 0; ok; ++p) {
+      const int cnt = ms.piece[p % kAhead].cnt;
+      if (cnt == 0) break;
+      ok = bar_wait(q_full, (uint32_t)p & 1u);
+      const uint64_t q0 = rows + (uint32_t)(p % M::kQs * (M::kQBytes / 16));
+      for (int i = 0; i < cnt && ok; ++i, ++g) {
+        const uint32_t b = g & 1;
+        if (g >= 2) ok = bar_wait(s_empty(b), ((g >> 1) - 1) & 1u);
+        if (ok) ok = bar_wait(full(slot), round & 1u);
+        if (!ok) break;
+        fence_async();
+        fence_after();
+        const uint64_t k0 = keys + slot * (M::kSlot / 16);
 #pragma unroll
-          for (int k = 0; k < D / kStep; ++k)
-            mma<kF8>(tmem + b * kWide,
-                     sdesc(ring + s * M::kSlot + (k >> 2) * (kTile * 128) + (k & 3) * 32, 16, 1024, 2),
-                     sdesc(qa + (k >> 2) * (kWide * 128) + (k & 3) * 32, 16, 1024, 2), ds, k != 0);
-          if (!TFD_TEST_STALL_EXCHANGE) mma_commit(s_full(b));
-          mma_commit(empty(s));
-          if (--left == 0) lasts |= 1u << (gq & 31);
-          ++gq;
-          moved = true;
-        }
-      }
-      if (gp < gq) {
-        const int64_t x = 2 * gp + 1;
-        const int s = (int)(x % M::kSlots);
-        const uint32_t bit = 1u << (gp & 31);
-        if (bar_test_now(p_full, (uint32_t)gp & 1u) &&
-            bar_test_now(full(s), (uint32_t)(x / M::kSlots) & 1u) &&
-            (!(firsts & bit) || begun == 0 || bar_test_now(o_empty, (uint32_t)(begun - 1) & 1u))) {
-          fence_async();
-          fence_after();
-          // values: 64 dims (E4M3: 128) a row of 128 bytes; heads of 64 leave the other 64 rows to themselves
-#pragma unroll
-          for (int k = 0; k < kTile / kStep; ++k)
-            mma<kF8>(tmem + kO,
-                     sdesc(ring + s * M::kSlot + k * kStep * 128, D == 64 || kF8 ? 0 : kTile * 128, 1024, 2),
-                     sdesc(pa + k * kStep * 16, 128, kTile * 16, 0), dv, !(firsts & bit) || k != 0);
-          mma_commit(empty(s));
-          mma_commit(p_empty);
-          if (lasts & bit) mma_commit(o_full);
-          if (firsts & bit) ++begun;
-          firsts &= ~bit;
-          lasts &= ~bit;
-          ++gp;
-          moved = true;
-        }
-      }
-      idle = moved ? 0 : idle + 1;
-      if (idle == 0) since = 0;
-      else if (idle % 256 == 0) {
-        const uint64_t t = now();
-        if (since == 0) since = t;
-        else if (t - since > 1000000000ull) {
-          ok = false;
-          break;
-        }
+        for (int k = 0; k < D / kStep; ++k)
+          mma<kF8>(tmem + b * kWide, k0 + (uint32_t)((k >> 2) * (kTile * 8) + (k & 3) * 2),
+                   q0 + (uint32_t)((k >> 2) * (kWide * 8) + (k & 3) * 2), desc, k != 0);
+        if (!TFD_TEST_STALL_EXCHANGE) mma_commit(s_full(b));
+        mma_commit(empty(slot));
+        slot += 2;
+        if (slot >= M::kSlots) slot -= M::kSlots, ++round;
+        if (i == min(cnt, 2) - 1)
+          while (ok && more_pieces && found < p + 1 + kAhead) find();
       }
     }
     if (!ok) {  // no product may still read or write when this block's memory is given back
       mma_commit(drained);
       bar_wait(drained, 0);
     }
-  } else if (steps > 0 && warp < kMmaWarp) {
+  } else if (steps > 0 && tid == 32 * R::kValueWarp) {
+    // ---- the values' products: one thread ------------------------------------------------------------
+    const uint32_t desc = idesc(kWide, kF8 ? 0 : 1, 1, true, true);
+    constexpr int kStep = kF8 ? 32 : 16;  // tokens of a product
+    // values: 64 dims (E4M3: 128) a row of 128 bytes; heads of 64 leave the other 64 rows to themselves
+    const uint64_t values = sdesc(sa(sm), D == 64 || kF8 ? 0 : kTile * 128, 1024, 2);
+    const uint64_t weights = sdesc(sa(sm + M::kP), 128, kTile * 16, 0);
+    uint32_t slot = 1, round = 0, g = 0;
+    for (int p = 0;; ++p) {
+      const Piece w = get_piece(p, true);
+      if (w.cnt == 0) break;
+      if (p > 0) ok = bar_wait(o_empty, (uint32_t)(p - 1) & 1u);
+      for (int i = 0; i < w.cnt && ok; ++i, ++g) {
+        const uint32_t turn = g % kTurns;
+        ok = bar_wait(p_full(turn), (g / kTurns) & 1u) && bar_wait(full(slot), round & 1u);
+        if (!ok) break;
+        fence_async();
+        fence_after();
+        const uint64_t v0 = values + slot * (M::kSlot / 16), p0 = weights + turn * (M::kPlace / 16);
+#pragma unroll
+        for (int k = 0; k < kTile / kStep; ++k)
+          mma<kF8>(tmem + kO + turn * kWide, v0 + (uint32_t)(k * kStep * 8), p0 + (uint32_t)(k * kStep), desc,
+                   i >= kTurns || k != 0);
+        mma_commit(empty(slot));
+        mma_commit(p_empty(turn));
+        if (i == w.cnt - 1) mma_commit(o_full);
+        slot += 2;
+        if (slot >= M::kSlots) slot -= M::kSlots, ++round;
+      }
+      if (!ok) break;
+    }
+    if (!ok) {
+      mma_commit(drained + 8u);
+      bar_wait(drained + 8u, 0);
+    }
+  } else if (steps > 0 && warp < kScoreWarp) {
     // ---- softmax of 16 rows: a thread a token; then their sums, a thread a dim -----------------------
-    const int grp = warp / 4, bid = 1 + grp, n0 = grp * kCols, gw = warp & 3, gt = tid & (kGroup - 1);
-    float* s_ref = reinterpret_cast<float*>(sm + M::kRef) + n0;
-    float* s_fac = reinterpret_cast<float*>(sm + M::kFac) + n0;
-    float* s_red = reinterpret_cast<float*>(sm + M::kRed) + 4 * n0;
+    const int grp = warp / 4, bid = 1 + grp, gw = warp & 3, gt = tid & (kGroup - 1);
+    const int turn = kTurns == 1 ? 0 : grp, n0 = kTurns == 1 ? grp * kCols : 0;
+    constexpr int kBoth = kTurns * kGroup, kBothId = 8, kSumId = 9;  // barriers of groups that share rows
+    float* s_ref = reinterpret_cast<float*>(sm + M::kRef) + grp * kCols;
+    float* s_fac = reinterpret_cast<float*>(sm + M::kFac) + grp * kCols;
+    float* s_red = reinterpret_cast<float*>(sm + M::kRed) + 4 * grp * kCols;
+    unsigned char* s_p = sm + M::kP + turn * M::kPlace;
+    const uint32_t o_at = kO + turn * kWide, lanes = (uint32_t)(32 * gw) << 16;
     // what the unit's rows of piece p see: the first cached token, the new ones
     auto rows_of = [&](int p) { return reinterpret_cast<int2*>(sm + M::kRows) + (p & 1) * N; };
     auto sees = [&](const int2& row, int key, int len) {
@@ -696,7 +707,6 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
     };
     // from where all the unit's rows see the cached tokens, and the new ones that they all see
     int2 every = make_int2(0, 0), every_next = every;
-    const uint32_t lanes = (uint32_t)(32 * gw) << 16;
 
     // q' of a piece in two parts, and what each of its rows sees; the rows' q is loaded before. Four rows
     // a warp at once, 8 lanes a row: a lane holds the first and second elements of D / 16 pairs.
@@ -714,6 +724,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
         if (a.tree) raw_word = (uint32_t)a.tree[w.row0 + lane];
         if (a.pos && (a.qk & TFD_QK_ROPE)) raw_pos = a.pos[w.row0 + lane];
       }
+      if (turn > 0) return;  // the first group makes q' for both
       const int v = w.h0 + min(n0 + 4 * gw + lane / 8, w.valid - 1), j = v / a.group;
       const uint16_t* src = a.q + (w.row0 + w.j0 + j) * a.ldq + (int64_t)(w.h * a.group + v - j * a.group) * D +
                             E * (lane & 7);
@@ -751,6 +762,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
         every_next.y = (int)(__reduce_and_sync(0xffffffffu, in ? words : 0xffffffffu) &
                              __ballot_sync(0xffffffffu, depths >= from));
       }
+      if (turn > 0) return;
       const int i = 4 * gw + lane / 8, n = n0 + i, l = lane & 7;
       const bool row = n < w.valid;
       const int j = w.j0 + (w.h0 + min(n, w.valid - 1)) / a.group;
@@ -831,7 +843,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
               y[2] = (y[2] - b1.x) * up, y[3] = (y[3] - b1.y) * up;
             }
             const int d = half * (D / 2) + E * l, r = part * N + n;
-            unsigned char* to = sm + M::kQ + r * 128 + (((d >> 4) ^ (r & 7)) << 4) + (d & 15);
+            unsigned char* to = sm + M::kQ + p % M::kQs * M::kQBytes + r * 128 + (((d >> 4) ^ (r & 7)) << 4) + (d & 15);
             if (E == 8) *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[E / 4 - 1]);
             else *reinterpret_cast<uint32_t*>(to) = w[0];
           }
@@ -847,7 +859,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
           lo[e / 2] = bf16x2(finite_(b0) ? y0 - b0 : 0.0f, finite_(b1) ? y1 - b1 : 0.0f);
         }
         const int d = half * (D / 2) + E * l;
-        unsigned char* to = sm + M::kQ + (d >> 6) * (kWide * 128) + n * 128 + ((((d >> 3) & 7) ^ (n & 7)) << 4) +
+        unsigned char* to = sm + M::kQ + p % M::kQs * M::kQBytes + (d >> 6) * (kWide * 128) + n * 128 + ((((d >> 3) & 7) ^ (n & 7)) << 4) +
                             (d & 7) * 2;
         if (E == 8) {
           *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[E / 2 - 2], hi[E / 2 - 1]);
@@ -862,9 +874,13 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
       bar_arrive(q_full);
     };
 
-    int64_t g = 0;  // tiles done
+    int64_t g0 = 0;  // tiles before the piece's
     Piece next = get_piece(0, false);
-    bool have = !group_any(bid, next.cnt == 0);
+    // decided by all that share rows: they wait for each other
+    auto any = [&](bool x) {
+      return kTurns == 1 ? warps_any<kGroup>(bid, x) : warps_any<kBoth>(kBothId, x);
+    };
+    bool have = !any(next.cnt == 0);
     if (have) {
       load_q(next);
       prepare(next, 0);
@@ -872,41 +888,45 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
     for (int p = 0; have; ++p) {
       const Piece cur = next;
       const int tokens = cur.len + cur.n;
-      group_sync(bid);  // the last piece's sums are done with
+      warps_sync<kGroup>(bid);  // the last piece's sums are done with
       if (gt < kCols) s_ref[gt] = kUnset;
-      group_sync(bid);  // what each row sees, and its reference
+      warps_sync<kGroup>(bid);  // what each row sees, and its reference
       const int2* s_rows = rows_of(p) + n0;
       if (tid == 0) ms.odd[(p + 2) & 3] = 0;
+      if (kTurns > 1 && turn > 0 && p > 0) warps_sync<kBoth>(kSumId);  // its last sums have been fetched
       every = every_next;
       float sum[kCols];
 #pragma unroll
       for (int n = 0; n < kCols; ++n) sum[n] = 0.0f;
-      int part_tile[4], part_tiles = 0;  // tiles that some rows see in part
       const int32_t* table = a.table + cur.r * a.ldt;
-      int64_t tok = (int64_t)(cur.tile0 + cur.first) * kTile + gt;
-      int page = tok < tokens ? table[page_of(a, tok)] : -1;  // of this thread's token; -1: none
+      const int i0 = kTurns == 1 ? 0 : (int)((turn + g0) & 1);  // this group's first tile of the piece
+      int64_t tok = (int64_t)(cur.tile0 + cur.first + i0) * kTile + gt;
+      auto page_at = [&](int64_t tok, int i) {  // of this thread's token; -1: none
+        return i < cur.cnt && tok < tokens ? table[page_of(a, tok)] : -1;
+      };
+      int page = page_at(tok, i0), page_next = page_at(tok + kTurns * kTile, i0 + kTurns);
       float ks = 0.0f, vs = 1.0f, ks_next = 0.0f, vs_next = 1.0f;  // E4M3: its scales
       auto load_scales = [&](int64_t tok, int page, float& ks, float& vs) {
         ks = 0.0f, vs = 1.0f;
         if (page >= 0 && page < a.c.pages) {
-          const int64_t at = ((int64_t)page * H + cur.h) * ps + ((int)tok - page_of(a, tok) * ps);
+          const int64_t at = (int64_t)page * (H * ps) + (cur.h * ps + (int)tok - page_of(a, tok) * ps);
           ks = a.c.k_scales[at];
           vs = a.c.v_scales[at];
         }
       };
-      int page_next = cur.cnt > 1 && tok + kTile < tokens ? table[page_of(a, tok + kTile)] : -1;
       if (kF8) load_scales(tok, page, ks_next, vs_next);
       next = get_piece(p + 1, false);
       if (next.cnt > 0) load_q(next);
 
 #pragma unroll 1
-      for (int i = 0; i < cur.cnt; ++i, ++g) {
+      for (int i = i0; i < cur.cnt; i += kTurns) {
+        const int64_t g = g0 + i;
         const int b = (int)(g & 1);
         const int key0 = (cur.tile0 + cur.first + i) * kTile, key = key0 + gt;
         const bool there = page >= 0 && page < a.c.pages;
-        tok += kTile;
+        tok += kTurns * kTile;
         page = page_next;
-        page_next = i + 2 < cur.cnt && tok + kTile < tokens ? table[page_of(a, tok + kTile)] : -1;
+        page_next = page_at(tok + kTurns * kTile, i + 2 * kTurns);
         if (kF8) {
           ks = ks_next, vs = vs_next;
           load_scales(tok, page, ks_next, vs_next);
@@ -957,9 +977,9 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
           for (int n = 0; n < kCols; ++n)
             if (!there || !sees(s_rows[n], key, cur.len)) s[n] = -INFINITY;
         }
-        bool free = g == 0;  // the weights' place
+        bool free = g < kTurns;  // the weights' place
         auto wait_free = [&]() {
-          if (!free && ok) ok = bar_wait(p_empty, (uint32_t)(g - 1) & 1u);
+          if (!free && ok) ok = bar_wait(p_empty(turn), (round_of(g) - 1) & 1u);
           free = true;
         };
         float over = -INFINITY;  // by how much a score passes its reference
@@ -968,7 +988,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
           const float4 r = *reinterpret_cast<const float4*>(s_ref + n);
           over = fmaxf(over, fmaxf(fmaxf(s[n] - r.x, s[n + 1] - r.y), fmaxf(s[n + 2] - r.z, s[n + 3] - r.w)));
         }
-        if (i == 0 || group_any(bid, over > kHead)) {  // every row's reference is its largest score so far
+        if (i == i0 || warps_any<kGroup>(bid, over > kHead)) {  // every row's reference is its largest score so far
           float most = 0.0f;
 #pragma unroll
           for (int n = 0; n < kCols; ++n) {
@@ -976,7 +996,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
             if (lane == n) most = x;
           }
           if (lane < kCols) s_red[gw * kCols + lane] = most;
-          group_sync(bid);
+          warps_sync<kGroup>(bid);
           if (gt < kCols) {
             const float was = s_ref[gt];
             const float x = fmaxf(fmaxf(fmaxf(s_red[gt], s_red[16 + gt]), fmaxf(s_red[32 + gt], s_red[48 + gt])),
@@ -984,18 +1004,18 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
             s_fac[gt] = exp2_(was - x);
             s_ref[gt] = x;
           }
-          group_sync(bid);
-          if (i > 0) {
+          warps_sync<kGroup>(bid);
+          if (i > i0) {
             wait_free();  // all so far is added up
             fence_after();
 #pragma unroll 1
             for (int part = 0; part < M::kParts; ++part) {
               float o[kCols];
-              tmem_ld16(tmem + lanes + kO + part * N + n0, o);
+              tmem_ld16(tmem + lanes + o_at + part * N + n0, o);
               tmem_ld_wait(o);
 #pragma unroll
               for (int n = 0; n < kCols; ++n) o[n] *= s_fac[n];
-              tmem_st16(tmem + lanes + kO + part * N + n0, o);
+              tmem_st16(tmem + lanes + o_at + part * N + n0, o);
             }
             fence_before();
 #pragma unroll
@@ -1029,7 +1049,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
             uint32_t c[4];
 #pragma unroll
             for (int n = 0; n < 4; ++n) c[n] = __byte_perm(w[2 * n], w[2 * n + 1], 0x7531);
-            *reinterpret_cast<uint4*>(sm + M::kP + ((part * N + n0) >> 4) * (kTile * 16) + gt * 16) =
+            *reinterpret_cast<uint4*>(s_p + ((part * N + n0) >> 4) * (kTile * 16) + gt * 16) =
                 make_uint4(c[0], c[1], c[2], c[3]);
             if (part < 3) {
 #pragma unroll
@@ -1049,7 +1069,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
               hi[e] = bf16x2(x, y);
               lo[e] = bf16x2(x - bf16_lo(hi[e]), y - bf16_hi(hi[e]));
             }
-            unsigned char* to = sm + M::kP + ((n0 + n) >> 3) * (kTile * 16) + gt * 16;
+            unsigned char* to = s_p + ((n0 + n) >> 3) * (kTile * 16) + gt * 16;
             *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<uint4*>(to + 2 * N * kTile) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
@@ -1057,7 +1077,6 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
         if (!kF8 && partly) {
           // a value that is not finite, of a token that not all rows see: 0 times it would be NaN. It
           // leaves the product, and is added at the end to the rows that see it
-          if (part_tiles < 4) part_tile[part_tiles] = key0;
           const int64_t x = 2 * g + 1;
           const int slot = (int)(x % M::kSlots);
           if (there && !sees(every, key, cur.len)) {
@@ -1086,24 +1105,34 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
               }
               *at(c) = v;
             }
-            if (odd) atomicOr(&ms.odd[p & 3], 1 << min(part_tiles, 3));
+            // such tiles are among the unit's first two and last two
+            const int at_tile = cur.first + i;
+            if (odd) atomicOr(&ms.odd[p & 3], 1 << (at_tile < 2 && key0 < every.x ? at_tile : 2 + cur.tiles - 1 - at_tile));
           }
-          ++part_tiles;
         }
         fence_async();
-        bar_arrive(p_full);
+        bar_arrive(p_full(turn));
+        if (M::kQs > 1 && i == i0 && next.cnt > 0) prepare(next, p + 1);
       }
+      if (M::kQs > 1 && i0 >= cur.cnt && next.cnt > 0) prepare(next, p + 1);
+      g0 += cur.cnt;
 
       // ---- the sums; the next piece's scores can begin meanwhile ---------------------------------------
-      const float ref = gt < kCols ? s_ref[gt] : 0.0f;  // of row gt, before the next piece's
+      const float mine_ref = gt < kCols ? s_ref[gt] : 0.0f;  // of row gt, before the next piece's
       column_sums(sum);
       if (!(lane & 1)) s_red[gw * kCols + (lane >> 1)] = sum[0];
-      have = !group_any(bid, !ok || next.cnt == 0);
-      if (have) prepare(next, p + 1);
-      float l = 0.0f;
+      have = !any(!ok || next.cnt == 0);
+      if (M::kQs == 1 && have) prepare(next, p + 1);
+      float l = 0.0f;  // row gt's sum, and reference
+      float ref = mine_ref;
       if (gt < kCols) {
         l = (s_red[gt] + s_red[16 + gt]) + (s_red[32 + gt] + s_red[48 + gt]);
-        s_fac[gt] = l == 0.0f ? 0.0f : 1.0f / l;  // 0: a row that sees nothing
+        if (kTurns == 1) {
+          s_fac[gt] = l == 0.0f ? 0.0f : 1.0f / l;  // 0: a row that sees nothing
+        } else {  // for the other group: in the place of the warps' sums, which this thread alone reads
+          s_red[gt] = ref;
+          s_red[16 + gt] = l;
+        }
       }
       if (ok) ok = bar_wait(o_full, (uint32_t)p & 1u);
       fence_after();
@@ -1112,18 +1141,18 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
       float o[kCols];
       {
         float rest[kCols];
-        tmem_ld16(tmem + lanes + kO + n0, o);
-        tmem_ld16(tmem + lanes + kO + N + n0, rest);
+        tmem_ld16(tmem + lanes + o_at + n0, o);
+        tmem_ld16(tmem + lanes + o_at + N + n0, rest);
         tmem_ld_wait(o);
         tmem_ld_wait(rest);
 #pragma unroll
         for (int n = 0; n < kCols; ++n) o[n] += rest[n];
         if (kF8) {
-          tmem_ld16(tmem + lanes + kO + 2 * N + n0, rest);
+          tmem_ld16(tmem + lanes + o_at + 2 * N + n0, rest);
           tmem_ld_wait(rest);
 #pragma unroll
           for (int n = 0; n < kCols; ++n) o[n] = fmaf(rest[n], 0.00390625f, o[n]);
-          tmem_ld16(tmem + lanes + kO + 3 * N + n0, rest);
+          tmem_ld16(tmem + lanes + o_at + 3 * N + n0, rest);
           tmem_ld_wait(rest);
 #pragma unroll
           for (int n = 0; n < kCols; ++n) o[n] = fmaf(rest[n], 0.00390625f, o[n]) * 0.0078125f;  // 2^-7
@@ -1131,9 +1160,9 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
       }
       if (!kF8 && ms.odd[p & 3]) {
 #pragma unroll 1
-        for (int k = 0; k < min(part_tiles, 4) && mine; ++k) {
+        for (int k = 0; k < 4 && mine; ++k) {
           if (!((ms.odd[p & 3] >> k) & 1)) continue;
-          const int k0 = k == 0 ? part_tile[0] : k == 1 ? part_tile[1] : k == 2 ? part_tile[2] : part_tile[3];
+          const int k0 = (cur.tile0 + (k < 2 ? k : cur.tiles - 1 - (k - 2))) * kTile;
 #pragma unroll 1
           for (int key = k0; key < min(k0 + kTile, tokens); ++key) {
             const int pg = page_of(a, key), page = table[pg];
@@ -1150,7 +1179,40 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
       }
       fence_before();
       bar_arrive(o_empty);
-      group_sync(bid);  // s_fac
+      if (kTurns > 1) {
+        // both groups' sums over one reference; the first adds the second's
+        warps_sync<kBoth>(kBothId);
+        const float* other = s_red + (turn == 0 ? 4 : -4) * kCols;
+        const bool any_mine = i0 < cur.cnt;  // else nothing of this piece is in its accumulators
+#pragma unroll
+        for (int n = 0; n < kCols; ++n) {
+          const float f = exp2_(s_red[n] - fmaxf(s_red[n], other[n]));
+          o[n] = any_mine ? o[n] * f : 0.0f;
+        }
+        float* sums = reinterpret_cast<float*>(sm + M::kP + M::kPlace);  // [16][D], where its weights were
+        if (turn > 0) {
+          if (mine) {
+#pragma unroll
+            for (int n = 0; n < kCols; ++n) sums[n * D + d] = o[n];
+          }
+          warps_sync<kBoth>(kBothId);
+          continue;
+        }
+        if (gt < kCols) {
+          const float top = fmaxf(ref, other[gt]);
+          l = l * exp2_(ref - top) + other[16 + gt] * exp2_(other[gt] - top);
+          ref = top;
+          s_fac[gt] = l == 0.0f ? 0.0f : 1.0f / l;
+        }
+        warps_sync<kBoth>(kBothId);
+        if (mine) {
+#pragma unroll
+          for (int n = 0; n < kCols; ++n) o[n] += sums[n * D + d];
+        }
+        if (have) warps_arrive<kBoth>(kSumId);
+      } else {
+        warps_sync<kGroup>(bid);  // s_fac
+      }
       const bool whole = cur.cnt == cur.tiles;
       const int64_t slot = (int64_t)(2 * blockIdx.x + (cur.first == 0 ? 1 : 0)) * N;
       auto put_lse = [&](int n, float ref, float l) {
@@ -1180,7 +1242,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
         for (int n = 0; n < kCols; ++n)
           if (n0 + n < cur.valid && mine) __stcg(a.acc + (slot + n0 + n) * D + d, o[n]);
         if (gt < kCols && n0 + gt < cur.valid) __stcg(a.ml + slot + n0 + gt, make_float2(ref, l));
-        group_sync(bid);
+        warps_sync<kGroup>(bid);
         if (gt == 0) {
           __threadfence();
           int32_t* count = a.count + b0 * R::kGroups + grp;
@@ -1188,7 +1250,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
           ms.last[grp] = was == pieces - 1;
           if (ms.last[grp]) *count = 0;
         }
-        group_sync(bid);
+        warps_sync<kGroup>(bid);
         if (ms.last[grp]) {  // all pieces are there: added in their order
           __threadfence();
           auto slot_of = [&](int k) { return (int64_t)(k == 0 ? 2 * b0 + 1 : 2 * (b0 + k)) * N + n0; };
@@ -1204,7 +1266,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
           for (int k = gt / 16 + 8; k < pieces; k += 8) top = fmaxf(top, stat(k).x);
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
           if (lane < 16) s_red[gw * 16 + jn] = top;
-          group_sync(bid);
+          warps_sync<kGroup>(bid);
           top = fmaxf(fmaxf(s_red[jn], s_red[16 + jn]), fmaxf(s_red[32 + jn], s_red[48 + jn]));
           float sums = exp2_(own.x - top) * own.y;
 #pragma unroll 1
@@ -1213,16 +1275,16 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
             sums += exp2_(st.x - top) * st.y;
           }
           sums += __shfl_xor_sync(0xffffffffu, sums, 16);
-          group_sync(bid);
+          warps_sync<kGroup>(bid);
           if (lane < 16) s_red[gw * 16 + jn] = sums;
-          group_sync(bid);
+          warps_sync<kGroup>(bid);
           sums = (s_red[jn] + s_red[16 + jn]) + (s_red[32 + jn] + s_red[48 + jn]);
           if (gt < kCols) {
             s_ref[gt] = top;  // the next piece's is set after
             s_fac[gt] = sums == 0.0f ? 0.0f : 1.0f / sums;
             if (gt < mine_n) put_lse(n0 + gt, top, sums);
           }
-          group_sync(bid);
+          warps_sync<kGroup>(bid);
           // several rows a thread at once, 4 dims of each
           constexpr int T = D / 4, kRowsAt = kGroup / T, kEach = kCols / kRowsAt;
           const int d4 = gt % T * 4, r0 = gt / T;
@@ -1263,7 +1325,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
   __syncwarp();
   fence_before();
   __syncthreads();
-  if (warp == kMmaWarp)
+  if (warp == kScoreWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem)
                  : "memory");
 }
@@ -1286,7 +1348,8 @@ tfd_status launch(const Args<D>& a, cudaStream_t stream) {
   const int sms = tfd_host::device_sms(dev);
   constexpr int smem = Smem<D, N, kF8>::kBytes;
   return tfd_host::launch_clusters<paged_attn_kernel<D, N, kF8>>(
-      a, dev, std::min(kMaxBlocks, std::max(1, sms)), 1, Roles<N>::kT, smem, smem, stream);
+      a, dev, std::min(kMaxBlocks, std::max(1, sms * Roles<D, N, kF8>::kCtas)), 1, Roles<D, N, kF8>::kT, smem, smem,
+      stream);
 }
 
 template <int D>
@@ -1331,7 +1394,8 @@ extern "C" tfd_status tfd_paged_attn(const void* q, int64_t ldq, int rows, int q
   const int64_t width = (int64_t)q_heads * c.dim;
   if (ldq < width || ldq % 8 || ldo < width || ldo % 8) return TFD_ERR_INVALID;
   if (requests > TFD_MAX_REQUESTS || ldq > ((int64_t)1 << 30) || ldo > ((int64_t)1 << 30) ||
-      ldt > ((int64_t)1 << 40) || (int64_t)rows * q_heads > 2147483647)
+      ldt > ((int64_t)1 << 40) || (int64_t)rows * q_heads > 2147483647 ||
+      std::max({c.page_stride, c.token_stride, c.head_stride}) > 2147483647)
     return TFD_ERR_UNSUPPORTED;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(table, 4) || !aligned(lens, 4) ||
       !aligned(row_start, 4) || !aligned(pos, 4) || !aligned(tree, 4) || !aligned(q_gamma, 2) ||
@@ -1371,14 +1435,14 @@ extern "C" tfd_status tfd_paged_attn(const void* q, int64_t ldq, int rows, int q
   float* acc = (float*)(w + kMaxBlocks * 16 + slots * 8);
   cudaStream_t s = tfd_host::as_stream(stream);
   // 2^(31 + b) / page_size rounded up, b the bits of page_size - 1: exact for tokens below 2^31
-  uint32_t shift = 31;
-  while ((1 << (shift - 31)) < c.page_size) ++shift;
-  const uint32_t mul = (uint32_t)((((uint64_t)1 << shift) + c.page_size - 1) / c.page_size);
+  uint32_t shift = 0;
+  while ((1 << shift) < c.page_size) ++shift;
+  const uint32_t mul = (uint32_t)((((uint64_t)1 << (31 + shift)) + c.page_size - 1) / c.page_size);
 #define TFD_ATTN_DIM(D)                                                                          \
   if (c.dim == D) {                                                                              \
     Args<D> a = {(const uint16_t*)q, ldq, table, ldt, lens, row_start, pos, tree,                \
                  (const uint16_t*)q_gamma, (uint16_t*)out, ldo, lse, count, ml, acc, dev_status, \
-                 c, rows, q_heads, group, max_pages, requests, max_new, window, qk, eps, sc, mul, shift, {}}; \
+                 c, rows, q_heads, group, max_pages, requests, max_new, window, qk, eps, sc, mul, shift, (int)c.page_stride, (int)c.token_stride, (int)c.head_stride, {}}; \
     return launch_dim<D>(a, rope_base, s);                                                       \
   }
   TFD_ATTN_DIM(64)

@@ -60,17 +60,23 @@ __device__ __forceinline__ int64_t shfl_up64(int64_t v, int d) {
   return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
+template <bool kOne>  // one block
 __global__ void __launch_bounds__(kT) page_plan_kernel(const Args a) {
   extern __shared__ int32_t sm[];
   __shared__ int64_t warp_sums[3][kT / 32];
   tfd_host::after_previous();
   cg::cluster_group cl = cg::this_cluster();
+  const unsigned rank = kOne ? 0 : cl.block_rank(), blocks = kOne ? 1 : cl.num_blocks();
+  auto sync = [&] {
+    if (kOne) __syncthreads();
+    else cl.sync();
+  };
   const int R = a.requests, ps = a.page_size;
   int32_t* first[3] = {sm, sm + R + 1, sm + 2 * (R + 1)};  // rows, given back, missing
   uint8_t* bad = reinterpret_cast<uint8_t*>(sm + 3 * (R + 1));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n_free = *a.n_free;
-  const bool lead = cl.block_rank() == 0;
+  const bool lead = rank == 0;
   for (int r = tid; r < R; r += kT) {
     const int32_t len = a.lens[r], n = a.n_new[r], held = a.held[r];
     bool b = len < 0 || n < 0 || held < 0 || held > a.max_pages;
@@ -125,7 +131,7 @@ __global__ void __launch_bounds__(kT) page_plan_kernel(const Args a) {
   const int32_t top = broken ? 0 : n_free + back;
   // a request gets its pages if all that are missing up to it are there
   auto without = [&](int r) { return first[2][r + 1] > first[2][r] && first[2][r + 1] > top; };
-  const int64_t t0 = (int64_t)cl.block_rank() * kT + tid, nt = (int64_t)cl.num_blocks() * kT;
+  const int64_t t0 = (int64_t)rank * kT + tid, nt = (int64_t)blocks * kT;
   if (back > 0 || missing > 0) {
     if (!broken) {
       for (int64_t i = t0; i < back; i += nt) {
@@ -136,7 +142,7 @@ __global__ void __launch_bounds__(kT) page_plan_kernel(const Args a) {
         a.free_ids[top - 1 - i] = id;
       }
     }
-    cl.sync();  // the stack is complete; every block has read what the requests held
+    sync();  // the stack is complete; every block has read what the requests held
     for (int64_t i = t0; i < missing; i += nt) {
       const int r = find(first[2], R, (int32_t)i);
       const int64_t want = pages_of(a.lens[r], a.n_new[r], ps);
@@ -159,26 +165,41 @@ __global__ void __launch_bounds__(kT) page_plan_kernel(const Args a) {
       }
       *a.n_free = top - first[2][lo];
     }
-    cl.sync();  // the tables are complete
+    sync();  // the tables are complete
   }
   for (int64_t r = t0; r <= R; r += nt) a.row_start[r] = first[0][r];
   const int32_t total = first[0][R];
   if (a.slots == nullptr) return;
   if (total > a.rows && t0 == 0) set_dev_status(a.dev_status, TFD_ERR_DEVICE_DATA);
-  for (int64_t i = t0; i < a.rows; i += nt) {
-    int32_t p = -1, slot = -1;
-    if (i < total) {
-      const int r = find(first[0], R, (int32_t)i);
-      if (!bad[r] && !without(r)) {
-        p = a.lens[r] + (int32_t)(i - first[0][r]);
-        const int32_t pg = p / ps;
-        const int32_t id = __ldcg(a.table + r * a.ldt + pg);
-        if (id >= 0 && id < a.pages) slot = id * ps + (p - pg * ps);
-        else set_dev_status(a.dev_status, TFD_ERR_DEVICE_DATA);
+  // several rows a thread at once: each waits for a search and then for its page
+  constexpr int kAtOnce = 4;
+  for (int64_t i0 = t0; i0 < a.rows; i0 += kAtOnce * nt) {
+    int32_t p[kAtOnce], pg[kAtOnce], id[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int64_t i = i0 + u * nt;
+      p[u] = id[u] = -1;
+      if (i < total && i < a.rows) {
+        const int r = find(first[0], R, (int32_t)i);
+        if (!bad[r] && !without(r)) {
+          p[u] = a.lens[r] + (int32_t)(i - first[0][r]);
+          pg[u] = (int32_t)((uint32_t)p[u] / (uint32_t)ps);
+          id[u] = __ldcg(a.table + r * a.ldt + pg[u]);
+        }
       }
     }
-    a.slots[i] = slot;
-    a.pos[i] = p;
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int64_t i = i0 + u * nt;
+      if (i >= a.rows) break;
+      int32_t slot = -1;
+      if (p[u] >= 0) {
+        if (id[u] >= 0 && id[u] < a.pages) slot = id[u] * ps + (p[u] - pg[u] * ps);
+        else set_dev_status(a.dev_status, TFD_ERR_DEVICE_DATA);
+      }
+      a.slots[i] = slot;
+      a.pos[i] = p[u];
+    }
   }
 }
 
@@ -227,6 +248,8 @@ extern "C" tfd_status tfd_page_plan(const int32_t* lens, const int32_t* n_new, i
   const size_t smem = (size_t)3 * 4 * (requests + 1) + requests;
   const int most = 3 * 4 * (TFD_MAX_REQUESTS + 1) + TFD_MAX_REQUESTS;
   const int c = requests <= kT && rows <= 8 * kT ? 1 : kBlocks;
-  return tfd_host::launch_clusters<page_plan_kernel>(a, dev, 1, c, kT, smem, most,
-                                                     tfd_host::as_stream(stream));
+  cudaStream_t st = tfd_host::as_stream(stream);
+  return c == 1
+             ? tfd_host::launch_clusters<page_plan_kernel<true>>(a, dev, 1, 1, kT, smem, most, st)
+             : tfd_host::launch_clusters<page_plan_kernel<false>>(a, dev, 1, c, kT, smem, most, st);
 }
