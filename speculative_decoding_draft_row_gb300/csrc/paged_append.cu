@@ -1,9 +1,10 @@
 // paged_append.cu - rows of keys and values into their slots of a paged cache: qk_norm and RoPE of the
 // keys, then bf16 or E4M3 codes with a scale a vector (largest magnitude / 448).
 //
-// A sweep bound by its bytes: a warp takes the heads of one row, 16 bytes a lane, all its loads in
-// flight before any arithmetic; a position's sines and cosines are formed once a warp, a pair or two a
-// lane, and shared through shared memory (with every lane forming its own, 4 times the work).
+// A sweep bound by its bytes, and for few rows by latency: a warp takes some heads of a row, 16 bytes a
+// lane, loads its next vectors (and their slot) before it uses these, and forms a position's sines and
+// cosines once, a pair or two a lane, shared through shared memory. 8193 rows of 8 heads of 128 in bf16 14.8 us,
+// 0.67 of the copy rate (one item a warp, loads after the slot is known: 18.6); one draft step 2.7 us.
 #include "paged.cuh"
 
 namespace {
@@ -11,13 +12,9 @@ namespace {
 using namespace tfd;
 
 constexpr int kT = 256;
-#ifndef KI
-#define KI 2
-#endif
-#ifndef KB
-#define KB 4
-#endif
-constexpr int kIter = KI;  // steps of a warp: 8 heads of 128, 16 of 64
+
+// Steps of an item (2 heads of 128 or 4 of 64 each), and blocks of an SM that registers allow for it.
+constexpr int blocks_of(int iter) { return iter == 1 ? 3 : 2; }
 
 template <int D>
 struct Args {
@@ -61,45 +58,31 @@ __device__ __forceinline__ void put_codes(const float (&x)[8], uint8_t* to, floa
   if (to && one) *scale = s;
 }
 
-template <int D, bool kF8>
-__global__ void __launch_bounds__(kT, KB) paged_append_kernel(const Args<D> a) {
+// A warp's share of a row into its slot.
+template <int D, bool kF8, int kIter>
+__device__ __forceinline__ void write_item(const Args<D>& a, const RopeTurns<D>& turns, float2* turn, int64_t w,
+                                           int slot, int p, const uint4 (&kr)[kIter], const uint4 (&vr)[kIter],
+                                           const float (&gm)[8]) {
   constexpr int L = D / 8, kPer = 32 / L;  // lanes of a vector, vectors of a step
-  __shared__ __align__(16) float2 turn[kT / 32][D / 2];
-  tfd_host::after_previous();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t w = (int64_t)blockIdx.x * (kT / 32) + warp;
-  if (w >= (int64_t)a.rows * a.groups) return;  // warp-uniform, and no barrier of the block follows
-  const int row = (int)(w / a.groups), h0 = (int)(w % a.groups) * (kIter * kPer) + lane / L;
-  const int l = lane % L;
-  const int slot = a.slots[row], p = a.qk & TFD_QK_ROPE ? a.pos[row] : 0;
+  const int lane = threadIdx.x & 31, l = lane % L;
+  const int h0 = (int)(w % a.groups) * (kIter * kPer) + lane / L;
   if (slot == -1) return;
   if (slot < 0 || slot >= a.c.pages * a.c.page_size || p < 0) {
     if (lane == 0) set_dev_status(a.dev_status, TFD_ERR_DEVICE_DATA);
     return;
   }
-  uint4 kr[kIter], vr[kIter];
-  const uint16_t* kp = a.k_rows + row * a.ldk + (int64_t)h0 * D + 8 * l;
-  const uint16_t* vp = a.v_rows + row * a.ldv + (int64_t)h0 * D + 8 * l;
-#pragma unroll
-  for (int i = 0; i < kIter; ++i) {
-    const bool in = h0 + i * kPer < a.c.heads;
-    kr[i] = in ? *reinterpret_cast<const uint4*>(kp + i * kPer * D) : make_uint4(0u, 0u, 0u, 0u);
-    vr[i] = in ? *reinterpret_cast<const uint4*>(vp + i * kPer * D) : make_uint4(0u, 0u, 0u, 0u);
-  }
-  float gm[8], sn[8], cs[8];
+  float sn[8], cs[8];
   if (a.qk & TFD_QK_ROPE) {
+    __syncwarp();  // the last item's are done with
 #pragma unroll
-    for (int i = lane; i < D / 2; i += 32) rope_pair_pi<D>(p, a.turns, i, turn[warp][i].y, turn[warp][i].x);
+    for (int i = lane; i < D / 2; i += 32) rope_pair_fast<D>(p, turns, i, turn[i].y, turn[i].x);
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
-      const float4 t = *reinterpret_cast<const float4*>(&turn[warp][8 * (l % (L / 2)) + j]);
+      const float4 t = *reinterpret_cast<const float4*>(&turn[8 * (l % (L / 2)) + j]);
       cs[j] = t.x, sn[j] = t.y, cs[j + 1] = t.z, sn[j + 1] = t.w;
     }
   }
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    gm[j] = a.gamma && (a.qk & TFD_QK_NORM) ? bf16_bits_to_f32(a.gamma[8 * l + j]) : 1.0f;
   const int page = slot / a.c.page_size, at = slot - page * a.c.page_size;
   const int64_t base = page * a.c.page_stride + at * a.c.token_stride + 8 * l;
 #pragma unroll
@@ -150,16 +133,70 @@ __global__ void __launch_bounds__(kT, KB) paged_append_kernel(const Args<D> a) {
   }
 }
 
+template <int D, bool kF8, int kIter>
+__global__ void __launch_bounds__(kT, blocks_of(kIter)) paged_append_kernel(const Args<D> a) {
+  constexpr int L = D / 8, kPer = 32 / L;  // lanes of a vector, vectors of a step
+  __shared__ __align__(16) float2 turn[kT / 32][D / 2];
+  // the pairs' frequencies: as an argument each lane's would be fetched after the other's, every time
+  __shared__ RopeTurns<D> turns;
+  if (threadIdx.x < D / 2) turns.t[threadIdx.x] = a.turns.t[threadIdx.x];
+  __syncthreads();
+  tfd_host::after_previous();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % L;
+  float gm[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    gm[j] = a.gamma && (a.qk & TFD_QK_NORM) ? bf16_bits_to_f32(a.gamma[8 * l + j]) : 1.0f;
+  // an item: the heads of a row that a warp takes; the next one's vectors are loaded before this one's are used
+  const int64_t items = (int64_t)a.rows * a.groups, step = (int64_t)gridDim.x * (kT / 32);
+  uint4 kr[kIter], vr[kIter];
+  int slot = -1, p = 0;
+  auto load = [&](int64_t w) {
+    if (w >= items) return;
+    const int row = (int)(w / a.groups), h0 = (int)(w - (int64_t)row * a.groups) * (kIter * kPer) + lane / L;
+    slot = a.slots[row];
+    p = a.qk & TFD_QK_ROPE ? a.pos[row] : 0;
+    const uint16_t* kp = a.k_rows + row * a.ldk + (int64_t)h0 * D + 8 * l;
+    const uint16_t* vp = a.v_rows + row * a.ldv + (int64_t)h0 * D + 8 * l;
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) {
+      const bool in = h0 + i * kPer < a.c.heads;
+      kr[i] = in ? *reinterpret_cast<const uint4*>(kp + i * kPer * D) : make_uint4(0u, 0u, 0u, 0u);
+      vr[i] = in ? *reinterpret_cast<const uint4*>(vp + i * kPer * D) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  int64_t w = (int64_t)blockIdx.x * (kT / 32) + warp;
+  load(w);
+  for (; w < items; w += step) {
+    uint4 k_now[kIter], v_now[kIter];
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) k_now[i] = kr[i], v_now[i] = vr[i];
+    const int slot_now = slot, p_now = p;
+    load(w + step);
+    write_item<D, kF8, kIter>(a, turns, turn[warp], w, slot_now, p_now, k_now, v_now, gm);
+  }
+}
+
+template <int D, bool kF8, int kIter>
+tfd_status launch_items(Args<D>& a, int dev, int sms, cudaStream_t stream) {
+  constexpr int heads = kIter * 32 / (D / 8);  // of an item
+  a.groups = (a.c.heads + heads - 1) / heads;
+  const int64_t blocks = ((int64_t)a.rows * a.groups + kT / 32 - 1) / (kT / 32);
+  return tfd_host::launch_clusters<paged_append_kernel<D, kF8, kIter>>(
+      a, dev, std::min(blocks, (int64_t)sms * blocks_of(kIter)), 1, kT, 0, 0, stream);
+}
+
+// Items of one step while there is a warp for each at once (288 rows of 8 heads 3.9 us, with four steps 7.8);
+// beyond, four steps share a row's sines and cosines and keep more loads in flight (8193 rows 14.8 us, with one
+// step 18.2).
 template <int D, bool kF8>
 tfd_status launch(Args<D>& a, float rope_base, cudaStream_t stream) {
   if (a.qk & TFD_QK_ROPE) a.turns = tfd_host::rope_turns<D>(rope_base);
-  constexpr int heads = kIter * 32 / (D / 8);  // of a warp
-  a.groups = (a.c.heads + heads - 1) / heads;
-  const int64_t warps = (int64_t)a.rows * a.groups;
   int dev = 0;
-  tfd_host::device_sms(dev);
-  return tfd_host::launch_clusters<paged_append_kernel<D, kF8>>(
-      a, dev, (warps + kT / 32 - 1) / (kT / 32), 1, kT, 0, 0, stream);
+  const int sms = std::max(1, tfd_host::device_sms(dev));
+  const int64_t single = (int64_t)a.rows * ((a.c.heads * (D / 8) + 31) / 32);
+  return single <= (int64_t)sms * blocks_of(1) * (kT / 32) ? launch_items<D, kF8, 1>(a, dev, sms, stream)
+                                                           : launch_items<D, kF8, 4>(a, dev, sms, stream);
 }
 
 template <int D>

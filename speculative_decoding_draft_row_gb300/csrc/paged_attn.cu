@@ -262,6 +262,11 @@ __device__ __forceinline__ int page_of(const Args<D>& a, int64_t token) {
   return (int)(__umulhi(2u * (uint32_t)token, a.page_mul) >> a.page_shift);
 }
 
+// a / b of numbers that rarely need 64 bits.
+__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+  return ((uint64_t)a | (uint64_t)b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // ---- the line ------------------------------------------------------------------------------------
 struct Request {
   int r, row0, n, len;   // its rows and the tokens before them
@@ -319,11 +324,11 @@ struct Cuts {
   int keep;
   // the block that has the first tile of the unit that begins at `line0`
   __device__ __forceinline__ int64_t owner(int64_t line0, int tiles) const {
-    return (line0 + kStart + (tiles < 2 * keep ? tiles : keep) - 1) / share;
+    return quot(line0 + kStart + (tiles < 2 * keep ? tiles : keep) - 1, share);
   }
   __device__ __forceinline__ int64_t pieces(int64_t line0, int tiles) const {
     if (tiles < 2 * keep) return 1;
-    return (line0 + kStart + tiles - keep) / share - owner(line0, tiles) + 1;
+    return quot(line0 + kStart + tiles - keep, share) - owner(line0, tiles) + 1;
   }
   // where the cut at `t`, which lies in the unit, moves to
   __device__ __forceinline__ int64_t moved(int64_t t, int64_t line0, int tiles) const {
@@ -467,7 +472,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
       if (w < warp) before += scan[w];
       total += scan[w];
     }
-    cuts.share = (total + gridDim.x - 1) / gridDim.x;
+    cuts.share = quot(total + gridDim.x - 1, gridDim.x);
     cuts.keep = (int)min(cuts.share, (int64_t)kKeep);
     // the block's stretch: from its cut to the next one's
     if (tid < 2) ms.ends[tid] = total;
@@ -483,7 +488,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
       for (int e = 0; e < 2; ++e) {
         const int64_t t = e ? hi : lo;
         if (at <= t && t < at + u) {
-          ms.ends[e] = cuts.moved(t, at + (t - at) / q.places * q.places, q.tiles);
+          ms.ends[e] = cuts.moved(t, at + quot(t - at, q.places) * q.places, q.tiles);
           if (e == 0) ms.first = q;
         }
       }
@@ -599,12 +604,12 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
         rq.base = next;
       }
       if (t < t_end) {
-        const int64_t unit = (t - rq.base) / rq.places;
+        const int64_t unit = quot(t - rq.base, rq.places);
         p.line0 = rq.base + unit * rq.places;
         p.r = rq.r, p.row0 = rq.row0, p.n = rq.n, p.len = rq.len, p.tile0 = rq.tile0, p.tiles = rq.tiles;
         const int64_t line1 = p.line0 + kStart;  // of its first tile
         p.first = (int)max((int64_t)0, t - line1);
-        p.h = (int)(unit / rq.mt);
+        p.h = (int)quot(unit, rq.mt);
         const int m0 = (int)(unit - (int64_t)p.h * rq.mt) * N;
         p.cnt = (int)(min((int64_t)rq.tiles, t_end - line1) - p.first);
         p.valid = min(N, rq.n * a.group - m0);

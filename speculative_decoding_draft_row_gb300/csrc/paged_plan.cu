@@ -18,8 +18,11 @@ namespace {
 using namespace tfd;
 namespace cg = cooperative_groups;
 
-constexpr int kT = 512;
 constexpr int kBlocks = 8;  // blocks of the cluster where there is work for them
+
+// A small round waits for barriers: 256 threads 4.2 us, 512 5.0. A large one has work for all (2048 requests,
+// 52000 rows: 14.8 us; 1024 threads a block 16.1).
+constexpr int threads_of(bool one) { return one ? 256 : 512; }
 
 struct Args {
   const int32_t* lens;
@@ -61,7 +64,8 @@ __device__ __forceinline__ int64_t shfl_up64(int64_t v, int d) {
 }
 
 template <bool kOne>  // one block
-__global__ void __launch_bounds__(kT) page_plan_kernel(const Args a) {
+__global__ void __launch_bounds__(threads_of(kOne)) page_plan_kernel(const Args a) {
+  constexpr int kT = threads_of(kOne);
   extern __shared__ int32_t sm[];
   __shared__ int64_t warp_sums[3][kT / 32];
   tfd_host::after_previous();
@@ -247,9 +251,9 @@ extern "C" tfd_status tfd_page_plan(const int32_t* lens, const int32_t* n_new, i
                   slots, pos,   dev_status, rows, requests, page_size, max_pages, pages};
   const size_t smem = (size_t)3 * 4 * (requests + 1) + requests;
   const int most = 3 * 4 * (TFD_MAX_REQUESTS + 1) + TFD_MAX_REQUESTS;
-  const int c = requests <= kT && rows <= 8 * kT ? 1 : kBlocks;
+  const int c = requests <= 512 && rows <= 4096 ? 1 : kBlocks;
   cudaStream_t st = tfd_host::as_stream(stream);
   return c == 1
-             ? tfd_host::launch_clusters<page_plan_kernel<true>>(a, dev, 1, 1, kT, smem, most, st)
-             : tfd_host::launch_clusters<page_plan_kernel<false>>(a, dev, 1, c, kT, smem, most, st);
+             ? tfd_host::launch_clusters<page_plan_kernel<true>>(a, dev, 1, 1, threads_of(true), smem, most, st)
+             : tfd_host::launch_clusters<page_plan_kernel<false>>(a, dev, 1, c, threads_of(false), smem, most, st);
 }
