@@ -439,7 +439,7 @@ tfd_status tfd_lora(const void* x, int rows, int64_t k, int64_t ldx, const void*
  *             E4M3 codes. Elements of a vector adjoin; the strides are multiples of 16 bytes, in any
  *             order ([page][head][token] as well), k and v 16-byte aligned.
  *   k_scales, v_scales device float [pages][heads][page_size] (E4M3 only, else NULL): a vector is its
- *             codes times its scale (not negative). No row sees a NaN code (0x7F, 0xFF).
+ *             codes times its scale. Tokens have no NaN codes (0x7F, 0xFF).
  * A slot is page * page_size + the token's place in the page; pages * page_size < 2^31. page_size
  * 1..TFD_MAX_PAGE; heads 1..1024; dim 64 or 128 (others: TFD_ERR_UNSUPPORTED).
  */
@@ -464,26 +464,27 @@ typedef struct {
  *   plans a round also returns what the last round's turned-down drafts took, and lens = n_new = 0
  *   returns all of a request. The free pages are a stack free_ids[0 .. *n_free): pages given back go
  *   on it, then missing ones come from its top, both in the order of requests and of their pages; of
- *   the pages given back the first ends on top, so that pages taken by one call and given back by the next
- *   leave the stack as it was. Lengths can stay on the GPU from round to round.
+ *   the pages given back the first ends on top, so that pages taken by one call and given back by
+ *   the next leave the stack as it was. Lengths can stay on the GPU from round to round.
  *   row_start[r] = n_new[0] + .. + n_new[r - 1] (requests + 1 values); for row i = row_start[r] + j:
  *   pos[i] = lens[r] + j, slots[i] = the slot of that token. Rows from row_start[requests] to
  *   `rows` get slot and position -1.
  * Args:
  *   lens, n_new device int32 [requests]; requests 1..TFD_MAX_REQUESTS; page_size 1..TFD_MAX_PAGE.
  *   table    device int32 [requests][ldt], ldt >= max_pages >= 1, requests * max_pages < 2^31:
- *            entries up to held[r] are the request's pages; entries behind what it then holds are left as they were.
+ *            entries up to held[r] are the request's pages; entries behind what it then holds are
+ *            left as they were.
  *   held     device int32 [requests], in and out. free_ids device int32 [pages], n_free device int32,
  *            in and out; pages >= 1 is the number of the cache's pages.
  *   row_start device int32 [requests + 1]; slots, pos device int32 [rows], or both NULL (rows 0).
  *   No array overlaps another.
  *   TFD_ERR_DEVICE_DATA: a negative length or count, a held count outside [0, max_pages] or a
  *   request that needs more than max_pages (it keeps its pages, its rows get slot and position -1; a
- *   negative count counts as 0); pages that run out (a request whose missing pages, counted with those of
- *   the requests before it, exceed the free ones gets none: it keeps what it holds, the table entries of the
- *   missing pages and its rows' slots and positions become -1); an n_free outside [0, pages], or more pages given
- *   back than the stack has room for (no page moves); a page id outside [0, pages) (slot -1); more
- *   rows than `rows` (those are not written).
+ *   negative count counts as 0); pages that run out (a request whose missing pages, counted with
+ *   those of the requests before it, exceed the free ones gets none: it keeps what it holds, the
+ *   table entries of the missing pages and its rows' slots and positions become -1); an n_free
+ *   outside [0, pages], or more pages given back than the stack has room for (no page moves); a page
+ *   id outside [0, pages) (slot -1); more rows than `rows` (those are not written).
  */
 tfd_status tfd_page_plan(const int32_t* lens, const int32_t* n_new, int requests, int page_size,
                          int32_t* table, int64_t ldt, int max_pages, int32_t* held,
@@ -496,13 +497,15 @@ tfd_status tfd_page_plan(const int32_t* lens, const int32_t* n_new, int requests
  *   Beside tfd_absorb, which writes a span into each stream's ring. For row i and head h:
  *     k' = rope(rmsnorm(k_rows[i][h]) * k_gamma, pos[i]), each step as `qk` names it;
  *     bf16: the cache takes bf16(k') and v_rows[i][h]; E4M3: s = fl32(amax / 448) and
- *     e4m3_rne_sat(fl32(x / s)) of k' (not rounded to bf16 before) and of v_rows[i][h] (amax 0 keeps its zeros).
+ *     e4m3_rne_sat(fl32(x / s)) of k' (not rounded to bf16 before) and of v_rows[i][h] (amax 0
+ *     keeps its zeros).
  *   The normalisation and rotation are those of tfd_window_attn.
  * Args:
  *   k_rows, v_rows device bf16 [rows][heads][dim], row strides ldk, ldv >= heads * dim, multiples
  *            of 8, 16-byte aligned; rows >= 1, rows * heads < 2^31.
- *   slots    device int32 [rows]: -1 leaves the row out; the others differ. Any other slot outside the cache, or a
- *            negative position (with TFD_QK_ROPE), sets TFD_ERR_DEVICE_DATA and the row is left out.
+ *   slots    device int32 [rows]: -1 leaves the row out; the others differ. Any other slot outside
+ *            the cache, or a negative position (with TFD_QK_ROPE), sets TFD_ERR_DEVICE_DATA and the
+ *            row is left out.
  *   pos      device int32 [rows] (may be NULL without TFD_QK_ROPE); k_gamma device bf16 [dim] or NULL
  *            (ones). E4M3 wants finite rows. The cache overlaps no input.
  */
@@ -523,10 +526,13 @@ tfd_status tfd_paged_append(const void* k_rows, int64_t ldk, const void* v_rows,
  *   those whose bit its word has set instead (bit j: row j; bits past the rows say nothing). With
  *   window >= 0 only tokens at depth >= its own - window: a cached token's depth is its number, a new
  *   row's lens[r] + j, or with `tree` lens[r] + (bits set in its word) - 1. A row that sees nothing
- *   gets zeros and an lse of -inf. What a row does not see (pages not in use, tokens behind the last, masked rows) may
- *   hold anything, NaN too.
- *   Sums and softmax statistics in fp32. q' enters its products as two bf16 parts (E4M3: four 8-bit parts),
- *   within 2^-16 of it; probabilities as two bf16 parts, within 2^-16 (E4M3: as f16, 2^-11).
+ *   gets zeros and an lse of -inf. What a row does not see (pages not in use, tokens behind the
+ *   last, masked ones) may hold anything, NaN too. Tokens before lens[r] - window (with `tree` before
+ *   lens[r] - window - 1) are not read, nor their table entries; of E4M3 the codes from there on are
+ *   not NaN.
+ *   Sums and softmax statistics in fp32. q' enters its products as two bf16 parts (E4M3: four 8-bit
+ *   parts), within 2^-16 of it; probabilities as two bf16 parts, within 2^-16 (E4M3: as f16, 2^-11;
+ *   value scales below 2^-96 lose more of them).
  * Args:
  *   q        device bf16 [rows][q_heads][dim], row stride ldq >= q_heads * dim, a multiple of 8,
  *            16-byte aligned; q_heads a multiple of the cache's heads, at most 64 times as many.
@@ -534,14 +540,20 @@ tfd_status tfd_paged_append(const void* k_rows, int64_t ldk, const void* v_rows,
  *            device int32 [requests + 1], from 0 to at most rows; max_new: no request has more rows,
  *            1..TFD_MAX_ROWS.
  *   pos      device int32 [rows] or NULL (the rows' depths): positions for TFD_QK_ROPE.
- *   tree     device int32 [rows] (32 bits) or NULL. window -1 or >= 0. scale > 0, or 0 for 1 / sqrt(dim).
+ *   tree     device int32 [rows] (32 bits) or NULL. window -1 or >= 0. scale > 0, or 0 for
+ *            1 / sqrt(dim).
  *   q_gamma  device bf16 [dim] or NULL (ones).
- *   out      device bf16 [rows][ldo], ldo >= q_heads * dim, a multiple of 8, 16-byte aligned; lse device float
- *            [rows][q_heads] or NULL. Rows of no request are left as they were. Outputs overlap no input.
+ *   out      device bf16 [rows][ldo], ldo >= q_heads * dim, a multiple of 8, 16-byte aligned; lse
+ *            device float [rows][q_heads] or NULL. Rows of no request are left as they were. Outputs
+ *            overlap no input.
  *   ws       device workspace of tfd_paged_attn_workspace() bytes.
- *   TFD_ERR_DEVICE_DATA: a request whose length is negative, whose tokens exceed max_pages or 2^31 - 1025,
- *   or whose rows are not 0..max_new rows within `rows` (its rows are left as they were); a page id outside [0, pages) where a
- *   token is needed (those tokens are not seen); a negative position (counts as 0).
+ *   dev_status also takes TFD_ERR_TIMEOUT: the parts of a block wait for each other, bounded to
+ *            about a second; outputs are then undefined, and ws is zero-filled before its next use.
+ *   TFD_ERR_DEVICE_DATA: a request whose length is negative, whose tokens exceed max_pages or 2^31 -
+ *   1025, or whose rows are not 0..max_new rows within `rows` (its rows are left as they were); a
+ *   page id outside [0, pages) where a token is read (those tokens are not seen); a negative
+ *   position (counts as 0).
+ *   TFD_ERR_UNSUPPORTED: strides of the cache, or rows * q_heads, from 2^31 on; ldq or ldo above 2^30.
  */
 size_t tfd_paged_attn_workspace(int max_new, int q_heads, int heads, int dim);
 tfd_status tfd_paged_attn(const void* q, int64_t ldq, int rows, int q_heads,

@@ -1,18 +1,41 @@
-// paged_attn_tc.cu - attention of a request's new rows over its tokens in a paged key-value cache, on the
-// tensor cores with accumulators in tensor memory: one pass with a running maximum and sum, split over
-// the cache's length and joined.
+// paged_attn.cu - attention of a request's new rows over its tokens in a paged key-value cache, on the
+// tensor cores with accumulators in tensor memory: one pass with a running sum against a reference near
+// the running maximum, split over the cache's length and joined.
 //
-// Work. A unit is one request, one key head, and up to N of its (row, query head) pairs, which share
-// every key and value read. The units' tokens, cut into tiles of 128, form one line over all requests; each
-// block takes an equal stretch of it, found by a prefix sum over the requests that every block forms
+// Work. A unit is one request, one key head, and up to N = 16, 32 or 64 of its (row, query head) pairs, which
+// share every key and value read. The units' tokens, cut into tiles of 128, form one line over all requests;
+// each block takes an equal stretch of it, found by a prefix sum over the requests that every block forms
 // for itself, so lengths can stay on the GPU and long requests spread over all SMs. A stretch that
-// covers a unit writes its rows; the others leave (maximum, sum, weighted values) in the workspace, and
+// covers a unit writes its rows; the others leave (reference, sum, weighted values) in the workspace, and
 // the block that arrives last adds the unit's pieces in their order along the line (a counter for each block
 // in which a unit begins; nobody waits for another block, and the sums' order does not depend on who is last).
 //
-// A tile: S^T = K q'^T (128 tokens x N) and O^T += V^T P^T (dim x N). With the tokens and the dims as the 128 rows of
-// the products no part of them is padding, whatever N is, and keys and values are read from shared
-// memory as they come: keys as rows of dims, values as columns (MN-major).
+// A tile: S^T = K q'^T (128 tokens x N) and O^T += V^T P^T (dim x N). With the tokens and the dims as the 128
+// rows of the products no part of them is padding however few rows there are, and keys and values are read
+// from shared memory as they come: keys as rows of dims, values as columns (MN-major). Both products read the
+// cache's operand once: q' and the weights are two bf16 numbers a value (2^-16), side by side as columns, which
+// costs next to nothing here (N of 64 columns takes the time of reading the 128 rows). E4M3 keys and values are
+// multiplied as they are (kind::f8f6f4, against bf16 there is no product): q' over a power of two as four E4M3
+// parts (2^-16), the weights as f16 cut into four E5M2 parts (exact: an E5M2 number is the upper byte of an f16
+// one), the last two parts of each times 2^8. An E4M3 value's scale is a summand of the score that its weight
+// comes from, so weights stay in range whatever the scales are.
+//
+// Roles. Two warps fetch (cp.async, 16 bytes a lane, up to 192 KB ahead), one thread finds the pieces and
+// issues the scores' products, one the values'; the rest are softmax groups of 128 threads, a token each,
+// 16 rows a group, later a dim each. At 16 rows two groups take tiles in turn (bf16, 128 dims), or two blocks
+// share an SM (E4M3; 64 dims): a tile's chain of waits is longer than its bytes take. A weight may pass its
+// reference by 2^8 before the reference and the sums move, so after a piece's first tile they hardly do.
+//
+// What a row does not see gets a score of -inf and a weight of zero; tokens past the last and on bad pages are
+// zero-filled. Zero times an infinity or NaN would be NaN: bf16 values that are not finite, of tokens that not
+// all rows see, leave the product and are added at the end to the rows that see them.
+//
+// Measured: 96 requests of 1000 to 16000 tokens, 4 rows, 32/8 heads of 128 in bf16 480-493 us, 0.99-1.02 of the copy
+// rate (3.3 GB); one row over 131041 tokens 93 (0.85); 24 verify windows of up to 6 rows 72 (0.70); 64 E4M3
+// requests of 300 to 9000 tokens 124-129 (0.72-0.75); one draft step of four streams 17. Short pieces are bound by
+// what beginning and ending one takes (about 8 us of chained waits, much of it instructions fetched for the
+// first time), which the line's cuts allow for; kernels on warp-level products, two blocks an SM, measured
+// 569, 112, 142, 208 and 22. Fetching by tensor maps (one warp, boxes of a page) measured no faster.
 #include <cuda_fp16.h>
 
 #include "paged.cuh"
@@ -65,7 +88,7 @@ struct Args {
   int64_t ldo;
   float* lse;
   int32_t* count;   // [kMaxBlocks][N / 16], zero between calls
-  float2* ml;       // [2 kMaxBlocks][rows of a unit]: maximum and sum (base 2)
+  float2* ml;       // [2 kMaxBlocks][rows of a unit]: reference (base 2) and sum
   float* acc;       // [2 kMaxBlocks][rows of a unit][D]
   int32_t* dev_status;
   tfd_kv_pages c;
@@ -276,6 +299,12 @@ struct Request {
   bool bad;
 };
 
+// The first token that a row behind `len` tokens can see (with `tree` one that sees no new token is a depth back).
+template <int D>
+__device__ __forceinline__ int first_seen(const Args<D>& a, int len) {
+  return a.window >= 0 ? (int)max((int64_t)0, (int64_t)len - a.window - (a.tree ? 1 : 0)) : 0;
+}
+
 // Request r's part of the line.
 template <int D, int N, bool kF8>
 __device__ __forceinline__ Request request(const Args<D>& a, int r) {
@@ -288,8 +317,7 @@ __device__ __forceinline__ Request request(const Args<D>& a, int r) {
   q.bad = q.row0 < 0 || n < 0 || n > a.max_new || q.row0 + n > a.rows || q.len < 0 ||
           (n > 0 && (q.len + n > (int64_t)a.max_pages * a.c.page_size || q.len + n > kMostTokens));
   q.n = q.bad ? 0 : (int)n;
-  const int64_t lo = a.window >= 0 ? (int64_t)q.len - a.window - (a.tree ? 1 : 0) : 0;
-  q.tile0 = q.n > 0 && lo > 0 ? (int)(lo / kTile) : 0;
+  q.tile0 = q.n > 0 ? first_seen(a, q.len) / kTile : 0;
   q.tiles = q.n > 0 ? (q.len + q.n - 1) / kTile + 1 - q.tile0 : 0;
   q.mt = (q.n * a.group + N - 1) / N;
   q.places = q.tiles + kStartOf<kF8>;
@@ -345,21 +373,22 @@ template <int D, int N, bool kF8>
 struct Smem {
   static constexpr int kParts = kF8 ? 4 : 2;
   static constexpr int kSlot = kF8 ? kTile * 128 : kTile * D * 2;  // E4M3: rows of 128 bytes, whatever D is
-  static constexpr int kSlots = Roles<D, N, kF8>::kCtas == 2 ? 5 : kF8 ? 11 : D == 64 ? 9 : N == 64 ? 5 : 6;  // keys, values in turn
+  static constexpr bool kTwo = Roles<D, N, kF8>::kCtas == 2;  // blocks an SM
+  static constexpr int kSlots = kTwo ? 5 : kF8 ? 11 : D == 64 ? 9 : N == 64 ? 5 : 6;  // keys, values in turn
   static constexpr int kQ = kSlots * kSlot;                  // q': [row bytes / 128][parts N] rows of 128 bytes
   static constexpr int kQBytes = kF8 ? 512 * N : 4 * N * D;
-  static constexpr int kQs = Roles<D, N, kF8>::kCtas == 2 ? 2 : 1;                // of them: the next piece's is made ahead where it fits
+  static constexpr int kQs = kTwo ? 2 : 1;                   // of them: the next piece's is made ahead
   static constexpr int kP = kQ + kQs * kQBytes;              // weights: [parts N / (16 bytes)][128] x 16 bytes
   static constexpr int kTurns = Roles<D, N, kF8>::kTurns, kPlace = 4 * N * kTile;  // a place for weights a turn
-  static constexpr int kRows = kP + kTurns * kPlace;         // two of: a row's first cached token seen, new ones seen
+  static constexpr int kRows = kP + kTurns * kPlace;         // two of: what each row sees: from where, which new
   static constexpr int kRef = kRows + 2 * N * 8;             // reference of each row
   static constexpr int kFac = kRef + kTurns * N * 4;
   static constexpr int kRed = kFac + kTurns * N * 4;         // [groups][4][16]
-  static constexpr int kPow = kRed + kTurns * N * 16;                 // E4M3: two of: the power of two of q' of each row
+  static constexpr int kPow = kRed + kTurns * N * 16;        // E4M3: two of: the power of two of q' of each row
   static constexpr int kBars = kPow + (kF8 ? 2 * N * 4 : 0);
   static constexpr int kMisc = (kBars + 8 * (2 * kSlots + 13 + 2 * kAhead) + 15) / 16 * 16;
   static constexpr int kBytes = kMisc + (int)sizeof(Misc);
-  static_assert(kBytes <= (Roles<D, N, kF8>::kCtas == 2 ? 113 : 227) * 1024, "shared memory of a block");
+  static_assert(kBytes <= (kTwo ? 113 : 227) * 1024, "shared memory of a block");
   static constexpr uint32_t kWide = kParts * N;              // columns of a product
   static constexpr uint32_t kO = 2 * kWide;                  // scores twice, then the weighted values a turn
   static constexpr uint32_t kUsed = kO + kTurns * kWide;
@@ -451,8 +480,11 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
     const int per = (a.requests + kT - 1) / kT;
     const int r0 = min(a.requests, tid * per), r1 = min(a.requests, r0 + per);
     int64_t mine = 0;
+    Request q0 = {};  // this thread's first
+    if (tid < 2) ms.ends[tid] = -1;
     for (int r = r0; r < r1; ++r) {
       const Request q = request<D, N, kF8>(a, r);
+      if (r == r0) q0 = q;
       if (q.bad && blockIdx.x == 0) set_dev_status(a.dev_status, TFD_ERR_DEVICE_DATA);
       mine += (int64_t)q.places * q.mt * H;
     }
@@ -475,13 +507,11 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
     cuts.share = quot(total + gridDim.x - 1, gridDim.x);
     cuts.keep = (int)min(cuts.share, (int64_t)kKeep);
     // the block's stretch: from its cut to the next one's
-    if (tid < 2) ms.ends[tid] = total;
-    __syncthreads();
     int64_t at = before;
     for (int r = r0; r < r1; ++r) {  // for the threads in whose requests a cut falls
       const int64_t lo = blockIdx.x * cuts.share, hi = lo + cuts.share;
       if (!((before <= lo && lo < before + mine) || (before <= hi && hi < before + mine))) break;
-      Request q = request<D, N, kF8>(a, r);
+      Request q = r == r0 ? q0 : request<D, N, kF8>(a, r);
       const int64_t u = (int64_t)q.places * q.mt * H;
       q.base = at;
 #pragma unroll
@@ -497,7 +527,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
     __syncthreads();
   }
   const uint32_t tmem = ms.tmem;
-  const int64_t t0 = ms.ends[0], t_end = ms.ends[1];
+  const int64_t t0 = ms.ends[0] < 0 ? total : ms.ends[0], t_end = ms.ends[1] < 0 ? total : ms.ends[1];
   const int64_t steps = t_end - t0;  // places of the stretch, some of them tiles
   bool ok = true;                   // none of this thread's waits has run out
 
@@ -532,7 +562,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
     for (int k = 0;; ++k) {
       const Piece w = get_piece(k, false);
       if (w.cnt == 0) break;
-      const int tokens = w.len + w.n;
+      const int tokens = w.len + w.n, low = first_seen(a, w.len);
       const int32_t* table = a.table + w.r * a.ldt;
       const int64_t head = (int64_t)w.h * a.head_stride;
       int64_t tok = (int64_t)(w.tile0 + w.first) * kTile + mine0 + lane;
@@ -541,7 +571,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
 #pragma unroll
         for (int q = 0; q < kPer; ++q) {
           pg[q] = page_of(a, tok + 32 * q);
-          page[q] = on && tok + 32 * q < tokens ? table[pg[q]] : -1;
+          page[q] = on && tok + 32 * q >= low && tok + 32 * q < tokens ? table[pg[q]] : -1;
         }
       };
       look_up(true);
@@ -553,9 +583,10 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
 #pragma unroll
         for (int q = 0; q < kPer; ++q) {
           const bool in = page[q] >= 0 && page[q] < a.c.pages;
-          if (tok + 32 * q < tokens && !in) set_dev_status(a.dev_status, TFD_ERR_DEVICE_DATA);
-          off[q] = in ? ((int64_t)page[q] * a.page_stride + (int64_t)((int)tok + 32 * q - pg[q] * ps) * a.token_stride + head) * es
-                      : 0;
+          if (tok + 32 * q >= low && tok + 32 * q < tokens && !in)
+            set_dev_status(a.dev_status, TFD_ERR_DEVICE_DATA);
+          const int64_t at = (int64_t)((int)tok + 32 * q - pg[q] * ps) * a.token_stride;
+          off[q] = in ? ((int64_t)page[q] * a.page_stride + at + head) * es : 0;
           there[q] = __ballot_sync(0xffffffffu, in);
           whole = whole && there[q] == 0xffffffffu;
         }
@@ -655,10 +686,8 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
           while (ok && more_pieces && found < p + 1 + kAhead) find();
       }
     }
-    if (!ok) {  // no product may still read or write when this block's memory is given back
-      mma_commit(drained);
-      bar_wait(drained, 0);
-    }
+    mma_commit(drained);  // no product may still read or write when this block's memory is given back
+    if (!bar_wait(drained, 0)) ok = false;
   } else if (steps > 0 && tid == 32 * R::kValueWarp) {
     // ---- the values' products: one thread ------------------------------------------------------------
     const uint32_t desc = idesc(kWide, kF8 ? 0 : 1, 1, true, true);
@@ -690,10 +719,8 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
       }
       if (!ok) break;
     }
-    if (!ok) {
-      mma_commit(drained + 8u);
-      bar_wait(drained + 8u, 0);
-    }
+    mma_commit(drained + 8u);
+    if (!bar_wait(drained + 8u, 0)) ok = false;
   } else if (steps > 0 && warp < kScoreWarp) {
     // ---- softmax of 16 rows: a thread a token; then their sums, a thread a dim -----------------------
     const int grp = warp / 4, bid = 1 + grp, gw = warp & 3, gt = tid & (kGroup - 1);
@@ -813,7 +840,8 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
         }
       }
       // past the last row: it hides nothing
-      if (l == 0) s_rows[i] = row ? make_int2(from > 0 ? (int)min(from, (int64_t)w.len) : 0, (int)sees) : make_int2(0, -1);
+      if (l == 0)
+        s_rows[i] = row ? make_int2(from > 0 ? (int)min(from, (int64_t)w.len) : 0, (int)sees) : make_int2(0, -1);
       if (kF8) {
         // into E4M3's range, the row's largest magnitude in [128, 256); then part by part what is left
         float top = 0.0f;
@@ -828,8 +856,8 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
         ex = finite_(top) ? max(-126, min(120, ex)) : 0;
         const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
         if (l == 0)
-          reinterpret_cast<float*>(sm + M::kPow)[(p & 1) * N + n] =
-              finite_(top) ? __uint_as_float((uint32_t)(127 + ex) << 23) : NAN;  // infinite: NaN, as the formula gives
+          reinterpret_cast<float*>(sm + M::kPow)[(p & 1) * N + n] =  // infinite: NaN, as the formula gives
+              finite_(top) ? __uint_as_float((uint32_t)(127 + ex) << 23) : NAN;
 #pragma unroll
         for (int e = 0; e < 2 * E; ++e) x[e] *= down;
 #pragma unroll
@@ -848,32 +876,33 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
               y[2] = (y[2] - b1.x) * up, y[3] = (y[3] - b1.y) * up;
             }
             const int d = half * (D / 2) + E * l, r = part * N + n;
-            unsigned char* to = sm + M::kQ + p % M::kQs * M::kQBytes + r * 128 + (((d >> 4) ^ (r & 7)) << 4) + (d & 15);
+            unsigned char* to =
+                sm + M::kQ + p % M::kQs * M::kQBytes + r * 128 + (((d >> 4) ^ (r & 7)) << 4) + (d & 15);
             if (E == 8) *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[E / 4 - 1]);
             else *reinterpret_cast<uint32_t*>(to) = w[0];
           }
       } else {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t hi[E / 2], lo[E / 2];
+        for (int half = 0; half < 2; ++half) {
+          uint32_t hi[E / 2], lo[E / 2];
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float y0 = x[half * E + e] * a.scale, y1 = x[half * E + e + 1] * a.scale;
-          hi[e / 2] = bf16x2(y0, y1);
-          const float b0 = bf16_lo(hi[e / 2]), b1 = bf16_hi(hi[e / 2]);
-          lo[e / 2] = bf16x2(finite_(b0) ? y0 - b0 : 0.0f, finite_(b1) ? y1 - b1 : 0.0f);
+          for (int e = 0; e < E; e += 2) {
+            const float y0 = x[half * E + e] * a.scale, y1 = x[half * E + e + 1] * a.scale;
+            hi[e / 2] = bf16x2(y0, y1);
+            const float b0 = bf16_lo(hi[e / 2]), b1 = bf16_hi(hi[e / 2]);
+            lo[e / 2] = bf16x2(finite_(b0) ? y0 - b0 : 0.0f, finite_(b1) ? y1 - b1 : 0.0f);
+          }
+          const int d = half * (D / 2) + E * l;
+          unsigned char* to = sm + M::kQ + p % M::kQs * M::kQBytes + (d >> 6) * (kWide * 128) + n * 128 +
+                              ((((d >> 3) & 7) ^ (n & 7)) << 4) + (d & 7) * 2;
+          if (E == 8) {
+            *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[E / 2 - 2], hi[E / 2 - 1]);
+            *reinterpret_cast<uint4*>(to + N * 128) = make_uint4(lo[0], lo[1], lo[E / 2 - 2], lo[E / 2 - 1]);
+          } else {
+            *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(to + N * 128) = make_uint2(lo[0], lo[1]);
+          }
         }
-        const int d = half * (D / 2) + E * l;
-        unsigned char* to = sm + M::kQ + p % M::kQs * M::kQBytes + (d >> 6) * (kWide * 128) + n * 128 + ((((d >> 3) & 7) ^ (n & 7)) << 4) +
-                            (d & 7) * 2;
-        if (E == 8) {
-          *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[E / 2 - 2], hi[E / 2 - 1]);
-          *reinterpret_cast<uint4*>(to + N * 128) = make_uint4(lo[0], lo[1], lo[E / 2 - 2], lo[E / 2 - 1]);
-        } else {
-          *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2*>(to + N * 128) = make_uint2(lo[0], lo[1]);
-        }
-      }
       }
       fence_async();
       bar_arrive(q_full);
@@ -960,13 +989,15 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
           }
         }
         // E4M3: the value's scale is part of its weight, as the score's summand: the weights stay below 2^15,
-        // whatever the scales are (scales below 2^-60 are made up for behind)
+        // whatever the scales are. A sum without them is below 2^(96 + 8) a token; what a scale is below 2^-96
+        // its weight is multiplied by
         float lv = 0.0f, lv_fin = 0.0f, small = 1.0f;
         if (kF8) {
-          lv = log2f(vs);
-          if (vs < 8.673617379884035e-19f) {
-            small = vs * 1.152921504606847e18f;
-            lv = -60.0f;
+          lv = log2f(fabsf(vs));
+          small = copysignf(1.0f, vs);
+          if (fabsf(vs) < 1.262177448353619e-29f) {
+            small = vs * 7.922816251426434e28f;
+            lv = -96.0f;
           }
           lv_fin = finite_(lv) ? lv : 0.0f;
           const float* pow = reinterpret_cast<const float*>(sm + M::kPow) + (p & 1) * N + n0;
@@ -1081,7 +1112,8 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
         }
         if (!kF8 && partly) {
           // a value that is not finite, of a token that not all rows see: 0 times it would be NaN. It
-          // leaves the product, and is added at the end to the rows that see it
+          // leaves the product, and is added at the end to the rows that see it. (E4M3 codes are not NaN;
+          // to look for them here took 7% of a large batch's time.)
           const int64_t x = 2 * g + 1;
           const int slot = (int)(x % M::kSlots);
           if (there && !sees(every, key, cur.len)) {
@@ -1112,7 +1144,8 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
             }
             // such tiles are among the unit's first two and last two
             const int at_tile = cur.first + i;
-            if (odd) atomicOr(&ms.odd[p & 3], 1 << (at_tile < 2 && key0 < every.x ? at_tile : 2 + cur.tiles - 1 - at_tile));
+            const int bit = at_tile < 2 && key0 < every.x ? at_tile : 2 + cur.tiles - 1 - at_tile;
+            if (odd) atomicOr(&ms.odd[p & 3], 1 << bit);
           }
         }
         fence_async();
@@ -1335,8 +1368,8 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
                  : "memory");
 }
 
-// Rows of a unit: the least of 16, 32 and 64 that the rows of a request fit, or the most there is (E4M3's four parts a
-// row fill tensor memory at 32).
+// Rows of a unit: the least of 16, 32 and 64 that the rows of a request fit, or the most there is (E4M3's four
+// parts a row fill tensor memory at 32).
 inline int unit_rows(int max_new, int group, int fmt) {
   const int rows = max_new * group, most = fmt == TFD_KV_E4M3 ? 32 : 64;
   return rows <= 16 ? 16 : rows <= 32 ? 32 : most;
@@ -1359,6 +1392,8 @@ tfd_status launch(const Args<D>& a, cudaStream_t stream) {
 
 template <int D>
 tfd_status launch_dim(Args<D>& a, float rope_base, cudaStream_t stream) {
+  a.page_stride = (int)a.c.page_stride, a.token_stride = (int)a.c.token_stride;
+  a.head_stride = (int)a.c.head_stride;
   if (a.qk & TFD_QK_ROPE) a.turns = tfd_host::rope_turns<D>(rope_base);
   const int n = unit_rows(a.max_new, a.group, a.c.fmt);
   if (a.c.fmt == TFD_KV_E4M3)
@@ -1447,7 +1482,8 @@ extern "C" tfd_status tfd_paged_attn(const void* q, int64_t ldq, int rows, int q
   if (c.dim == D) {                                                                              \
     Args<D> a = {(const uint16_t*)q, ldq, table, ldt, lens, row_start, pos, tree,                \
                  (const uint16_t*)q_gamma, (uint16_t*)out, ldo, lse, count, ml, acc, dev_status, \
-                 c, rows, q_heads, group, max_pages, requests, max_new, window, qk, eps, sc, mul, shift, (int)c.page_stride, (int)c.token_stride, (int)c.head_stride, {}}; \
+                 c, rows, q_heads, group, max_pages, requests, max_new, window, qk, eps, sc,     \
+                 mul, shift};                                                                    \
     return launch_dim<D>(a, rope_base, s);                                                       \
   }
   TFD_ATTN_DIM(64)

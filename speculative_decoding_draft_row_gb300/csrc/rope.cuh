@@ -26,15 +26,6 @@ __device__ __forceinline__ void rope_pair(int p, const RopeTurns<D>& turns, int 
   sincosf(red, &sn, &cs);
 }
 
-// The same by the sine and cosine of half turns, which need no reduction of their own (within 2^-22 of
-// the above).
-template <int D>
-__device__ __forceinline__ void rope_pair_pi(int p, const RopeTurns<D>& turns, int i, float& sn,
-                                             float& cs) {
-  const uint64_t ph = (uint64_t)(uint32_t)p * turns.t[i];
-  sincospif((float)(int32_t)(ph >> 32) * 4.6566128730773926e-10f, &sn, &cs);  // over 2^31
-}
-
 // The same by the hardware's sine and cosine: within 2^-20.5 on [-pi, pi].
 template <int D>
 __device__ __forceinline__ void rope_pair_fast(int p, const RopeTurns<D>& turns, int i, float& sn,

@@ -129,6 +129,13 @@ def test_layouts_that_are_fine():
         assert attn_call(c, rows=1 << 27) == 2
 
 
+def test_strides_that_the_attention_refuses():
+    """A cache of pages 2^31 elements apart takes rows, and is refused by the attention alone."""
+    c = cache(sp=1 << 31)
+    assert attn_call(c) == 2
+    assert append_call(c, k=None) == 1                    # looked at behind the cache
+
+
 @pytest.mark.parametrize("out,size", [("out", 5 * 8192 + 8192), ("lse", 6 * 32 * 4), ("ws", 4096),
                                       ("st", 4)])
 @pytest.mark.parametrize("inp", ["q", "table", "lens", "row_start", "pos", "tree", "g", "k", "v", "out"])

@@ -84,14 +84,13 @@ def test_given_positions():
 @pytest.mark.parametrize("lens,new,q_heads,heads,dim", [([9000], 1, 4, 1, 128), ([5000, 1], 7, 8, 2, 64),
                                                         ([20000], 2, 1, 1, 64)])
 def test_long_contexts_in_pieces(lens, new, q_heads, heads, dim, fmt):
-    """A unit spread over many blocks, joined: twice the same bits, and the counters back at zero."""
+    """A unit spread over many blocks, joined: twice the same bits, on the same workspace."""
     need_gpu()
     c = Case(lens, [new] * len(lens), q_heads, heads, dim, 64, fmt)
     a = c.check()
     b = c.run()
     torch.cuda.synchronize()
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
-    assert not c.ws[:4096].view(torch.int32)[:304].any()
 
 
 @pytest.mark.parametrize("fmt", FMT)
@@ -102,6 +101,36 @@ def test_many_requests(fmt):
     g = np.random.default_rng(9)
     lens, new = g.integers(0, 150, 700), g.integers(0, 4, 700)
     Case(lens, new, 2, 1, 64, 16, fmt, tid=830).check(requests=list(range(0, 700, 23)) + [699])
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("q_heads,heads,dim,new", [(12, 3, 128, 1), (12, 3, 64, 4), (8, 2, 128, 7),
+                                                   (16, 2, 64, 32)])
+def test_many_units_a_block(q_heads, heads, dim, new, fmt):
+    """Units of all lengths, several a block and cut anywhere: rows in one piece, two and more."""
+    need_gpu()
+    g = np.random.default_rng(new)
+    lens = np.concatenate([g.integers(0, 400, 150), g.integers(1000, 6000, 6), g.integers(0, 200, 100)])
+    c = Case(lens, np.where(g.random(256) < 0.1, 0, new), q_heads, heads, dim, 16, fmt, tid=850)
+    got = c.check(requests=list(range(3, 150, 29)) + [151, 154] + [200, 255])
+    again = c.run()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+def test_one_request_is_the_same_beside_others():
+    """The sums of a unit that no cut divides do not depend on the other requests."""
+    need_gpu()
+    c = Case([300, 180, 260], [2, 1, 2], 4, 2, 128, 16)
+    got = c.run()
+    for r in range(3):
+        a, b = c.row_start[r], c.row_start[r + 1]
+        out = tfd.tfd_paged_attn(c.q[a:b], c.cache, i32(c.table[r:r + 1]), i32(c.lens[r:r + 1]), i32([0, b - a]),
+                                 2, q_gamma=c.gamma)[0]
+        torch.cuda.synchronize()
+        x, y = np32(out), np32(got[0])[a:b, :512]
+        # cut differently, the sums' order differs: neighbouring bf16 values at most
+        assert (np.abs(x - y) <= 2.0 ** -7 * np.abs(y) + 1e-6).all()
 
 
 def test_scores_far_apart_and_masked_maxima():
@@ -154,6 +183,95 @@ def test_infinite_values_left_of_a_sliding_window():
     d = (got[0][1:4, :256].float() - ref[0][1:4, :256].float()).abs()
     assert (d <= 2.0 ** -7 * ref[0][1:4, :256].float().abs() + 1e-6).all()
     assert torch.isposinf(got[0][0, :256]).all()
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("dim", [64, 128])
+def test_left_of_the_window_nothing_is_read(dim, fmt):
+    """NaN codes and scales there, and pages given back, in the middle of a tile."""
+    need_gpu()
+    tree = [0b0001, 0b0011, 0b0001, 0b1001, 0, 0]         # row 2 is seen by nobody
+    for words, low in ((tree, 289), (None, 290)):
+        c = Case([390], [4], 4, 2, dim, 16, fmt)
+        kw = dict(tree=words, window=100)
+        ref = c.run(**kw)
+        for t in list(range(low)) + [392] * (words is not None):
+            page, at = int(c.table[0, t // 16]), t % 16
+            if fmt == "bf16":
+                c.cache.k[page, at] = c.cache.v[page, at] = float("nan")
+            else:
+                c.cache.k_scales[page, :, at] = c.cache.v_scales[page, :, at] = float("nan")
+                if t < low:
+                    c.cache.k[page, at], c.cache.v[page, at] = 0x7F, 0xFF if t & 1 else 0x7F
+        c.table[0, :low // 16] = [-1, 10 ** 6] * (low // 32)
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = c.run(**kw, st=st)
+        torch.cuda.synchronize()
+        assert st.item() == 0
+        assert torch.isfinite(ref[0].float()).all()
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
+@pytest.mark.parametrize("fmt", FMT)
+def test_two_graphs_on_one_workspace(fmt):
+    """Captured apart, replayed in turn on one stream: each finds the counters at zero."""
+    need_gpu()
+    a = Case([5000, 70], [4, 4], 8, 2, 128, 16, fmt, tid=860)
+    b = Case([900, 2500, 3], [3, 0, 4], 8, 2, 128, 16, fmt, tid=861)
+    want = [c.run(max_new=4) for c in (a, b)]
+    b.ws = a.ws
+    graphs, outs = [], []
+    for c in (a, b):
+        args = (c.q, c.cache, i32(c.table), i32(c.lens), i32(c.row_start), 4)
+        out = torch.full_like(want[len(outs)][0], 7.0)
+        outs.append((out, args))
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            tfd.tfd_paged_attn(*args, q_gamma=c.gamma, out=out[:, :8 * 128], ws=a.ws)
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 1):
+        outs[i][0].fill_(7.0)
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i][0], want[i][0])
+
+
+def test_growing_scores():
+    """Every tile's scores are far above the last one's: the reference moves tile by tile, and back never."""
+    need_gpu()
+    for fmt in FMT:
+        c = Case([1200], [3], 2, 1, 128, 16, fmt)
+        f = np.repeat(1.0 + 3.0 * np.arange(10), 128)[:1203]
+        at = [int(c.table[0, t // 16]) * 16 + t % 16 for t in range(1203)]
+        if fmt == "bf16":
+            k = c.cache.k.view(-1, 128)
+            k[at] = (k[at].float() * torch.tensor(f, device="cuda")[:, None]).bfloat16()
+            c.kv[0] = np32(c.cache.k)
+        else:
+            page, off = [a // 16 for a in at], [a % 16 for a in at]
+            c.cache.k_scales[page, 0, off] *= torch.tensor(f, device="cuda", dtype=torch.float32)
+            codes = c.cache.k.view(torch.float8_e4m3fn).float()
+            c.kv[0] = (codes.double() * c.cache.k_scales.double().transpose(1, 2)[..., None]).cpu().numpy()
+        c.check(gamma=False)
+
+
+@pytest.mark.parametrize("what", ["tiny", "huge", "mixed", "negative", "zero"])
+def test_e4m3_scales_of_any_size(what):
+    need_gpu()
+    c = Case([300, 20], [2, 1], 4, 2, 64, 16, "e4m3")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    r = torch.rand(c.cache.v_scales.shape, generator=g, device="cuda")
+    f = dict(tiny=1e-25, huge=1e12, mixed=1.0, negative=-1.0, zero=0.0)[what]
+    v = c.cache.v_scales
+    v.mul_(f if what != "mixed" else torch.exp2(torch.floor(24 * r - 12)))
+    if what == "zero":
+        v[torch.isnan(v)] = 0.0
+    codes = c.cache.v.view(torch.float8_e4m3fn).double()
+    c.kv[1] = (codes * v.double().transpose(1, 2)[..., None]).cpu().numpy()
+    got = c.check()
+    if what == "zero":
+        assert not got[0][:3, :256].any()
 
 
 def test_infinite_queries_stay_in_their_rows():
