@@ -8,7 +8,8 @@
 //
 // One cluster; every block forms the prefix sums for itself (12 bytes a request, from L2) and takes its
 // share of the moves and rows, with a cluster barrier between pages given back, pages taken, and rows.
-// Bound by latency: a few dependent reads and, when pages move, three barriers.
+// Bound by latency: a few dependent reads and, when pages move, three barriers (4 requests 4.2 us, 2048 requests
+// with 52000 rows 14.8).
 #include <cooperative_groups.h>
 
 #include "paged.cuh"
