@@ -31,7 +31,7 @@
 // all rows see, leave the product and are added at the end to the rows that see them.
 //
 // Measured: 96 requests of 1000 to 16000 tokens, 4 rows, 32/8 heads of 128 in bf16 480-493 us, 0.99-1.02 of the copy
-// rate (3.3 GB); one row over 131041 tokens 93 (0.85); 24 verify windows of up to 6 rows 72 (0.70); 64 E4M3
+// rate (3.3 GB); one row over 131041 tokens 93 (0.85); 24 verify windows of up to 6 rows 68 (0.74); 64 E4M3
 // requests of 300 to 9000 tokens 124-129 (0.72-0.75); one draft step of four streams 17. Short pieces are bound by
 // what beginning and ending one takes (about 8 us of chained waits, much of it instructions fetched for the
 // first time), which the line's cuts allow for; kernels on warp-level products, two blocks an SM, measured
@@ -48,7 +48,10 @@ constexpr int kTile = 128;                   // tokens of a tile
 constexpr int kCols = 16;                    // rows of a unit that one softmax group takes
 constexpr int kGroup = 128;                  // its threads, one a token; then one a dim
 constexpr int kAhead = 3;                    // pieces found ahead
-constexpr int kKeep = 3;                     // tiles that a unit's end keeps
+// A unit's end keeps its last kKeep tiles, and a unit of fewer than kLeast is not cut: a piece that small costs more,
+// being joined, than it takes off its neighbour (four streams of 5 tiles a head 17.5 us, cut 24; verify windows 67.8,
+// with ends of 3 tiles 70.8, units of fewer than 12 whole 70.6).
+constexpr int kKeep = 1, kLeast = 6;
 // Places on the line that beginning a unit takes, in tiles of its type: its query, its first and last tiles and its
 // sums cost a block about that. The blocks' times even out by it (96 requests: 557 us at 0, 531 at 1, 508 at 3,
 // 479 at 5, 490 at 12; the E4M3 batch 173, 165, 147, 134 and at 8 124).
@@ -345,23 +348,23 @@ struct Misc {
 
 // Cuts of the line, on which a unit of `tiles` takes kStart places and one for each tile. A cut falls every
 // `share` places, but not within `keep` tiles of a unit's ends (there it moves to that end), nor in a unit of
-// fewer than 2 keep: a piece that small costs more, being joined, than it takes off its neighbour.
+// fewer than `least`.
 template <int kStart>
 struct Cuts {
   int64_t share;
-  int keep;
+  int keep, least;
   // the block that has the first tile of the unit that begins at `line0`
   __device__ __forceinline__ int64_t owner(int64_t line0, int tiles) const {
-    return quot(line0 + kStart + (tiles < 2 * keep ? tiles : keep) - 1, share);
+    return quot(line0 + kStart + (tiles < least ? tiles : keep) - 1, share);
   }
   __device__ __forceinline__ int64_t pieces(int64_t line0, int tiles) const {
-    if (tiles < 2 * keep) return 1;
+    if (tiles < least) return 1;
     return quot(line0 + kStart + tiles - keep, share) - owner(line0, tiles) + 1;
   }
   // where the cut at `t`, which lies in the unit, moves to
   __device__ __forceinline__ int64_t moved(int64_t t, int64_t line0, int tiles) const {
     const int64_t at = t - line0 - kStart;
-    if (tiles < 2 * keep || at < keep) return line0;
+    if (tiles < least || at < keep) return line0;
     return at > tiles - keep ? line0 + kStart + tiles : t;
   }
 };
@@ -506,6 +509,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
     }
     cuts.share = quot(total + gridDim.x - 1, gridDim.x);
     cuts.keep = (int)min(cuts.share, (int64_t)kKeep);
+    cuts.least = (int)min(2 * cuts.share, (int64_t)kLeast);
     // the block's stretch: from its cut to the next one's
     int64_t at = before;
     for (int r = r0; r < r1; ++r) {  // for the threads in whose requests a cut falls
