@@ -31,7 +31,7 @@
 // all rows see, leave the product and are added at the end to the rows that see them.
 //
 // Measured: 96 requests of 1000 to 16000 tokens, 4 rows, 32/8 heads of 128 in bf16 480-493 us, 0.99-1.02 of the copy
-// rate (3.3 GB); one row over 131041 tokens 93 (0.85); 24 verify windows of up to 6 rows 68 (0.74); 64 E4M3
+// rate (3.3 GB); one row over 131041 tokens 93 (0.85); 24 verify windows of up to 6 rows 69 (0.73); 64 E4M3
 // requests of 300 to 9000 tokens 124-129 (0.72-0.75); one draft step of four streams 17. Short pieces are bound by
 // what beginning and ending one takes (about 8 us of chained waits, much of it instructions fetched for the
 // first time), which the line's cuts allow for; kernels on warp-level products, two blocks an SM, measured
@@ -1263,26 +1263,50 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
           a.lse[(int64_t)(cur.row0 + cur.j0 + j) * a.q_heads + cur.h * a.group + v - j * a.group] =
               l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
       };
+      // Small units are often nearly empty (a row a head): a thread puts its column where its rows' weights were,
+      // and a short loop takes the rows there are (70 requests of 32 heads 171 us, all 16 written out, and 152 so;
+      // verify windows 72 and 69; 32 rows in E4M3 35 and 38, 64 rows 43 and 45: those write out all)
+      constexpr bool kShort = N == 16 || (N == 32 && !kF8);
+      const int rows_here = min(kCols, cur.valid - n0);
+      auto column = [&](int n) {
+        unsigned char* at = kF8 ? s_p + (n >> 2) * (kTile * 16) + (n & 3) * (D * 4)
+                                : s_p + (n0 >> 3) * (kTile * 16) + (n >> 3) * (2 * N * kTile) + (n & 7) * (D * 4);
+        return reinterpret_cast<float*>(at) + d;
+      };
+      if (kShort && mine) {
+#pragma unroll
+        for (int n = 0; n < kCols; ++n) *column(n) = o[n];
+      }
       if (whole) {
         if (mine) {
           int j = (cur.h0 + n0) / a.group, hq = cur.h0 + n0 - j * a.group;
           uint16_t* to = a.out + (cur.row0 + cur.j0 + j) * a.ldo + (int64_t)(cur.h * a.group + hq) * D + d;
+          auto put = [&](int n, float x) {
+            const float inv = s_fac[n];
+            *to = f32_to_bf16_bits(inv == 0.0f ? 0.0f : x * inv);
+            to += D;
+            if (++hq == a.group) hq = 0, to += a.ldo - (int64_t)a.group * D;
+          };
+          if (kShort) {
+#pragma unroll 1
+            for (int n = 0; n < rows_here; ++n) put(n, *column(n));
+          } else {
 #pragma unroll
-          for (int n = 0; n < kCols; ++n) {
-            if (n0 + n < cur.valid) {
-              const float inv = s_fac[n];
-              *to = f32_to_bf16_bits(inv == 0.0f ? 0.0f : o[n] * inv);
-              to += D;
-              if (++hq == a.group) hq = 0, to += a.ldo - (int64_t)a.group * D;
-            }
+            for (int n = 0; n < kCols; ++n)
+              if (n < rows_here) put(n, o[n]);
           }
         }
         if (gt < kCols && n0 + gt < cur.valid) put_lse(n0 + gt, ref, l);
       } else {
         const int b0 = (int)cuts.owner(cur.line0, cur.tiles), pieces = (int)cuts.pieces(cur.line0, cur.tiles);
+        if (kShort) {
+#pragma unroll 1
+          for (int n = 0; n < rows_here && mine; ++n) __stcg(a.acc + (slot + n0 + n) * D + d, *column(n));
+        } else {
 #pragma unroll
-        for (int n = 0; n < kCols; ++n)
-          if (n0 + n < cur.valid && mine) __stcg(a.acc + (slot + n0 + n) * D + d, o[n]);
+          for (int n = 0; n < kCols; ++n)
+            if (n < rows_here && mine) __stcg(a.acc + (slot + n0 + n) * D + d, o[n]);
+        }
         if (gt < kCols && n0 + gt < cur.valid) __stcg(a.ml + slot + n0 + gt, make_float2(ref, l));
         warps_sync<kGroup>(bid);
         if (gt == 0) {
@@ -1329,6 +1353,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
           warps_sync<kGroup>(bid);
           // several rows a thread at once, 4 dims of each
           constexpr int T = D / 4, kRowsAt = kGroup / T, kEach = kCols / kRowsAt;
+          constexpr int kBatch = (N == 64 ? 8 : 16) / kEach;  // pieces read at once
           const int d4 = gt % T * 4, r0 = gt / T;
           float4 v[kEach];
           float tops[kEach];
@@ -1337,17 +1362,45 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
             v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             tops[u] = s_ref[r0 + u * kRowsAt];
           }
+          // many pieces are read several at once (one row over 55000 tokens 38 us, one by one, and 31 so); for few
+          // the longer loop's instructions take longer to come than its reads (E4M3 batch 127 us and 132)
+          if (pieces <= 4) {
 #pragma unroll 1
-          for (int k = 0; k < pieces; ++k)
+            for (int k = 0; k < pieces; ++k)
 #pragma unroll
-            for (int u = 0; u < kEach; ++u) {
-              const int n = r0 + u * kRowsAt;
-              if (n < mine_n) {
-                const float f = exp2_(__ldcg(a.ml + slot_of(k) + n).x - tops[u]);
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(a.acc + (slot_of(k) + n) * D + d4));
-                v[u].x += f * x.x, v[u].y += f * x.y, v[u].z += f * x.z, v[u].w += f * x.w;
+              for (int u = 0; u < kEach; ++u) {
+                const int n = r0 + u * kRowsAt;
+                if (n < mine_n) {
+                  const float f = exp2_(__ldcg(a.ml + slot_of(k) + n).x - tops[u]);
+                  const float4 x = __ldcg(reinterpret_cast<const float4*>(a.acc + (slot_of(k) + n) * D + d4));
+                  v[u].x += f * x.x, v[u].y += f * x.y, v[u].z += f * x.z, v[u].w += f * x.w;
+                }
               }
+          } else {
+#pragma unroll 1
+            for (int k0 = 0; k0 < pieces; k0 += kBatch) {
+              float f[kBatch][kEach];
+              float4 x[kBatch][kEach];
+#pragma unroll
+              for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+                for (int u = 0; u < kEach; ++u) {
+                  const int n = r0 + u * kRowsAt;
+                  const bool in = k0 + k < pieces && n < mine_n;
+                  f[k][u] = in ? __ldcg(a.ml + slot_of(k0 + k) + n).x : -INFINITY;
+                  x[k][u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                  if (in) x[k][u] = __ldcg(reinterpret_cast<const float4*>(a.acc + (slot_of(k0 + k) + n) * D + d4));
+                }
+#pragma unroll
+              for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+                for (int u = 0; u < kEach; ++u) {
+                  const float e = exp2_(f[k][u] - tops[u]);
+                  v[u].x += e * x[k][u].x, v[u].y += e * x[k][u].y;
+                  v[u].z += e * x[k][u].z, v[u].w += e * x[k][u].w;
+                }
             }
+          }
 #pragma unroll
           for (int u = 0; u < kEach; ++u) {
             const int n = r0 + u * kRowsAt;
@@ -1372,11 +1425,13 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
                  : "memory");
 }
 
-// Rows of a unit: the least of 16, 32 and 64 that the rows of a request fit, or the most there is (E4M3's four
-// parts a row fill tensor memory at 32).
-inline int unit_rows(int max_new, int group, int fmt) {
-  const int rows = max_new * group, most = fmt == TFD_KV_E4M3 ? 32 : 64;
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : most;
+// Rows of a unit: 16 where a request's rows of a key head fit, else 32, or 64 (bf16; E4M3's four parts a row fill
+// tensor memory at 32) where a head has several units of 64, which then read its tokens half as often, and such
+// units are there for half the SMs: 48 requests of 32 rows, 8 query heads a key head, 1034 us and with 32 1202; four
+// such of few tokens 22 and 15, one unit of 40 rows 23 and 14.
+inline int unit_rows(int rows, int fmt, int64_t heads, int sms) {
+  if (rows <= 16) return 16;
+  return fmt == TFD_KV_BF16 && rows > 64 && heads * ((rows + 63) / 64) >= sms / 2 ? 64 : 32;
 }
 
 inline size_t workspace(int rows_of_unit, int dim) {
@@ -1399,7 +1454,8 @@ tfd_status launch_dim(Args<D>& a, float rope_base, cudaStream_t stream) {
   a.page_stride = (int)a.c.page_stride, a.token_stride = (int)a.c.token_stride;
   a.head_stride = (int)a.c.head_stride;
   if (a.qk & TFD_QK_ROPE) a.turns = tfd_host::rope_turns<D>(rope_base);
-  const int n = unit_rows(a.max_new, a.group, a.c.fmt);
+  int dev = 0;
+  const int n = unit_rows(a.max_new * a.group, a.c.fmt, (int64_t)a.requests * a.c.heads, tfd_host::device_sms(dev));
   if (a.c.fmt == TFD_KV_E4M3)
     return n == 16 ? launch<D, 16, true>(a, stream) : launch<D, 32, true>(a, stream);
   return n == 16   ? launch<D, 16, false>(a, stream)
@@ -1413,7 +1469,7 @@ extern "C" size_t tfd_paged_attn_workspace(int max_new, int q_heads, int heads, 
   if (max_new < 1 || max_new > TFD_MAX_ROWS || heads < 1 || heads > 1024 || q_heads < heads ||
       q_heads % heads || q_heads / heads > 64 || (dim != 64 && dim != 128))
     return 0;
-  return workspace(unit_rows(max_new, q_heads / heads, TFD_KV_BF16), dim);
+  return workspace(unit_rows(max_new * (q_heads / heads), TFD_KV_BF16, 1, 0), dim);
 }
 
 extern "C" tfd_status tfd_paged_attn(const void* q, int64_t ldq, int rows, int q_heads,
@@ -1446,7 +1502,8 @@ extern "C" tfd_status tfd_paged_attn(const void* q, int64_t ldq, int rows, int q
       !aligned(lse, 4) || !aligned(dev_status, 4) || !aligned(ws, 16))
     return TFD_ERR_INVALID;
   const int group = q_heads / c.heads;
-  const size_t need = workspace(unit_rows(max_new, group, TFD_KV_BF16), c.dim);
+  const int most_rows = unit_rows(max_new * group, TFD_KV_BF16, 1, 0);  // of a unit, whatever the form
+  const size_t need = workspace(most_rows, c.dim);
   if (!ws || ws_bytes < need) return TFD_ERR_WORKSPACE;
   const struct {
     const void* p;
@@ -1473,7 +1530,7 @@ extern "C" tfd_status tfd_paged_attn(const void* q, int64_t ldq, int rows, int q
   const float sc =
       (float)((scale > 0.0f ? (double)scale : 1.0 / std::sqrt((double)c.dim)) * 1.4426950408889634);
   char* w = (char*)ws;
-  const size_t slots = (size_t)2 * kMaxBlocks * unit_rows(max_new, group, TFD_KV_BF16);
+  const size_t slots = (size_t)2 * kMaxBlocks * most_rows;
   int32_t* count = (int32_t*)w;
   float2* ml = (float2*)(w + kMaxBlocks * 16);
   float* acc = (float*)(w + kMaxBlocks * 16 + slots * 8);

@@ -118,6 +118,16 @@ def test_many_units_a_block(q_heads, heads, dim, new, fmt):
     assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("requests,new,q_heads,heads", [(40, 20, 16, 2), (2, 20, 16, 2), (1, 3, 40, 1), (300, 1, 5, 5)])
+def test_units_of_each_size(requests, new, q_heads, heads, dim):
+    """Many rows a head with and without units for the SMs, one unit of rows between 64 and 128, one row a unit."""
+    need_gpu()
+    g = np.random.default_rng(requests)
+    c = Case(g.integers(100, 600, requests), [new] * requests, q_heads, heads, dim, 16, tid=870)
+    c.check(requests=sorted({0, requests // 2, requests - 1}))
+
+
 def test_one_request_is_the_same_beside_others():
     """The sums of a unit that no cut divides do not depend on the other requests."""
     need_gpu()
