@@ -30,9 +30,9 @@
 // zero-filled. Zero times an infinity or NaN would be NaN: bf16 values that are not finite, of tokens that not
 // all rows see, leave the product and are added at the end to the rows that see them.
 //
-// Measured: 96 requests of 1000 to 16000 tokens, 4 rows, 32/8 heads of 128 in bf16 485-498 us, 0.98-1.00 of the copy
+// Measured: 96 requests of 1000 to 16000 tokens, 4 rows, 32/8 heads of 128 in bf16 498 us, 0.98 of the copy
 // rate (3.3 GB); one row over 131041 tokens 93 (0.85); 24 verify windows of up to 6 rows 69 (0.73); 64 E4M3
-// requests of 300 to 9000 tokens 123-127 (0.73-0.75); one draft step of four streams 17. Short pieces are bound by
+// requests of 300 to 9000 tokens 127 (0.73); one draft step of four streams 17. Short pieces are bound by
 // what beginning and ending one takes (about 8 us of chained waits, much of it instructions fetched for the
 // first time), which the line's cuts allow for; kernels on warp-level products, two blocks an SM, measured
 // 569, 112, 142, 208 and 22. Fetching by tensor maps (one warp, boxes of a page) measured no faster.
