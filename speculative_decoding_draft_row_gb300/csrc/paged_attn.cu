@@ -1200,7 +1200,10 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
           for (int n = 0; n < kCols; ++n) o[n] = fmaf(rest[n], 0.00390625f, o[n]) * 0.0078125f;  // 2^-7
         }
       }
-      if (!kF8 && ms.odd[p & 3]) {
+      // the values that left the products, to the rows that see them: once a piece, after its groups' sums are
+      // over one reference (0 times an infinity is NaN)
+      auto add_odd = [&]() {
+        if (kF8 || !ms.odd[p & 3]) return;
 #pragma unroll 1
         for (int k = 0; k < 4 && mine; ++k) {
           if (!((ms.odd[p & 3] >> k) & 1)) continue;
@@ -1218,7 +1221,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
               if (sees(rows_of(p)[n0 + n], key, cur.len)) o[n] += v;
           }
         }
-      }
+      };
       fence_before();
       bar_arrive(o_empty);
       if (kTurns > 1) {
@@ -1255,6 +1258,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
       } else {
         warps_sync<kGroup>(bid);  // s_fac
       }
+      add_odd();
       const bool whole = cur.cnt == cur.tiles;
       const int64_t slot = (int64_t)(2 * blockIdx.x + (cur.first == 0 ? 1 : 0)) * N;
       auto put_lse = [&](int n, float ref, float l) {

@@ -1,0 +1,77 @@
+"""tfd_paged_attn where values are not ordinary numbers: infinite values that rows see.
+
+Where only some elements of a value vector are infinite, all other elements, and all other rows, come from
+the same products in the same order as without them, so they are equal bit by bit."""
+import numpy as np
+import pytest
+import torch
+
+from helpers import need_gpu
+from paged_cases import Case
+
+pytestmark = pytest.mark.gpu
+
+
+def place(c, r, t):
+    """Page and place in it of request r's token t."""
+    return int(c.table[r, t // c.page]), t % c.page
+
+
+def rows_of(c, got, r):
+    """Request r's outputs [n][q_heads][dim]."""
+    a, b = c.row_start[r], c.row_start[r + 1]
+    return got[0][a:b, :c.q_heads * c.dim].float().cpu().numpy().reshape(b - a, c.q_heads, c.dim)
+
+
+def check_infinite_values(c, r, t, seen_by=None, **kw):
+    """Every third element of token t's values +inf, every third -inf: they reach the rows that see the token
+    (seen_by, or by causal order), and change nothing else."""
+    ref = c.run(**kw)
+    page, at = place(c, r, t)
+    keep = c.cache.v[page, at].clone()
+    c.cache.v[page, at, :, 0::3] = float("inf")
+    c.cache.v[page, at, :, 1::3] = float("-inf")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = c.run(**kw, st=st)
+    torch.cuda.synchronize()
+    c.cache.v[page, at] = keep
+    assert st.item() == 0
+    n, length = int(c.new[r]), int(c.lens[r])
+    want = rows_of(c, ref, r).copy()
+    assert np.isfinite(want).all()
+    for j in range(n) if seen_by is None else seen_by:
+        if seen_by is not None or t <= length + j:
+            want[j, :, 0::3], want[j, :, 1::3] = np.inf, -np.inf
+    x = rows_of(c, got, r)
+    assert np.array_equal(x, want), (t, np.argwhere(x != want)[:4], x[x != want][:4])
+    other = np.ones(c.rows, bool)
+    other[c.row_start[r]:c.row_start[r + 1]] = False
+    assert torch.equal(got[0][other], ref[0][other]) and torch.equal(got[1], ref[1])
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("q_heads,heads", [(4, 1), (2, 2), (8, 1)])
+def test_infinite_values_that_some_rows_see(q_heads, heads, dim):
+    """New tokens on both sides of a tile's end: rows that see one tile, and rows that see two."""
+    need_gpu()
+    c = Case([125, 40], [4, 2], q_heads, heads, dim, 16)
+    for t in (126, 127, 128):
+        check_infinite_values(c, 0, t)
+
+
+@pytest.mark.parametrize("k", [150, 153, 156, 157, 158, 161])
+def test_infinite_values_that_some_rows_see_in_pieces(k):
+    """The same where the unit is cut at several places, with two tiles and more a piece."""
+    need_gpu()
+    c = Case([128 * k + 125], [4], 8, 2, 128, 64)
+    for t in (1, 2, 3):
+        check_infinite_values(c, 0, 128 * k + 125 + t)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_infinite_values_left_of_some_rows_windows(dim):
+    need_gpu()
+    c = Case([140], [4], 4, 1, dim, 16)
+    check_infinite_values(c, 0, 127, seen_by=[0], window=13)
+    check_infinite_values(c, 0, 128, seen_by=[0, 1], window=13)
+    check_infinite_values(c, 0, 129, seen_by=[0, 1, 2], window=13)
