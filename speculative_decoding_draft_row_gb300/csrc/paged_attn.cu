@@ -274,6 +274,12 @@ __device__ __forceinline__ uint32_t mul16x2(uint32_t x, uint32_t y) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
   return r;
 }
+// A product's high and low part. Where the high one is infinite the low one may be the other infinity, or zero
+// times one: NaN, and the sum is the high part's.
+__device__ __forceinline__ float add_low(float high, float low) {
+  const float x = high + low;
+  return x == x ? x : high;
+}
 // The largest of a warp's values (NaN passed over), in all lanes.
 __device__ __forceinline__ float warp_most(float x) {
   float r;
@@ -1188,7 +1194,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
         tmem_ld_wait(o);
         tmem_ld_wait(rest);
 #pragma unroll
-        for (int n = 0; n < kCols; ++n) o[n] += rest[n];
+        for (int n = 0; n < kCols; ++n) o[n] = kF8 ? o[n] + rest[n] : add_low(o[n], rest[n]);
         if (kF8) {
           tmem_ld16(tmem + lanes + o_at + 2 * N + n0, rest);
           tmem_ld_wait(rest);

@@ -75,3 +75,31 @@ def test_infinite_values_left_of_some_rows_windows(dim):
     check_infinite_values(c, 0, 127, seen_by=[0], window=13)
     check_infinite_values(c, 0, 128, seen_by=[0, 1], window=13)
     check_infinite_values(c, 0, 129, seen_by=[0, 1, 2], window=13)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("lens,new,q_heads,heads,tokens", [([0], [1], 1, 1, [0]), ([300], [4], 4, 1, [5, 200, 300]),
+                                                           ([300, 9], [4, 4], 16, 2, [0, 127, 300]),
+                                                           ([9000], [1], 4, 1, [0, 4444, 8999, 9000])])
+def test_infinite_values_that_all_rows_see(lens, new, q_heads, heads, tokens, dim):
+    """The weights enter as two parts, of which the low one is zero or negative: inf times it is not added."""
+    need_gpu()
+    c = Case(lens, new, q_heads, heads, dim, 16)
+    for t in tokens:
+        check_infinite_values(c, 0, t)
+
+
+def many_rows(dim, **kw):
+    """Requests of up to 32 rows of 8 query heads a key head, enough of them for units of 64 rows."""
+    g = np.random.default_rng(dim)
+    new = np.full(24, 32)
+    new[[3, 11, 17]] = 19, 1, 0
+    return Case(g.integers(0, 260, 24), new, 16, 2, dim, 16, tid=880, **kw)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_infinite_values_in_units_of_64_rows(dim):
+    need_gpu()
+    c = many_rows(dim)
+    for r, t in ((0, 0), (5, int(c.lens[5]) + 9), (20, int(c.lens[20]) + 31), (22, int(c.lens[22]))):
+        check_infinite_values(c, r, t)
