@@ -532,6 +532,8 @@ tfd_status tfd_paged_append(const void* k_rows, int64_t ldk, const void* v_rows,
  *   not NaN.
  *   An infinite value that a row sees makes its output infinite as the formula says (NaN where both signs
  *   meet); one whose weight is below 2^-126 of the row's largest makes it infinite or NaN.
+ *   A key with infinite elements likewise: a score of -inf has no weight, and one of +inf, or NaN, makes the row
+ *   and its lse NaN. A row whose scores are all -inf gets zeros and -inf.
  *   Sums and softmax statistics in fp32. q' enters its products as two bf16 parts (E4M3: four 8-bit
  *   parts), within 2^-16 of it; probabilities as two bf16 parts, within 2^-16 (E4M3: as f16, 2^-11;
  *   value scales below 2^-96 lose more of them).

@@ -280,6 +280,12 @@ __device__ __forceinline__ float add_low(float high, float low) {
   const float x = high + low;
   return x == x ? x : high;
 }
+// The largest of three; NaN if one is.
+__device__ __forceinline__ float nan_or_most(float x, float y, float z) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
 // The largest of a warp's values (NaN passed over), in all lanes.
 __device__ __forceinline__ float warp_most(float x) {
   float r;
@@ -992,10 +998,22 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
           if (kF8) tmem_ld_wait(more);
           fence_before();
           bar_arrive(s_empty(b));
+          if (kF8) {
 #pragma unroll
-          for (int n = 0; n < kCols; ++n) {
-            s[n] += rest[n];
-            if (kF8) s[n] = fmaf(more[kF8 ? n : 0] + more[kF8 ? kCols + n : 0], 0.00390625f, s[n]);
+            for (int n = 0; n < kCols; ++n)
+              s[n] = fmaf(more[kF8 ? n : 0] + more[kF8 ? kCols + n : 0], 0.00390625f, s[n] + rest[n]);
+          } else {
+            // as add_low, looking at all sums before any (48 requests of 32 rows 1008 us, each by itself 1021, not at
+            // all 1005; verify windows 69.1, 69.4 and 68.7)
+            float odd = 0.0f;
+#pragma unroll
+            for (int n = 0; n < kCols; n += 2) odd = nan_or_most(odd, rest[n] += s[n], rest[n + 1] += s[n + 1]);
+            if (odd != odd) {
+#pragma unroll
+              for (int n = 0; n < kCols; ++n) rest[n] = rest[n] == rest[n] ? rest[n] : s[n];
+            }
+#pragma unroll
+            for (int n = 0; n < kCols; ++n) s[n] = rest[n];
           }
         }
         // E4M3: the value's scale is part of its weight, as the score's summand: the weights stay below 2^15,

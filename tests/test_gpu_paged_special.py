@@ -1,4 +1,4 @@
-"""tfd_paged_attn where values are not ordinary numbers: infinite values that rows see.
+"""tfd_paged_attn where values are not ordinary numbers: infinite keys and values that rows see.
 
 Where only some elements of a value vector are infinite, all other elements, and all other rows, come from
 the same products in the same order as without them, so they are equal bit by bit."""
@@ -6,7 +6,8 @@ import numpy as np
 import pytest
 import torch
 
-from helpers import need_gpu
+from helpers import assert_bf16_rounding, need_gpu, np32
+from oracle.paged import attend
 from paged_cases import Case
 
 pytestmark = pytest.mark.gpu
@@ -103,3 +104,69 @@ def test_infinite_values_in_units_of_64_rows(dim):
     c = many_rows(dim)
     for r, t in ((0, 0), (5, int(c.lens[5]) + 9), (20, int(c.lens[20]) + 31), (22, int(c.lens[22]))):
         check_infinite_values(c, r, t)
+
+
+def check_infinite_keys(c, r, t):
+    """One element of a cached token's keys infinite: rows and heads whose score is -inf do without the token, in
+    the others it is +inf, and the softmax NaN."""
+    kw = dict(norm=False, rope=False, gamma=False)
+    ref = c.run(**kw)
+    page, at = place(c, r, t)
+    for d, bad in ((0, float("inf")), (c.dim - 1, float("-inf"))):
+        keep = c.cache.k[page, at].clone()
+        c.cache.k[page, at, :, d] = bad
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = c.run(**kw, st=st)
+        torch.cuda.synchronize()
+        c.cache.k[page, at] = keep
+        assert st.item() == 0
+        a, b = c.row_start[r], c.row_start[r + 1]
+        other = np.ones(c.rows, bool)
+        other[a:b] = False
+        assert torch.equal(got[0][other], ref[0][other]) and torch.equal(got[1][other], ref[1][other])
+        q = np32(c.q)[a:b]
+        k, v = (np.delete(x, t, 0) for x in c.tokens(r))
+        sc = 1.0 / np.sqrt(c.dim)
+        y, ls, m = attend(q, k, v, int(c.lens[r]) - 1, scale=sc)
+        without = np.sign(q[:, :, d]) * np.sign(bad) < 0
+        assert without.any() and not without.all()
+        x, l = rows_of(c, got, r), np32(got[1])[a:b]
+        assert np.isnan(x[~without]).all() and np.isnan(l[~without]).all()
+        # the tolerances of paged_cases, for the tokens that are left
+        part, tok = 2.0 ** -16 + 2.0 ** -18, len(k) + 1
+        err = 1.01 * (part * m["dev_a"] + 2.0 ** -20 * m["dev"]) + \
+            (2.0 ** -16 + 2.0 ** -17 + 2.0 ** -23 * tok / 8) * m["abs_out"]
+        assert_bf16_rounding(x[without], y[without], err[without], f"token {t}")
+        lim = 2 * part * m["a"] + 2.0 ** -20 + 2.0 ** -24 * tok + 2.0 ** -23 * np.abs(ls)
+        assert (np.abs(l - ls) <= lim)[without].all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("lens,new,q_heads,heads,tokens", [([2], [4], 4, 1, [0, 1]), ([300], [4], 4, 1, [5, 200]),
+                                                           ([300, 9], [4, 4], 16, 2, [0, 127, 299]),
+                                                           ([9000], [2], 8, 1, [0, 4444])])
+def test_infinite_keys(lens, new, q_heads, heads, tokens, dim):
+    need_gpu()
+    c = Case(lens, new, q_heads, heads, dim, 16)
+    for t in tokens:
+        check_infinite_keys(c, 0, t)
+
+
+def test_infinite_keys_in_units_of_64_rows():
+    need_gpu()
+    c = many_rows(64)
+    r = int(np.argmax(c.lens * (c.new == 32)))
+    for t in (0, int(c.lens[r]) - 1):
+        check_infinite_keys(c, r, t)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("lens", [0, 260])
+def test_rows_whose_scores_are_all_minus_infinity(lens, dim):
+    need_gpu()
+    c = Case([lens], [1], 8, 2, dim, 16)
+    c.cache.k[:, :, :, 3] = float("inf")
+    c.q[0, :, 3] = -c.q[0, :, 3].abs()
+    out, lse = c.run(norm=False, rope=False, gamma=False)
+    torch.cuda.synchronize()
+    assert not out[0, :8 * dim].any() and torch.isneginf(lse[0]).all()
