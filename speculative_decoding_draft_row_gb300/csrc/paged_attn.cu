@@ -18,7 +18,7 @@
 // multiplied as they are (kind::f8f6f4, against bf16 there is no product): q' over a power of two as four E4M3
 // parts (2^-16), the weights as f16 cut into four E5M2 parts (exact: an E5M2 number is the upper byte of an f16
 // one), the last two parts of each times 2^8. An E4M3 value's scale is a summand of the score that its weight
-// comes from, so weights stay in range whatever the scales are.
+// comes from, so weights stay in range; the sum, in which it is not, for scales up to 2^80.
 //
 // Roles. Two warps fetch (cp.async, 16 bytes a lane, up to 192 KB ahead), one thread finds the pieces and
 // issues the scores' products, one the values'; the rest are softmax groups of 128 threads, a token each,
@@ -75,6 +75,9 @@ struct Roles {
 constexpr int kMostTokens = 0x7fffffff - 1024;  // of a request: a tile behind them is still an int
 constexpr int kMaxBlocks = 304;              // blocks of a launch at most
 constexpr float kHead = 8.0f;                // powers of two that a weight may pass its reference by
+// The largest value scale (E4M3). Where scales are 2^L the references are higher by L, and the sum, of probabilities
+// alone, begins at 2^-L: what fp32 drops of it, below 2^-126, is then less than 2^-46 of the largest.
+constexpr float kMostScale = 1.2089258196146292e24f;  // 2^80
 
 template <int D>
 struct Args {
@@ -293,6 +296,10 @@ __device__ __forceinline__ float warp_most(float x) {
   return r;
 }
 __device__ __forceinline__ bool finite_(float x) { return fabsf(x) < INFINITY; }
+// l 2^e, e <= 0, also where 2^e is below fp32's range and l is large.
+__device__ __forceinline__ float lowered(float l, float e) {
+  return l * exp2_(fmaxf(e, -100.0f)) * exp2_(fminf(e + 100.0f, 0.0f));
+}
 
 // A token's place in its request's table.
 template <int D>
@@ -398,7 +405,8 @@ struct Smem {
   static constexpr int kRows = kP + kTurns * kPlace;         // two of: what each row sees: from where, which new
   static constexpr int kRef = kRows + 2 * N * 8;             // reference of each row
   static constexpr int kFac = kRef + kTurns * N * 4;
-  static constexpr int kRed = kFac + kTurns * N * 4;         // [groups][4][16]
+  static constexpr int kFac2 = kFac + kTurns * N * 4;        // E4M3: what a factor is below 2^-100
+  static constexpr int kRed = kFac2 + (kF8 ? N * 4 : 0);    // [groups][4][16]
   static constexpr int kPow = kRed + kTurns * N * 16;        // E4M3: two of: the power of two of q' of each row
   static constexpr int kBars = kPow + (kF8 ? 2 * N * 4 : 0);
   static constexpr int kMisc = (kBars + 8 * (2 * kSlots + 13 + 2 * kAhead) + 15) / 16 * 16;
@@ -744,6 +752,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
     constexpr int kBoth = kTurns * kGroup, kBothId = 8, kSumId = 9;  // barriers of groups that share rows
     float* s_ref = reinterpret_cast<float*>(sm + M::kRef) + grp * kCols;
     float* s_fac = reinterpret_cast<float*>(sm + M::kFac) + grp * kCols;
+    float* s_fac2 = reinterpret_cast<float*>(sm + M::kFac2) + grp * kCols;
     float* s_red = reinterpret_cast<float*>(sm + M::kRed) + 4 * grp * kCols;
     unsigned char* s_p = sm + M::kP + turn * M::kPlace;
     const uint32_t o_at = kO + turn * kWide, lanes = (uint32_t)(32 * gw) << 16;
@@ -1016,12 +1025,11 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
             for (int n = 0; n < kCols; ++n) s[n] = rest[n];
           }
         }
-        // E4M3: the value's scale is part of its weight, as the score's summand: the weights stay below 2^15,
-        // whatever the scales are. A sum without them is below 2^(96 + 8) a token; what a scale is below 2^-96
-        // its weight is multiplied by
+        // E4M3: the value's scale is part of its weight, as the score's summand: the weights stay below 2^15. A sum
+        // without them is below 2^(96 + 8) a token; what a scale is below 2^-96 its weight is multiplied by
         float lv = 0.0f, lv_fin = 0.0f, small = 1.0f;
         if (kF8) {
-          lv = log2f(fabsf(vs));
+          lv = fabsf(vs) <= kMostScale ? log2f(fabsf(vs)) : NAN;  // beyond: NaN for the rows that see it
           small = copysignf(1.0f, vs);
           if (fabsf(vs) < 1.262177448353619e-29f) {
             small = vs * 7.922816251426434e28f;
@@ -1065,7 +1073,10 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
             const float was = s_ref[gt];
             const float x = fmaxf(fmaxf(fmaxf(s_red[gt], s_red[16 + gt]), fmaxf(s_red[32 + gt], s_red[48 + gt])),
                                   was);
-            s_fac[gt] = exp2_(was - x);
+            // E4M3, as two factors: a reference can rise with the values' scales where a sum is large (lowered; all
+            // of that in each thread 131.9 us in a large batch, two factors 129.7, one 127.3)
+            s_fac[gt] = exp2_(kF8 ? fmaxf(was - x, -100.0f) : was - x);
+            if (kF8) s_fac2[gt] = exp2_(fminf(was - x + 100.0f, 0.0f));
             s_ref[gt] = x;
           }
           warps_sync<kGroup>(bid);
@@ -1078,12 +1089,12 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
               tmem_ld16(tmem + lanes + o_at + part * N + n0, o);
               tmem_ld_wait(o);
 #pragma unroll
-              for (int n = 0; n < kCols; ++n) o[n] *= s_fac[n];
+              for (int n = 0; n < kCols; ++n) o[n] *= kF8 ? s_fac[n] * s_fac2[n] : s_fac[n];
               tmem_st16(tmem + lanes + o_at + part * N + n0, o);
             }
             fence_before();
 #pragma unroll
-            for (int n = 0; n < kCols; ++n) sum[n] *= s_fac[n];
+            for (int n = 0; n < kCols; ++n) sum[n] = kF8 ? sum[n] * s_fac[n] * s_fac2[n] : sum[n] * s_fac[n];
           }
         }
 #pragma unroll
@@ -1362,12 +1373,14 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
           if (lane < 16) s_red[gw * 16 + jn] = top;
           warps_sync<kGroup>(bid);
           top = fmaxf(fmaxf(s_red[jn], s_red[16 + jn]), fmaxf(s_red[32 + jn], s_red[48 + jn]));
-          float sums = exp2_(own.x - top) * own.y;
+          // E4M3: references hold the values' scales, so that of a piece with few of the weights can be far above
+          // that of one with many
+          auto over_top = [&](const float2& st) {
+            return kF8 ? lowered(st.y, st.x - top) : exp2_(st.x - top) * st.y;
+          };
+          float sums = over_top(own);
 #pragma unroll 1
-          for (int k = gt / 16 + 8; k < pieces; k += 8) {
-            const float2 st = stat(k);
-            sums += exp2_(st.x - top) * st.y;
-          }
+          for (int k = gt / 16 + 8; k < pieces; k += 8) sums += over_top(stat(k));
           sums += __shfl_xor_sync(0xffffffffu, sums, 16);
           warps_sync<kGroup>(bid);
           if (lane < 16) s_red[gw * 16 + jn] = sums;

@@ -1,4 +1,5 @@
-"""tfd_paged_attn where values are not ordinary numbers: infinite keys and values that rows see.
+"""tfd_paged_attn where values are not ordinary numbers: infinite keys and values that rows see, value scales far
+apart and beyond what is served.
 
 Where only some elements of a value vector are infinite, all other elements, and all other rows, come from
 the same products in the same order as without them, so they are equal bit by bit."""
@@ -170,3 +171,82 @@ def test_rows_whose_scores_are_all_minus_infinity(lens, dim):
     out, lse = c.run(norm=False, rope=False, gamma=False)
     torch.cuda.synchronize()
     assert not out[0, :8 * dim].any() and torch.isneginf(lse[0]).all()
+
+
+def scaled_values(c, f):
+    """Value scales times f [pages][heads][page], also in what the oracle reads."""
+    c.cache.v_scales.mul_(f)
+    codes = c.cache.v.view(torch.float8_e4m3fn).double()
+    c.kv[1] = (codes * c.cache.v_scales.double().transpose(1, 2)[..., None]).cpu().numpy()
+
+
+def by_token(c, exponent):
+    """2^exponent(token) at each token of request 0, 1 elsewhere."""
+    f = torch.ones_like(c.cache.v_scales)
+    for t in range(int(c.lens[0] + c.new[0])):
+        page, at = place(c, 0, t)
+        f[page, :, at] = 2.0 ** exponent(t)
+    return f
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("lens,new,q_heads,heads", [([700], [2], 4, 2), ([600], [6], 8, 1), ([9000], [1], 4, 1)])
+@pytest.mark.parametrize("what", ["rising", "falling", "by turns", "all large"])
+def test_e4m3_scales_far_apart(what, lens, new, q_heads, heads, dim):
+    """From 2^-95 to 2^79.6, tile by tile: what a weight is relative to the largest one is far from what its
+    probability is, and every probability counts in the sum."""
+    need_gpu()
+    c = Case(lens, new, q_heads, heads, dim, 16, "e4m3")
+    n = lens[0]
+    scaled_values(c, by_token(c, {
+        "rising": lambda t: -86 if t < n // 2 else 87, "falling": lambda t: 87 if t < n // 2 else -86,
+        "by turns": lambda t: 87 if t // 128 % 3 == 1 else -86, "all large": lambda t: 87}[what]))
+    c.check()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("bad", [2.0 ** 81, 2.0 ** 112, 2.0 ** 127, -2.0 ** 90, float("inf"), float("nan")])
+def test_e4m3_scales_beyond_what_is_served(bad, dim):
+    """NaN for the rows that see such a value, and for no others."""
+    need_gpu()
+    c = Case([45, 200], [6, 4], 4, 2, dim, 16, "e4m3")
+    ref = c.run()
+    page, at = place(c, 0, 45 + 3)
+    c.cache.v_scales[page, :, at] = bad
+    got = c.run()
+    torch.cuda.synchronize()
+    others = [0, 1, 2, 6, 7, 8, 9]
+    assert torch.equal(got[0][others], ref[0][others]) and torch.equal(got[1][others], ref[1][others])
+    assert torch.isnan(got[0][3:6, :4 * dim]).all() and torch.isnan(got[1][3:6]).all()
+
+
+def test_the_largest_e4m3_scale_that_is_served():
+    """One value scale 2^88 times the others. Weights enter as f16 numbers exp2(s - reference + 7), s with the
+    scale in it and the reference at most the largest s; rounding one is off by at most half of f16's smallest step,
+    2^-25, where it is not by 2^-11 of itself. So beside the tolerances of paged_cases an output may be off by
+    2^-25 2^-7 max_j(p_j s_j) sum_j |code_j|: most of it in elements where that token's code is zero."""
+    need_gpu()
+    c = Case([400], [3], 4, 2, 128, 16, "e4m3")
+    page, at = place(c, 0, 77)
+    f = torch.ones_like(c.cache.v_scales)
+    f[page, :, at] = 2.0 ** 80 / c.cache.v_scales[page, :, at]
+    scaled_values(c, f)
+    assert (c.cache.v_scales[page, :, at] == 2.0 ** 80).all()
+    got = c.run(norm=False, rope=False, gamma=False)
+    torch.cuda.synchronize()
+    k, v = c.tokens(0)
+    q, sc = np32(c.q)[:3].astype(float), 1.0 / np.sqrt(128)
+    t = np.arange(403)
+    scales = np32(c.cache.v_scales)[c.table[0, t // 16], :, t % 16].astype(float)
+    y, ls, m = attend(q, k, v, 400, scale=sc)
+    part = 2.0 ** -16 + 2.0 ** -18
+    err = 1.01 * (part * m["dev_a"] + (2.0 ** -20 + 2.0 ** -23 * m["a_most"][..., None]) * m["dev"]) + \
+        (2.0 ** -11 + 2.0 ** -17 + 2.0 ** -23 * 403 / 8) * m["abs_out"]
+    for j in range(3):
+        for i in range(4):
+            n, h = 401 + j, i // 2
+            p = np.exp(sc * k[:n, h] @ q[j, i] - ls[j, i])
+            err[j, i] += 2.0 ** -32 * (p * scales[:n, h]).max() * np.abs(v[:n, h] / scales[:n, h, None]).sum(0)
+    assert_bf16_rounding(rows_of(c, got, 0), y, err)
+    lim = 2 * part * m["a"] + 2.0 ** -23 * m["a_most"] + 2.0 ** -20 + 2.0 ** -24 * 403 + 2.0 ** -23 * (80 + np.abs(ls))
+    assert (np.abs(np32(got[1])[:3] - ls) <= lim).all()
