@@ -484,7 +484,8 @@ typedef struct {
  *   those of the requests before it, exceed the free ones gets none: it keeps what it holds, the
  *   table entries of the missing pages and its rows' slots and positions become -1); an n_free
  *   outside [0, pages], or more pages given back than the stack has room for (no page moves); a page
- *   id outside [0, pages) (slot -1); more rows than `rows` (those are not written).
+ *   id outside [0, pages) (slot -1; one that a request gives back is left out of the stack); more rows than
+ *   `rows` (those are not written).
  */
 tfd_status tfd_page_plan(const int32_t* lens, const int32_t* n_new, int requests, int page_size,
                          int32_t* table, int64_t ldt, int max_pages, int32_t* held,

@@ -3,8 +3,8 @@
 Oracle (test infrastructure only; see ``oracle/__init__.py``), in float64 and plain loops. The pages keep
 a ring a stream (``attn``, ``layer.absorb``); the paged cache is the library's own, with the same qk_norm,
 RoPE and rounding of keys. Readings:
-* pages given back go on the free stack in the order of requests and pages, the first ending on top;
-  then missing pages come from its top in the same order;
+* pages given back go on the free stack in the order of requests and pages, the first ending on top (ids
+  that are no pages are left out); then missing pages come from its top in the same order;
 * a row sees the cached tokens and the new ones up to itself (or those its tree word names), from its
   own depth minus the window on; a row that sees nothing gives zeros and a log-sum of -inf;
 * E4M3 keys are quantised from the exact key, by the row rule (largest magnitude / 448).
@@ -34,7 +34,7 @@ def plan(lens, n_new, page_size, table, held, free_ids, n_free, rows):
     else:
         given = [int(table[r, p]) for r, p in back]
         bad |= any(not 0 <= i < pages for i in given)
-        stack += given[::-1]                             # the first given back ends on top
+        stack += [i for i in given[::-1] if 0 <= i < pages]  # the first given back ends on top
         free[:len(stack)] = stack
         for r in range(R):
             held[r] = min(held[r], want[r])

@@ -64,11 +64,27 @@ __device__ __forceinline__ int64_t shfl_up64(int64_t v, int d) {
   return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
+// Ids in free_ids[first .. end) that are no pages leave it, the others keep their order: a warp; where they end. A
+// function of its own, as it is hardly ever called (its loop in the kernel: two plans of a large round 30.3 us, so 30.0).
+__device__ __noinline__ int32_t without_none(int32_t* free_ids, int32_t first, int32_t end, int32_t pages) {
+  const int lane = threadIdx.x & 31;
+  int32_t to = first;
+  for (int64_t i = first; i < end; i += 32) {
+    const int32_t id = end - i > lane ? __ldcg(free_ids + i + lane) : -1;
+    const bool in = id >= 0 && id < pages;
+    const uint32_t ins = __ballot_sync(0xffffffffu, in);  // all 32 have been read
+    if (in) free_ids[to + __popc(ins & ((1u << lane) - 1u))] = id;
+    to += __popc(ins);
+  }
+  return to;
+}
+
 template <bool kOne>  // one block
 __global__ void __launch_bounds__(threads_of(kOne)) page_plan_kernel(const Args a) {
   constexpr int kT = threads_of(kOne);
   extern __shared__ int32_t sm[];
   __shared__ int64_t warp_sums[3][kT / 32];
+  __shared__ int32_t s_odd, s_top;  // a block of several met a page that is none; the lead's: the stack without them
   tfd_host::after_previous();
   cg::cluster_group cl = cg::this_cluster();
   const unsigned rank = kOne ? 0 : cl.block_rank(), blocks = kOne ? 1 : cl.num_blocks();
@@ -82,6 +98,7 @@ __global__ void __launch_bounds__(threads_of(kOne)) page_plan_kernel(const Args 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n_free = *a.n_free;
   const bool lead = rank == 0;
+  if (!kOne && tid == 0) s_odd = 0;
   for (int r = tid; r < R; r += kT) {
     const int32_t len = a.lens[r], n = a.n_new[r], held = a.held[r];
     bool b = len < 0 || n < 0 || held < 0 || held > a.max_pages;
@@ -133,21 +150,41 @@ __global__ void __launch_bounds__(threads_of(kOne)) page_plan_kernel(const Args 
   const int32_t back = first[1][R], missing = first[2][R];
   const bool broken = n_free < 0 || n_free > a.pages || (int64_t)n_free + back > a.pages;
   if (broken && lead && tid == 0) set_dev_status(a.dev_status, TFD_ERR_DEVICE_DATA);
-  const int32_t top = broken ? 0 : n_free + back;
+  int32_t top = broken ? 0 : n_free + back;
   // a request gets its pages if all that are missing up to it are there
   auto without = [&](int r) { return first[2][r + 1] > first[2][r] && first[2][r + 1] > top; };
   const int64_t t0 = (int64_t)rank * kT + tid, nt = (int64_t)blocks * kT;
   if (back > 0 || missing > 0) {
+    bool odd = false;  // a page that is none is among those given back
     if (!broken) {
       for (int64_t i = t0; i < back; i += nt) {
         const int r = find(first[1], R, (int32_t)i);
         const int64_t at = pages_of(a.lens[r], a.n_new[r], ps) + (i - first[1][r]);
         const int32_t id = a.table[r * a.ldt + at];
-        if (id < 0 || id >= a.pages) set_dev_status(a.dev_status, TFD_ERR_DEVICE_DATA);
+        if (id < 0 || id >= a.pages) {
+          set_dev_status(a.dev_status, TFD_ERR_DEVICE_DATA);
+          odd = true;
+        }
         a.free_ids[top - 1 - i] = id;
       }
     }
-    sync();  // the stack is complete; every block has read what the requests held
+    // the stack is complete; every block has read what the requests held
+    if (kOne) {
+      odd = __syncthreads_or(odd);
+    } else {
+      if (odd) s_odd = 1;
+      cl.sync();
+      odd = back > 0 && __any_sync(0xffffffffu, lane < (int)blocks && *cl.map_shared_rank(&s_odd, lane));
+    }
+    if (odd) {
+      // ids that are no pages leave the stack, or a sound request would get them; the others keep their order
+      if (lead && warp == 0) {
+        const int32_t to = without_none(a.free_ids, n_free, top, a.pages);
+        if (lane == 0) s_top = to;
+      }
+      sync();
+      top = kOne ? s_top : *cl.map_shared_rank(&s_top, 0);
+    }
     for (int64_t i = t0; i < missing; i += nt) {
       const int r = find(first[2], R, (int32_t)i);
       const int64_t want = pages_of(a.lens[r], a.n_new[r], ps);

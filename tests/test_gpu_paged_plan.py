@@ -157,3 +157,37 @@ def test_captured_and_replayed_on_another_stream():
     for name, t in zip(("table", "held", "free_ids", "n_free", "slots", "pos"),
                        [*s.d, slots, pos]):
         assert np.array_equal(t.cpu().numpy().reshape(-1), np.asarray(ex[name]).reshape(-1)), name
+
+
+@pytest.mark.parametrize("R,page", [(6, 4), (512, 1), (600, 4)])
+def test_pages_that_are_none_do_not_come_back(R, page):
+    """Ids outside the cache in what requests give back are reported and left out of the stack: the pages that are
+    there move as ever, in the same call too, and later requests get pages that are some."""
+    need_gpu()
+    s = State(R, 40, 40 * R, page, seed=R)
+    new = np.full(R, 20)
+    s.round(np.zeros(R, int), new, int(new.sum()))
+    had = s.held.copy()
+    s.table[2, 1], s.table[2, int(had[2]) - 1], s.table[R - 1, 0] = -3, 10 ** 6, 40 * R
+    s.n_free = s.n_free.astype(np.int32)
+    s.on_gpu()
+    lens, new = np.full(R, 20), np.full(R, 10)            # the others grow meanwhile
+    lens[[1, 2, R - 1]], new[[1, 2, R - 1]] = 0, 0
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+    st = i32([0])
+    got = tfd.tfd_page_plan(i32(lens), i32(new), page, *s.d, rows=int(new.sum()), dev_status=st)
+    torch.cuda.synchronize()
+    ex = oracle_plan(lens, new, page, s.table, s.held, s.free, s.n_free[0], int(new.sum()))
+    assert ex["bad"] and st.item() == tfd.ERR_DEVICE_DATA
+    for name, t in zip(("row_start", "slots", "pos"), got):
+        assert np.array_equal(t.cpu().numpy(), ex[name]), name
+    table, held, free, n_free = (t.cpu().numpy() for t in s.d)
+    assert n_free[0] == ex["n_free"]
+    assert np.array_equal(free[:n_free[0]], ex["free_ids"][:n_free[0]])   # what stands behind is of no meaning
+    assert np.array_equal(table, ex["table"]) and np.array_equal(held, ex["held"])
+    s.table[:], s.held, s.free, s.n_free = table, held, free, n_free
+    mine = np.concatenate([free[:n_free[0]]] + [table[r, :held[r]] for r in range(R)])
+    assert len(set(mine.tolist())) == len(mine) == 40 * R - 3 and mine.min() >= 0 and mine.max() < 40 * R
+    s.round(np.zeros(R, int), np.full(R, 37), 37 * R)     # and a round that is sound
+    s.round(np.zeros(R, int), np.zeros(R, int), 0)
+    assert s.n_free[0] == 40 * R - 3

@@ -107,3 +107,14 @@ def test_attend_is_the_ring_oracle():
     np.testing.assert_allclose(y.reshape(1, -1), terms["out_exact"], rtol=1e-12)
     np.testing.assert_allclose(t["abs_out"].reshape(1, -1), terms["abs_out"], rtol=1e-12)
     np.testing.assert_allclose(np.hypot(qt[..., :4], qt[..., 4:]), pair[..., :4], rtol=1e-12)
+
+
+def test_plan_leaves_out_pages_that_are_none():
+    table, held, free, n = fresh(3, 4, 12)
+    p = plan([8, 8, 0], [0, 0, 0], 4, table, held, free, n, 0)
+    t = p["table"]
+    given = t[0, :2].tolist() + t[1, :2].tolist()
+    t[0, 1] = 12
+    q = plan([0, 0, 0], [0, 0, 0], 4, t, p["held"], p["free_ids"], p["n_free"], 0)
+    assert q["bad"] and q["n_free"] == 11 and q["held"].tolist() == [0, 0, 0]
+    assert q["free_ids"][8:11].tolist() == [given[3], given[2], given[0]]
