@@ -558,7 +558,7 @@ tfd_status tfd_paged_append(const void* k_rows, int64_t ldk, const void* v_rows,
  *   TFD_ERR_DEVICE_DATA: a request whose length is negative, whose tokens exceed max_pages or 2^31 -
  *   1025, or whose rows are not 0..max_new rows within `rows` (its rows are left as they were); a
  *   page id outside [0, pages) where a token is read (those tokens are not seen); a negative
- *   position (counts as 0).
+ *   position (counts as 0; positions that no rotation uses are not read).
  *   TFD_ERR_UNSUPPORTED: strides of the cache, or rows * q_heads, from 2^31 on; ldq or ldo above 2^30.
  */
 size_t tfd_paged_attn_workspace(int max_new, int q_heads, int heads, int dim);

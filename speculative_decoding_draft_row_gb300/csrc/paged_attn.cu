@@ -808,7 +808,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
       const int depths = w.len + (a.tree ? __popc(words) - 1 : lane);
       int places = there && a.pos && (a.qk & TFD_QK_ROPE) ? raw_pos : depths;
       if (places < 0) {
-        if (there && a.pos) set_dev_status(a.dev_status, TFD_ERR_DEVICE_DATA);
+        if (there && a.pos && (a.qk & TFD_QK_ROPE)) set_dev_status(a.dev_status, TFD_ERR_DEVICE_DATA);
         places = 0;
       }
       {

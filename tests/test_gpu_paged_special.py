@@ -1,5 +1,5 @@
 """tfd_paged_attn where values are not ordinary numbers: infinite keys and values that rows see, value scales far
-apart and beyond what is served.
+apart and beyond what is served, and what is reported and what is not.
 
 Where only some elements of a value vector are infinite, all other elements, and all other rows, come from
 the same products in the same order as without them, so they are equal bit by bit."""
@@ -10,6 +10,7 @@ import torch
 from helpers import assert_bf16_rounding, need_gpu, np32
 from oracle.paged import attend
 from paged_cases import Case
+from speculative_decoding_draft_row_gb300 import tfd
 
 pytestmark = pytest.mark.gpu
 
@@ -250,3 +251,22 @@ def test_the_largest_e4m3_scale_that_is_served():
     assert_bf16_rounding(rows_of(c, got, 0), y, err)
     lim = 2 * part * m["a"] + 2.0 ** -23 * m["a_most"] + 2.0 ** -20 + 2.0 ** -24 * 403 + 2.0 ** -23 * (80 + np.abs(ls))
     assert (np.abs(np32(got[1])[:3] - ls) <= lim).all()
+
+
+def test_positions_that_no_rotation_uses_are_not_judged():
+    """A row that sees nothing, in a request without tokens: its depth is -1, its position nobody's."""
+    need_gpu()
+    c = Case([0, 30], [3, 2], 2, 1, 64, 16)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kw = dict(tree=[0, 0b010, 0b110, 1, 3, 0, 0], rope=False)
+    ref = c.run(**kw)
+    got = c.run(**kw, pos=[0, 0, 1, 30, 31, 0, 0], st=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+    c.run(**kw, pos=[-1] * 7, st=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    c.run(tree=kw["tree"], pos=[0, 0, 0, -1, 0, 0, 0], st=st)
+    torch.cuda.synchronize()
+    assert st.item() == tfd.ERR_DEVICE_DATA
