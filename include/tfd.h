@@ -529,8 +529,9 @@ tfd_status tfd_paged_append(const void* k_rows, int64_t ldk, const void* v_rows,
  *   row's lens[r] + j, or with `tree` lens[r] + (bits set in its word) - 1. A row that sees nothing
  *   gets zeros and an lse of -inf. What a row does not see (pages not in use, tokens behind the
  *   last, masked ones) may hold anything, NaN too. Tokens before lens[r] - window (with `tree` before
- *   lens[r] - window - 1) are not read, nor their table entries; of E4M3 the codes from there on are
- *   not NaN.
+ *   lens[r] - window - 1) are not read and need no pages: their table entries may hold anything (those of the
+ *   last 127 such tokens may be read, and the E4M3 scales of a page that one names, and say nothing). Of E4M3
+ *   the codes from there on are not NaN.
  *   An infinite value that a row sees makes its output infinite as the formula says (NaN where both signs
  *   meet); one whose weight is below 2^-126 of the row's largest makes it infinite or NaN.
  *   A key with infinite elements likewise: a score of -inf has no weight, and one of +inf, or NaN, makes the row

@@ -960,7 +960,9 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
       const int32_t* table = a.table + cur.r * a.ldt;
       const int i0 = kTurns == 1 ? 0 : (int)((turn + g0) & 1);  // this group's first tile of the piece
       int64_t tok = (int64_t)(cur.tile0 + cur.first + i0) * kTile + gt;
-      auto page_at = [&](int64_t tok, int i) {  // of this thread's token; -1: none
+      // of this thread's token; -1: none. In a unit's first tile also of tokens left of every row's window, whose
+      // entries may name any page: what is read of it is masked (to leave them out here took 4% of an E4M3 batch)
+      auto page_at = [&](int64_t tok, int i) {
         return i < cur.cnt && tok < tokens ? table[page_of(a, tok)] : -1;
       };
       int page = page_at(tok, i0), page_next = page_at(tok + kTurns * kTile, i0 + kTurns);
