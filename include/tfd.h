@@ -500,7 +500,9 @@ tfd_status tfd_page_plan(const int32_t* lens, const int32_t* n_new, int requests
  *     bf16: the cache takes bf16(k') and v_rows[i][h]; E4M3: s = fl32(amax / 448) and
  *     e4m3_rne_sat(fl32(x / s)) of k' (not rounded to bf16 before) and of v_rows[i][h] (amax 0
  *     keeps its zeros).
- *   The normalisation and rotation are those of tfd_window_attn.
+ *   The normalisation is that of tfd_window_attn, and so is the rotation's angle; its sine and cosine are the
+ *   hardware's, within 2^-20.5 (tfd_window_attn and tfd_absorb: fp32 functions, within 2^-23), so keys of the two
+ *   may round to neighbouring values.
  * Args:
  *   k_rows, v_rows device bf16 [rows][heads][dim], row strides ldk, ldv >= heads * dim, multiples
  *            of 8, 16-byte aligned; rows >= 1, rows * heads < 2^31.
@@ -536,7 +538,7 @@ tfd_status tfd_paged_append(const void* k_rows, int64_t ldk, const void* v_rows,
  *   meet); one whose weight is below 2^-126 of the row's largest makes it infinite or NaN.
  *   A key with infinite elements likewise: a score of -inf has no weight, and one of +inf, or NaN, makes the row
  *   and its lse NaN. A row whose scores are all -inf gets zeros and -inf.
- *   Sums and softmax statistics in fp32. q' enters its products as two bf16 parts (E4M3: four 8-bit
+ *   Sums and softmax statistics in fp32, sines and cosines within 2^-20.5. q' enters its products as two bf16 parts (E4M3: four 8-bit
  *   parts), within 2^-16 of it; probabilities as two bf16 parts, within 2^-16. E4M3: a probability times its value's
  *   scale as f16, within 2^-11 of it or 2^-32 of the row's largest (scales below 2^-96 lose more); a scale above
  *   2^80, or NaN, makes the rows that see its token, and their lse, NaN.
