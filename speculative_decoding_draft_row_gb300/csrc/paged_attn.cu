@@ -400,6 +400,7 @@ struct Smem {
   static constexpr int kQ = kSlots * kSlot;                  // q': [row bytes / 128][parts N] rows of 128 bytes
   static constexpr int kQBytes = kF8 ? 512 * N : 4 * N * D;
   static constexpr int kQs = kTwo ? 2 : 1;                   // of them: the next piece's is made ahead
+  static_assert(kQs == 1 || Roles<D, N, kF8>::kTurns == 1, "made after the piece's first tile, which the group has");
   static constexpr int kP = kQ + kQs * kQBytes;              // weights: [parts N / (16 bytes)][128] x 16 bytes
   static constexpr int kTurns = Roles<D, N, kF8>::kTurns, kPlace = 4 * N * kTile;  // a place for weights a turn
   static constexpr int kRows = kP + kTurns * kPlace;         // two of: what each row sees: from where, which new
@@ -1193,7 +1194,6 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
         bar_arrive(p_full(turn));
         if (M::kQs > 1 && i == i0 && next.cnt > 0) prepare(next, p + 1);
       }
-      if (M::kQs > 1 && i0 >= cur.cnt && next.cnt > 0) prepare(next, p + 1);
       g0 += cur.cnt;
 
       // ---- the sums; the next piece's scores can begin meanwhile ---------------------------------------
