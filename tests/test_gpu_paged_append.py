@@ -189,3 +189,19 @@ def test_a_slot_behind_2_to_the_32_elements():
     torch.cuda.synchronize()
     assert torch.equal(k[-1, -1], x[0]) and torch.equal(v[-2, -1], x[1])
     assert not k[0].any() and not v[0].any()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("rows,heads,page,layout", [(4000, 3, 16, "nhd"), (1300, 17, 64, "hnd"), (2500, 8, 24, "both")])
+def test_prompts(rows, heads, page, layout, dim, fmt):
+    """More warps' work than the GPU holds at once: items of four steps, a warp's second one loaded ahead."""
+    need_gpu()
+    run(rows, heads, dim, page, fmt, layout, skip=True, tid=960)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_prompts_as_they_are(fmt):
+    """Without normalisation or rotation, in items of four steps: bf16 keys copied."""
+    need_gpu()
+    run(2500, 8, 128, 16, fmt, norm=False, rope=False, gamma=False, tid=970)
