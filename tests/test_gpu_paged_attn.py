@@ -417,3 +417,55 @@ def test_without_lse_and_allocating():
                                   q_gamma=c.gamma)
     torch.cuda.synchronize()
     assert lse is None and torch.equal(out[:2], ref[0][:2, :256])
+
+
+def of_64_rows(dim, seed=0):
+    """Requests of up to 32 rows of 8 query heads a key head, enough of them for units of 64 rows."""
+    g = np.random.default_rng(seed)
+    new = np.full(24, 32)
+    new[[3, 11, 17]] = 19, 1, 0
+    return Case(g.integers(0, 260, 24), new, 16, 2, dim, 16, tid=880 + seed)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("window", [-1, 2, 40, 300])
+def test_trees_and_windows_in_units_of_64_rows(window, dim):
+    need_gpu()
+    g = np.random.default_rng(6)
+    c = of_64_rows(dim, seed=1)
+    c.lens[8] = 0
+    words = np.zeros(c.rows, np.uint32)
+    for r, n in enumerate(c.new):
+        if n:
+            words[c.row_start[r]:c.row_start[r + 1]] = random_tree(int(n), g)
+    words[c.row_start[5] + 7] = 0                         # sees the cached tokens alone
+    words[c.row_start[8] + 4] = 0                         # nothing cached, nothing seen
+    words[c.row_start[9] + 1] = 1 << 1 | 1 << 30          # itself and a later row
+    got = c.check(tree=words, window=window, requests=[3, 5, 8, 9, 11, 23])
+    row = c.row_start[8] + 4
+    assert not got[0][row, :16 * dim].any() and torch.isneginf(got[1][row]).all()
+    c.check(window=window, requests=[3, 5, 8, 11, 22])
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("what", ["inf", "nan"])
+def test_tokens_that_are_not_finite_in_units_of_64_rows(what, dim):
+    """Edited in a tile by four groups at once; only the rows that see such a token know of it."""
+    need_gpu()
+    c = of_64_rows(dim, seed=2)
+    ref = c.run()
+    for r, j, key in ((5, 9, False), (6, 31, True), (20, 16, True)):
+        t = int(c.lens[r]) + j
+        page, at = int(c.table[r, t // 16]), t % 16
+        keep = c.cache.k[page, at].clone(), c.cache.v[page, at].clone()
+        c.cache.v[page, at] = float(what)
+        if key:
+            c.cache.k[page, at] = float(what)
+        got = c.run()
+        torch.cuda.synchronize()
+        c.cache.k[page, at], c.cache.v[page, at] = keep
+        see = np.zeros(c.rows, bool)
+        see[c.row_start[r] + j:c.row_start[r + 1]] = True
+        assert torch.equal(got[0][~see], ref[0][~see]) and torch.equal(got[1][~see], ref[1][~see])
+        x = got[0][see][:, :16 * dim].float()
+        assert torch.isposinf(x).all() if what == "inf" and not key else torch.isnan(x).all()
