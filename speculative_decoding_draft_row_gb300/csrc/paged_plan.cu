@@ -8,8 +8,8 @@
 //
 // One cluster; every block forms the prefix sums for itself (12 bytes a request, from L2) and takes its
 // share of the moves and rows, with a cluster barrier between pages given back, pages taken, and rows.
-// Bound by latency: a few dependent reads and, when pages move, three barriers (4 requests 4.2 us, 2048 requests
-// with 52000 rows 14.8).
+// Bound by latency: a few dependent reads and, when pages move, three barriers (4 requests 4.3 us, 2048 requests
+// with 52000 rows 15.0).
 #include <cooperative_groups.h>
 
 #include "paged.cuh"
@@ -21,8 +21,8 @@ namespace cg = cooperative_groups;
 
 constexpr int kBlocks = 8;  // blocks of the cluster where there is work for them
 
-// A small round waits for barriers: 256 threads 4.2 us, 512 5.0. A large one has work for all (2048 requests,
-// 52000 rows: 14.8 us; 1024 threads a block 16.1).
+// A small round waits for barriers: with 256 threads it took 4.2 us, with 512 5.0. A large one has work for all (2048
+// requests, 52000 rows: with 512 threads a block 14.8 us, with 1024 16.1). Both before ids that are no pages left the stack.
 constexpr int threads_of(bool one) { return one ? 256 : 512; }
 
 struct Args {
@@ -289,7 +289,13 @@ extern "C" tfd_status tfd_page_plan(const int32_t* lens, const int32_t* n_new, i
                   slots, pos,   dev_status, rows, requests, page_size, max_pages, pages};
   const size_t smem = (size_t)3 * 4 * (requests + 1) + requests;
   const int most = 3 * 4 * (TFD_MAX_REQUESTS + 1) + TFD_MAX_REQUESTS;
-  const int c = requests <= 512 && rows <= 4096 ? 1 : kBlocks;
+  // One block where that is at least as fast, by what the host knows: rows, or without them the pages that can move. One
+  // block and eight, us, no page moved and pages taken and given back in turn: 4 requests x 6 rows 3.4 4.6 | 4.1 6.8;
+  // 32 x 32 4.6 5.3 | 4.2 6.9; 128 x 8 5.1 5.7 | 4.4 6.9; 512 x 1 5.1 7.2 | 5.1 7.9; 1024 x 1 7.6 11.3 | 5.7 8.5;
+  // 128 x 32 11.6 9.6 | 4.5 6.9; 512 x 8 13.6 12.3 | 4.8 7.8. Without rows, requests x pages each: 4 x 100 4.7 | 6.3;
+  // 512 x 2 7.6 | 6.9; 32 x 100 11.1 | 6.7; 512 x 10 18.8 | 8.1; 512 x 1000 1423 | 104.
+  const bool few = slots ? rows <= 1024 : (int64_t)requests * max_pages <= 2048;
+  const int c = requests <= 512 && few ? 1 : kBlocks;
   cudaStream_t st = tfd_host::as_stream(stream);
   return c == 1
              ? tfd_host::launch_clusters<page_plan_kernel<true>>(a, dev, 1, 1, threads_of(true), smem, most, st)

@@ -191,3 +191,19 @@ def test_pages_that_are_none_do_not_come_back(R, page):
     s.round(np.zeros(R, int), np.full(R, 37), 37 * R)     # and a round that is sound
     s.round(np.zeros(R, int), np.zeros(R, int), 0)
     assert s.n_free[0] == 40 * R - 3
+
+
+@pytest.mark.parametrize("R,new,max_pages", [(512, 2, 40), (32, 32, 40), (41, 25, 60), (513, 1, 30), (1, 1024, 300),
+                                             (1, 1025, 300), (512, 1, 4), (409, 1, 5), (410, 1, 5)])
+def test_sizes_around_one_block(R, new, max_pages):
+    """Rounds of about 1024 rows, about 512 requests, and pages given back without rows, about 2048 that can move."""
+    need_gpu()
+    s = State(R, max_pages, R * max_pages, 4, seed=R + new)
+    lens, n = np.arange(R) % 7, np.full(R, new)
+    lens[n + lens > 4 * max_pages] = 0
+    s.round(lens, np.zeros(R, int), 0)
+    for i in range(3):
+        s.round(lens, n, R * new + (i == 1))
+        s.round(lens, np.zeros(R, int), 0)
+    s.round(np.zeros(R, int), np.zeros(R, int), 0)
+    assert s.n_free[0] == R * max_pages
