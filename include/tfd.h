@@ -540,7 +540,7 @@ tfd_status tfd_paged_append(const void* k_rows, int64_t ldk, const void* v_rows,
  *   and its lse NaN. A row whose scores are all -inf gets zeros and -inf.
  *   Sums and softmax statistics in fp32, sines and cosines within 2^-20.5. q' enters its products as two bf16
  *   parts (E4M3: four 8-bit parts), within 2^-16 of it; probabilities as two bf16 parts, within 2^-16. E4M3: a
- *   probability times its value's scale as f16, within 2^-11 of it or 2^-32 of the row's largest (scales below
+ *   probability times its value's scale as f16, within 2^-11 of it or 2^-29 of the row's largest (scales below
  *   2^-96 lose more); a scale above 2^80, or NaN, makes the rows that see its token, and their lse, NaN.
  * Args:
  *   q        device bf16 [rows][q_heads][dim], row stride ldq >= q_heads * dim, a multiple of 8,

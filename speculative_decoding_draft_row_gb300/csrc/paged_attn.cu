@@ -16,7 +16,7 @@
 // cache's operand once: q' and the weights are two bf16 numbers a value (2^-16), side by side as columns, which
 // costs next to nothing here (N of 64 columns takes the time of reading the 128 rows). E4M3 keys and values are
 // multiplied as they are (kind::f8f6f4, against bf16 there is no product): q' over a power of two as four E4M3
-// parts (2^-16), the weights as f16 cut into four E5M2 parts (exact: an E5M2 number is the upper byte of an f16
+// parts (2^-16), the weights as f16 cut into four E5M2 parts (an E5M2 number is the upper byte of an f16
 // one), the last two parts of each times 2^8. An E4M3 value's scale is a summand of the score that its weight
 // comes from, so weights stay in range; the sum, in which it is not, for scales up to 2^80.
 //
@@ -24,7 +24,7 @@
 // issues the scores' products, one the values'; the rest are softmax groups of 128 threads, a token each,
 // 16 rows a group, later a dim each. At 16 rows two groups take tiles in turn (bf16, 128 dims), or two blocks
 // share an SM (E4M3; 64 dims): a tile's chain of waits is longer than its bytes take. A weight may pass its
-// reference by 2^8 before the reference and the sums move, so after a piece's first tile they hardly do.
+// reference by 2^8 (E4M3: 2^7) before the reference and the sums move, so after a piece's first tile they hardly do.
 //
 // What a row does not see gets a score of -inf and a weight of zero; tokens past the last and on bad pages are
 // zero-filled. Zero times an infinity or NaN would be NaN: bf16 values that are not finite, of tokens that not
@@ -74,7 +74,10 @@ struct Roles {
 };
 constexpr int kMostTokens = 0x7fffffff - 1024;  // of a request: a tile behind them is still an int
 constexpr int kMaxBlocks = 304;              // blocks of a launch at most
-constexpr float kHead = 8.0f;                // powers of two that a weight may pass its reference by
+// Powers of two that a weight may pass its reference by. E4M3: its f16 number is at most 2^(7 + 7), so that what two
+// of its parts leave, below 2^8, times 2^8 is an f16 number (from 18688 on it was not: infinite, and the row NaN).
+template <bool kF8>
+constexpr float kHead = kF8 ? 7.0f : 8.0f;
 // The largest value scale (E4M3). Where scales are 2^L the references are higher by L, and the sum, of probabilities
 // alone, begins at 2^-L: what fp32 drops of it, below 2^-126, is then less than 2^-46 of the largest.
 constexpr float kMostScale = 1.2089258196146292e24f;  // 2^80
@@ -1028,8 +1031,8 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
             for (int n = 0; n < kCols; ++n) s[n] = rest[n];
           }
         }
-        // E4M3: the value's scale is part of its weight, as the score's summand: the weights stay below 2^15. A sum
-        // without them is below 2^(96 + 8) a token; what a scale is below 2^-96 its weight is multiplied by
+        // E4M3: the value's scale is part of its weight, as the score's summand: the weights are at most 2^14. A sum
+        // without them is at most 2^(96 + 7) a token; what a scale is below 2^-96 its weight is multiplied by
         float lv = 0.0f, lv_fin = 0.0f, small = 1.0f;
         if (kF8) {
           lv = fabsf(vs) <= kMostScale ? log2f(fabsf(vs)) : NAN;  // beyond: NaN for the rows that see it
@@ -1063,7 +1066,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
           const float4 r = *reinterpret_cast<const float4*>(s_ref + n);
           over = fmaxf(over, fmaxf(fmaxf(s[n] - r.x, s[n + 1] - r.y), fmaxf(s[n + 2] - r.z, s[n + 3] - r.w)));
         }
-        if (i == i0 || warps_any<kGroup>(bid, over > kHead)) {  // every row's reference is its largest score so far
+        if (i == i0 || warps_any<kGroup>(bid, over > kHead<kF8>)) {  // every row's reference is its largest score so far
           float most = 0.0f;
 #pragma unroll
           for (int n = 0; n < kCols; ++n) {
@@ -1118,7 +1121,7 @@ paged_attn_kernel(const __grid_constant__ Args<D> a) {
         wait_free();
         if (kF8) {
           // f16 weights (2^-11) by bits: an E5M2 number is the upper half of an f16 one, and 3 of its 11
-          // bits; what is left is exact, and four parts hold it all
+          // bits; what is left is exact, and four parts hold it all (of a number below 2^-12 all but 3 2^-24)
           uint32_t w[kCols / 2];
 #pragma unroll
           for (int n = 0; n < kCols; n += 2) w[n / 2] = f16x2(s[n], s[n + 1]);
