@@ -4,7 +4,8 @@
 // A sweep bound by its bytes, and for few rows by latency: a warp takes some heads of a row, 16 bytes a
 // lane, loads its next vectors (and their slot) before it uses these, and forms a position's sines and
 // cosines once, a pair or two a lane, shared through shared memory. 8193 rows of 8 heads of 128 in bf16 14.8 us,
-// 0.67 of the copy rate (one item a warp, loads after the slot is known: 18.6); one draft step 2.7 us.
+// 0.67 of the copy rate (one item a warp, loads after the slot is known: 18.6); in E4M3 29.8, 0.25, bound by its sixteen
+// exact divisions a lane for a pair of vectors; one draft step 2.6 us.
 #include "paged.cuh"
 
 namespace {

@@ -30,9 +30,9 @@
 // zero-filled. Zero times an infinity or NaN would be NaN: bf16 values that are not finite, of tokens that not
 // all rows see, leave the product and are added at the end to the rows that see them.
 //
-// Measured: 96 requests of 1000 to 16000 tokens, 4 rows, 32/8 heads of 128 in bf16 498 us, 0.98 of the copy
-// rate (3.3 GB); one row over 131041 tokens 93 (0.85); 24 verify windows of up to 6 rows 69 (0.73); 64 E4M3
-// requests of 300 to 9000 tokens 127 (0.73); one draft step of four streams 17. Short pieces are bound by
+// Measured: 96 requests of 1000 to 16000 tokens, 4 rows, 32/8 heads of 128 in bf16 493 us, 0.99 of the copy
+// rate (3.3 GB); one row over 131041 tokens 95 (0.83); 24 verify windows of up to 6 rows 69 (0.72); 64 E4M3
+// requests of 300 to 9000 tokens 130 (0.72); one draft step of four streams 17. Short pieces are bound by
 // what beginning and ending one takes (about 8 us of chained waits, much of it instructions fetched for the
 // first time), which the line's cuts allow for; kernels on warp-level products, two blocks an SM, measured
 // 569, 112, 142, 208 and 22. Fetching by tensor maps (one warp, boxes of a page) measured no faster.
@@ -49,12 +49,12 @@ constexpr int kCols = 16;                    // rows of a unit that one softmax 
 constexpr int kGroup = 128;                  // its threads, one a token; then one a dim
 constexpr int kAhead = 3;                    // pieces found ahead
 // A unit's end keeps its last kKeep tiles, and a unit of fewer than kLeast is not cut: a piece that small costs more,
-// being joined, than it takes off its neighbour (four streams of 5 tiles a head 17.5 us, cut 24; verify windows 67.8,
-// with ends of 3 tiles 70.8, units of fewer than 12 whole 70.6).
+// being joined, than it takes off its neighbour (four streams of 5 tiles a head 16.9 us, cut 23.8; verify windows 69.1,
+// with ends of 3 tiles 71.6, units of fewer than 12 whole 71.7).
 constexpr int kKeep = 1, kLeast = 6;
 // Places on the line that beginning a unit takes, in tiles of its type: its query, its first and last tiles and its
-// sums cost a block about that. The blocks' times even out by it (96 requests: 557 us at 0, 531 at 1, 508 at 3,
-// 479 at 5, 490 at 12; the E4M3 batch 173, 165, 147, 134 and at 8 124).
+// sums cost a block about that. The blocks' times even out by it (in turn on one GPU, at 0, 1, 3, 5, 8 and 12: 96
+// requests 532 522 497 479 481 489 us; verify windows 106 86 71 69 74 79; the E4M3 batch 165 156 140 128 125 128).
 template <bool kF8>
 constexpr int kStartOf = kF8 ? 8 : 5;
 constexpr float kUnset = -3.0e38f;           // a reference that no score has set
